@@ -14,6 +14,8 @@ __device__ uint32_t g_status_word[2];
 constexpr int kMaxDevices = 64;
 std::atomic<uint32_t *> g_status_ptr[kMaxDevices];
 
+}  // namespace
+
 DeviceStatus device_status() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return {nullptr};
@@ -26,6 +28,8 @@ DeviceStatus device_status() {
     }
     return {p};
 }
+
+namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool ok_ptr(const void *p) { return p != nullptr && aligned16(p); }

@@ -226,6 +226,78 @@ struct CheckArgs {
     DeviceStatus status;
 };
 
+// The paged key/value cache of the softmax-attention layers (kda.h): one layer's pool, the
+// table of pages per row, and the requests of a step.
+struct CacheArgs {
+    int32_t batch, total_tokens, num_pages, page_size, table_rows, table_width;
+    const int32_t *page_table, *slot, *cu_tokens, *kv_len;  // [R][M], [B], [B+1], [R]
+};
+
+// Queries and keys normed per head and rotated; k and v into the cache when kv_pool is set.
+struct NormRopeArgs {
+    kda_dtype in_dtype, out_dtype;
+    int32_t num_q_heads, num_kv_heads;
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements from token to token
+    const float *q_weight, *k_weight;      // [128] or null
+    float eps;
+    int32_t norm, interleaved, rotary_dim, num_positions;
+    const float *rope_table;   // [num_positions][rotary_dim / 2][2]
+    const int32_t *positions;  // [T]
+    void *q_out, *k_out;       // [T][Hq][128], [T][Hkv][128] (without a cache)
+    void *kv_pool;             // [P][2][Hkv][page_size][128] or null
+    CacheArgs cache;           // total_tokens always; the rest with kv_pool
+    DeviceStatus status;
+};
+
+struct WindowAttentionArgs {
+    kda_dtype dtype;
+    int32_t max_tokens, num_q_heads, num_kv_heads, window, sinks;
+    const void *q, *kv_pool;  // [T][Hq][128], [P][2][Hkv][page_size][128]
+    float scale;
+    void *o;  // [T][Hq][128]
+    CacheArgs cache;
+    DeviceStatus status;
+};
+
+// Moves of pages: pages dst[i] := pages src[i] of each layer, i < *count (or n when null).
+struct PageMoves {
+    int32_t num_layers, num_pages, n;
+    int64_t page_bytes;
+    const int32_t *src, *dst, *count;
+    void *pool;
+};
+struct PageForkArgs {
+    PageMoves moves;
+    int32_t page_size, table_rows, table_width;
+    const int32_t *parent, *child;
+    int32_t *page_table, *kv_len;
+    int32_t *free_list, *src, *dst;  // [F] each, in the workspace
+    DeviceStatus status;
+};
+struct PageReleaseArgs {
+    int32_t table_rows, table_width, page_size, n, window, sinks;
+    const int32_t *rows;
+    int32_t *page_table, *kv_len;
+    DeviceStatus status;
+};
+struct PageCompactArgs {
+    PageMoves moves;
+    int32_t table_rows, table_width;
+    const int32_t *table_in;
+    int32_t *table_out, *num_live;
+    int32_t *src, *dst, *remap, *count;  // [P] each and [1], in the workspace
+};
+
+// The current device's status word (null when it cannot be found).
+DeviceStatus device_status();
+
+cudaError_t launch_qk_norm_rope(const NormRopeArgs &a, cudaStream_t stream);
+cudaError_t launch_window_attention(const WindowAttentionArgs &a, cudaStream_t stream);
+cudaError_t launch_pages_copy(const PageMoves &a, cudaStream_t stream);
+cudaError_t launch_pages_fork(const PageForkArgs &a, cudaStream_t stream);
+cudaError_t launch_pages_release(const PageReleaseArgs &a, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PageCompactArgs &a, cudaStream_t stream);
 cudaError_t launch_check_prefill(const CheckArgs &a, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream);
 cudaError_t launch_decode_layer(const DecodeLayerArgs &a, cudaStream_t stream);

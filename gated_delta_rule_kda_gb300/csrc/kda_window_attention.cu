@@ -1,0 +1,199 @@
+// Sliding-window attention over the paged cache, in fp32 on the FMA units.
+//
+// A work item is 64 rows of one request and key/value head; a row is a (token, query head of the
+// group) pair, so that the group's heads share each key and value.  Over tiles of 64 keys:
+//   s = scale q k^T;  m' = max(m, max s);  l <- l e^(m - m') + sum e^(s - m');
+//   o <- o e^(m - m') + e^(s - m') v;  at the end o / l   (l = 0: no key was visible, o = 0)
+// Tiles of q, k, v and of the probabilities lie in shared memory as fp32; a thread computes 4 x 4
+// scores and 4 x 8 outputs, so that each shared-memory read feeds two to four FMAs.  A key that a
+// row does not see takes no part: its score is replaced (never computed with), its probability of
+// zero skips the product with v, and keys past the end or without a page are loaded as zeros.
+#include "kda_window_attention.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = 64;              // rows of an item, keys of a tile
+constexpr int kPitch = kD + 4;         // q, k rows: float4 reads of 16 rows hit distinct banks
+constexpr int kPitchP = kTile + 4;
+constexpr size_t kSmem = sizeof(float) * (2 * kTile * kPitch + kTile * kD + kTile * kPitchP);
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) attention_rows_kernel(const WindowAttentionArgs a) {
+    extern __shared__ float4 smem4[];
+    float *sq = reinterpret_cast<float *>(smem4), *sk = sq + kTile * kPitch;
+    float *sv = sk + kTile * kPitch, *sp = sv + kTile * kD;
+    __shared__ uint64_t s_mapped;  // bit j: key j of the tile has a page
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int32_t G = a.num_q_heads / a.num_kv_heads, h = blockIdx.y;
+    const CacheArgs &cache = a.cache;
+
+    AttnRequest req;
+    int32_t index;
+    AttnWalk walk;
+    if (!walk.find(a, blockIdx.x, G, kTile, req, index)) return;  // the same for every warp
+    const int32_t rows = req.n * G, r0 = index * kTile;
+    const int32_t p0 = req.len - req.n;  // index of the request's first token
+    const T *q = static_cast<const T *>(a.q), *pool = static_cast<const T *>(a.kv_pool);
+
+    for (int i = tid; i < kTile * (kD / 4); i += kThreads) {
+        const int r = i / (kD / 4), c = i % (kD / 4) * 4, row = r0 + r;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row < rows)
+            x = load4(q + ((int64_t)(req.first + row / G) * a.num_q_heads + h * G + row % G) * kD + c);
+        *reinterpret_cast<float4 *>(sq + r * kPitch + c) = x;
+    }
+
+    int32_t p[4];  // indices of this thread's rows 4 ty + i (past the last row: -1 sees nothing)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int32_t row = r0 + 4 * ty + i;
+        p[i] = row < rows ? p0 + row / G : -1;
+    }
+    float o[4][8], m[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) o[i][c] = 0.f;
+    }
+
+    const AttnKeys keys(p0 + r0 / G, p0 + (min(r0 + kTile, rows) - 1) / G, a.window, a.sinks, kTile);
+    const int32_t end = p0 + (min(r0 + kTile, rows) - 1) / G + 1;  // no row sees a key from here on
+    for (int32_t it = 0; it < keys.count(); ++it) {
+        const int32_t j0 = keys.tile(it) * kTile;
+        __syncthreads();  // the previous tile has been used
+        if (tid == 0) s_mapped = 0;
+        __syncthreads();
+        for (int i = tid; i < kTile * (kD / 4); i += kThreads) {
+            const int r = i / (kD / 4), c = i % (kD / 4) * 4, j = j0 + r;
+            float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
+            if (j < end) {  // end <= len <= table_width * page_size
+                const int32_t page = cache.page_table[(int64_t)req.row * cache.table_width + j / cache.page_size];
+                if ((uint32_t)page < (uint32_t)cache.num_pages) {
+                    const int64_t kv_stride = (int64_t)a.num_kv_heads * cache.page_size * kD;
+                    const T *src = pool + (int64_t)page * 2 * kv_stride +
+                                   ((int64_t)h * cache.page_size + j % cache.page_size) * kD + c;
+                    kx = load4(src);
+                    vx = load4(src + kv_stride);
+                    if (c == 0) atomicOr(reinterpret_cast<unsigned long long *>(&s_mapped), 1ull << r);
+                }
+            }
+            *reinterpret_cast<float4 *>(sk + r * kPitch + c) = kx;
+            *reinterpret_cast<float4 *>(sv + r * kD + c) = vx;
+        }
+        __syncthreads();
+        const uint64_t mapped = s_mapped;
+
+        float s[4][4];  // rows 4 ty + i, keys tx + 16 j
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < kD; c += 4) {
+            float4 x[4], y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(sq + (4 * ty + i) * kPitch + c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(sk + (tx + 16 * j) * kPitch + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i][j] = fmaf(x[i].x, y[j].x, s[i][j]);
+                    s[i][j] = fmaf(x[i].y, y[j].y, s[i][j]);
+                    s[i][j] = fmaf(x[i].z, y[j].z, s[i][j]);
+                    s[i][j] = fmaf(x[i].w, y[j].w, s[i][j]);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float top = m[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = tx + 16 * j;
+                const bool seen = attn_visible(p[i], j0 + k, a.window, a.sinks) && (mapped >> k & 1);
+                s[i][j] = seen ? s[i][j] * a.scale : -INFINITY;
+                top = fmaxf(top, s[i][j]);
+            }
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const float base = top == -INFINITY ? 0.f : top;  // nothing visible yet: e^-inf = 0
+            const float keep = expf(m[i] - base);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float e = expf(s[i][j] - base);
+                sp[(4 * ty + i) * kPitchP + tx + 16 * j] = e;
+                sum += e;
+            }
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            m[i] = top;
+            l[i] = fmaf(l[i], keep, sum);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) o[i][c] *= keep;
+        }
+        __syncwarp();  // a row's probabilities are written and read by the same half-warp
+#pragma unroll 2
+        for (int k = 0; k < kTile; k += 4) {
+            float4 e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = *reinterpret_cast<const float4 *>(sp + (4 * ty + i) * kPitchP + k);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                const float4 v0 = *reinterpret_cast<const float4 *>(sv + (k + kk) * kD + 4 * tx);
+                const float4 v1 = *reinterpret_cast<const float4 *>(sv + (k + kk) * kD + 64 + 4 * tx);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float w = kk == 0 ? e[i].x : kk == 1 ? e[i].y : kk == 2 ? e[i].z : e[i].w;
+                    if (w != 0.f) {  // NaN counts as well
+                        o[i][0] = fmaf(w, v0.x, o[i][0]); o[i][1] = fmaf(w, v0.y, o[i][1]);
+                        o[i][2] = fmaf(w, v0.z, o[i][2]); o[i][3] = fmaf(w, v0.w, o[i][3]);
+                        o[i][4] = fmaf(w, v1.x, o[i][4]); o[i][5] = fmaf(w, v1.y, o[i][5]);
+                        o[i][6] = fmaf(w, v1.z, o[i][6]); o[i][7] = fmaf(w, v1.w, o[i][7]);
+                    }
+                }
+            }
+        }
+    }
+
+    T *out = static_cast<T *>(a.o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int32_t row = r0 + 4 * ty + i;
+        if (row >= rows) continue;
+        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+        T *dst = out + ((int64_t)(req.first + row / G) * a.num_q_heads + h * G + row % G) * kD;
+        store4(dst + 4 * tx, make_float4(o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv));
+        store4(dst + 64 + 4 * tx, make_float4(o[i][4] * inv, o[i][5] * inv, o[i][6] * inv, o[i][7] * inv));
+    }
+}
+
+template <typename T>
+cudaError_t launch_rows(const WindowAttentionArgs &a, cudaStream_t stream) {
+    cudaError_t e = cudaFuncSetAttribute(attention_rows_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)kSmem);
+    if (e != cudaSuccess) return e;
+    // each request rounds up to whole items at most once
+    const int64_t rows = (int64_t)a.cache.total_tokens * (a.num_q_heads / a.num_kv_heads);
+    const int64_t items = (rows + kTile - 1) / kTile + a.cache.batch;
+    if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    attention_rows_kernel<T><<<dim3((unsigned)items, (unsigned)a.num_kv_heads), kThreads, kSmem, stream>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_window_attention_rows(const WindowAttentionArgs &a, cudaStream_t stream) {
+    return a.dtype == KDA_BF16 ? launch_rows<__nv_bfloat16>(a, stream) : launch_rows<float>(a, stream);
+}
+
+cudaError_t launch_window_attention(const WindowAttentionArgs &a, cudaStream_t stream) {
+    return launch_window_attention_rows(a, stream);
+}
+
+}  // namespace kda

@@ -1,0 +1,98 @@
+// What the kernels of kda_window_attention share: the requests of a step, and which keys the
+// tokens of a work item can see.
+#pragma once
+
+#include "kda_common.cuh"
+
+namespace kda {
+
+// One request of the step, checked: its tokens [first, first + n) of q and o, its row of the
+// table, and the tokens in that row (n of them the step's own).
+struct AttnRequest {
+    int32_t b, first, n, row, len;
+};
+
+// Request b, with n = 0 when its slot, kv_len or token range is out of range (then *bad is set).
+__device__ __forceinline__ AttnRequest attn_request(const WindowAttentionArgs &a, int32_t b, bool *bad) {
+    const CacheArgs &c = a.cache;
+    AttnRequest r{b, c.cu_tokens[b], 0, c.slot[b], 0};
+    const int32_t end = c.cu_tokens[b + 1];
+    bool ok = r.first >= 0 && end >= r.first && end <= c.total_tokens && end - r.first <= a.max_tokens &&
+              (uint32_t)r.row < (uint32_t)c.table_rows;
+    if (ok) {
+        r.len = c.kv_len[r.row];
+        ok = r.len >= 0 && r.len <= c.table_width * c.page_size;
+    }
+    if (ok) r.n = end - r.first;
+    *bad = !ok;
+    return r;
+}
+
+// Walks the work items of a step in order: request b has ceil(n_b per / tile) of them, where n_b
+// tokens make n_b * per rows of `tile`.  A whole warp calls find() with non-decreasing items.
+struct AttnWalk {
+    int32_t base = 0;      // requests [base, base + 32) were looked at last
+    int64_t before = 0;    // items of the requests before base
+
+    // The request that holds `item` and the item's number in it; false past the last item.
+    __device__ __forceinline__ bool find(const WindowAttentionArgs &a, int64_t item, int32_t per,
+                                         int32_t tile, AttnRequest &req, int32_t &index) {
+        const int lane = threadIdx.x & 31;
+        for (; base < a.cache.batch; base += 32) {
+            AttnRequest mine{0, 0, 0, 0, 0};
+            if (base + lane < a.cache.batch) {
+                bool bad;
+                mine = attn_request(a, base + lane, &bad);
+                if (bad) record_status(a.status, KDA_ERR_DEVICE_CHECK, (uint32_t)(base + lane));
+            }
+            const int64_t items = ((int64_t)mine.n * per + tile - 1) / tile;
+            int64_t sum = items;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, sum, off);
+                if (lane >= off) sum += y;
+            }
+            const uint32_t holds = __ballot_sync(0xffffffffu, item < before + sum);
+            if (holds != 0) {
+                const int src = __ffs(holds) - 1;
+                req.b = __shfl_sync(0xffffffffu, mine.b, src);
+                req.first = __shfl_sync(0xffffffffu, mine.first, src);
+                req.n = __shfl_sync(0xffffffffu, mine.n, src);
+                req.row = __shfl_sync(0xffffffffu, mine.row, src);
+                req.len = __shfl_sync(0xffffffffu, mine.len, src);
+                index = (int32_t)(item - before - __shfl_sync(0xffffffffu, sum - items, src));
+                return true;
+            }
+            before += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        return false;
+    }
+};
+
+// Keys that the tokens p in [p_min, p_max] of a row of `len` tokens see: [0, sink_end) and
+// [low, end), in tiles of `tile` keys: tiles [0, sink_tiles) and [low_tile, end_tile).
+struct AttnKeys {
+    int32_t sink_tiles, low_tile, end_tile;
+    __device__ __forceinline__ AttnKeys(int32_t p_min, int32_t p_max, int32_t window, int32_t sinks,
+                                        int32_t tile) {
+        const int32_t end = max(p_max + 1, 0);
+        const int32_t low = p_min < window ? 0 : p_min - window + 1;
+        end_tile = (end + tile - 1) / tile;
+        sink_tiles = (min(sinks, end) + tile - 1) / tile;
+        low_tile = min(max(low / tile, sink_tiles), max(end_tile, sink_tiles));
+        end_tile = max(end_tile, low_tile);
+    }
+    __device__ __forceinline__ int32_t count() const { return sink_tiles + end_tile - low_tile; }
+    __device__ __forceinline__ int32_t tile(int32_t i) const {
+        return i < sink_tiles ? i : low_tile + i - sink_tiles;
+    }
+};
+
+// Whether the token with index p sees key j (of a mapped page).
+__device__ __forceinline__ bool attn_visible(int32_t p, int32_t j, int32_t window, int32_t sinks) {
+    return j <= p && (p - j < window || j < sinks);
+}
+
+cudaError_t launch_window_attention_rows(const WindowAttentionArgs &a, cudaStream_t stream);
+
+}  // namespace kda

@@ -57,6 +57,14 @@ EXPORTED = (
     "kda_decode_layer",
     "kda_decode_tokens",
     "kda_decode_layer_tokens",
+    "kda_qk_norm_rope",
+    "kda_qk_norm_rope_append",
+    "kda_window_attention",
+    "kda_pages_copy",
+    "kda_pages_workspace_size",
+    "kda_pages_fork",
+    "kda_pages_release",
+    "kda_pages_compact",
     "kda_check_prefill_inputs",
     "kda_get_device_status",
     "kda_debug_inject_handoff_timeout",
@@ -135,6 +143,25 @@ def _load() -> ctypes.CDLL:
     lib.kda_decode_layer_tokens.argtypes = [I32, I32, I32, I32, P, P, P, P, P, P, P, P, P, P, P,
                                             P, P, I32, F, F, F, ctypes.c_int, P, P]
     lib.kda_decode_layer_tokens.restype = ctypes.c_int
+    lib.kda_qk_norm_rope.argtypes = [ctypes.c_int, ctypes.c_int, I32, I32, I32, P, I64, P, I64, P, P,
+                                     F, I32, P, I32, I32, I32, P, P, P, P]
+    lib.kda_qk_norm_rope.restype = ctypes.c_int
+    lib.kda_qk_norm_rope_append.argtypes = [ctypes.c_int, ctypes.c_int, I32, I32, I32, I32, P, I64,
+                                            P, I64, P, I64, P, P, F, I32, P, I32, I32, I32, P, I32,
+                                            I32, I32, I32, P, P, P, P, P, P, P]
+    lib.kda_qk_norm_rope_append.restype = ctypes.c_int
+    lib.kda_window_attention.argtypes = [ctypes.c_int] + [I32] * 11 + [P] * 6 + [F, P, P]
+    lib.kda_window_attention.restype = ctypes.c_int
+    lib.kda_pages_copy.argtypes = [I32, I32, I64, I32, P, P, P, P]
+    lib.kda_pages_copy.restype = ctypes.c_int
+    lib.kda_pages_workspace_size.argtypes = [I32, I32]
+    lib.kda_pages_workspace_size.restype = SZ
+    lib.kda_pages_fork.argtypes = [I32, I32, I64, I32, I32, I32, I32, P, P, P, P, P, P, SZ, P]
+    lib.kda_pages_fork.restype = ctypes.c_int
+    lib.kda_pages_release.argtypes = [I32, I32, I32, I32, P, I32, I32, P, P, P]
+    lib.kda_pages_release.restype = ctypes.c_int
+    lib.kda_pages_compact.argtypes = [I32, I32, I64, I32, I32, P, P, P, P, P, SZ, P]
+    lib.kda_pages_compact.restype = ctypes.c_int
     lib.kda_check_prefill_inputs.argtypes = [I32, I32, I32, P, I32, P, P]
     lib.kda_check_prefill_inputs.restype = ctypes.c_int
     lib.kda_get_device_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
@@ -507,6 +534,201 @@ def kda_decode_layer_tokens(qp, kp, vp, conv_w, z, A, b, beta_logit, g, cu_token
                                       _dtype_code(o.dtype), _p(o), _stream(stream))
     _check("kda_decode_layer_tokens", rc)
     return o
+
+
+def rope_table(num_positions: int, rotary_dim: int = HEAD_DIM, base: float = 10000.0, *,
+               inv_freq=None, magnitude: float = 1.0, device="cuda") -> torch.Tensor:
+    """(cos, sin) of every position and rotated pair, [num_positions, rotary_dim/2, 2] fp32, kept
+    by the caller like a weight.  inv_freq [rotary_dim/2] (default base^(-2i/rotary_dim)) and
+    magnitude carry a long-context scaling; the angles are formed in 64 bits."""
+    if inv_freq is None:
+        inv_freq = base ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device) / rotary_dim)
+    inv_freq = torch.as_tensor(inv_freq, dtype=torch.float64, device=device)
+    angle = torch.arange(num_positions, dtype=torch.float64, device=device)[:, None] * inv_freq
+    return torch.stack([angle.cos(), angle.sin()], -1).mul_(magnitude).float().contiguous()
+
+
+def _i32(t: Optional[torch.Tensor]):
+    if t is not None and t.dtype != torch.int32:
+        raise TypeError(f"expected int32, got {t.dtype}")
+    return _p(t)
+
+
+def _f32(t: Optional[torch.Tensor]):
+    if t is not None and t.dtype != torch.float32:
+        raise TypeError(f"expected float32, got {t.dtype}")
+    return _p(t)
+
+
+def _heads(t: torch.Tensor, dtype: torch.dtype):
+    """(pointer, elements from token to token) of [T, heads, 128] whose heads lie side by side."""
+    T, H, d = t.shape
+    if t.dtype != dtype:
+        raise TypeError(f"expected {dtype}, got {t.dtype}")
+    s = t.stride()
+    if d != HEAD_DIM or s[2] != 1 or (H > 1 and s[1] != HEAD_DIM):
+        raise ValueError("the heads of a token must lie side by side, 128 channels each")
+    return ctypes.c_void_p(t.data_ptr()), (s[0] if T > 1 else H * HEAD_DIM)
+
+
+def _pool_shape(kv_pool):
+    """(pages, kv heads, page_size) of a cache pool [P, 2, Hkv, page_size, 128]."""
+    if kv_pool.dim() != 5 or kv_pool.shape[1] != 2 or kv_pool.shape[4] != HEAD_DIM:
+        raise ValueError("kv_pool must be [pages, 2, kv heads, page_size, 128]")
+    return kv_pool.shape[0], kv_pool.shape[2], kv_pool.shape[3]
+
+
+def _rope_args(rope, positions, T):
+    if rope is None:
+        return None, 0, 0, None
+    if positions.numel() != T:
+        raise ValueError("positions must have one entry per token")
+    return _f32(rope), rope.shape[0], 2 * rope.shape[1], _i32(positions)
+
+
+def kda_qk_norm_rope(q, k, rope, positions, q_weight=None, k_weight=None, eps=1e-6, *, norm=True,
+                     interleaved=False, out_dtype=None, q_out=None, k_out=None, stream=None):
+    """q [T, Hq, 128] and k [T, Hkv, 128] (heads dense, any token stride) normed per head and
+    rotated by rope_table(...) at positions [T] int32 (rope None: no rotation).
+    Returns (q_out, k_out)."""
+    T, Hq, _ = q.shape
+    Hkv = k.shape[1]
+    out_dtype = q_out.dtype if q_out is not None else out_dtype or q.dtype
+    if q_out is None:
+        q_out = torch.empty((T, Hq, HEAD_DIM), dtype=out_dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty((T, Hkv, HEAD_DIM), dtype=out_dtype, device=q.device)
+    if k.shape[0] != T or q_out.shape != q.shape or k_out.shape != k.shape or k_out.dtype != out_dtype:
+        raise ValueError("q, k and their outputs must agree in tokens, heads and type")
+    (qp, qs), (kp, ks) = _heads(q, q.dtype), _heads(k, q.dtype)
+    table, P, R, pos = _rope_args(rope, positions, T)
+    rc = _lib.kda_qk_norm_rope(_dt(q), _dt(q_out), T, Hq, Hkv, qp, qs, kp, ks, _f32(q_weight),
+                               _f32(k_weight), float(eps), int(norm), table, P, R, int(interleaved),
+                               pos, _p(q_out), _p(k_out), _stream(stream))
+    _check("kda_qk_norm_rope", rc)
+    return q_out, k_out
+
+
+def kda_qk_norm_rope_append(q, k, v, rope, positions, kv_pool, page_table, slot, cu_tokens, kv_len,
+                            q_weight=None, k_weight=None, eps=1e-6, *, norm=True, interleaved=False,
+                            q_out=None, stream=None):
+    """kda_qk_norm_rope with k (normed and rotated) and v written to the cache pages of the tokens:
+    kv_pool [P, 2, Hkv, page_size, 128], page_table [R, M], kv_len [R] (these tokens counted),
+    slot [B], cu_tokens [B+1].  Outputs have the pool's type.  Returns q_out."""
+    T, Hq, _ = q.shape
+    Hkv = k.shape[1]
+    P, pool_heads, page = _pool_shape(kv_pool)
+    if q_out is None:
+        q_out = torch.empty((T, Hq, HEAD_DIM), dtype=kv_pool.dtype, device=q.device)
+    if k.shape[0] != T or v.shape != k.shape or pool_heads != Hkv or q_out.shape != q.shape \
+            or q_out.dtype != kv_pool.dtype:
+        raise ValueError("q, k, v, q_out and kv_pool must agree in tokens, heads and type")
+    if cu_tokens.numel() != slot.numel() + 1 or page_table.shape[0] != kv_len.numel():
+        raise ValueError("cu_tokens must have one entry more than slot, kv_len one per table row")
+    (qp, qs), (kp, ks), (vp, vs) = _heads(q, q.dtype), _heads(k, q.dtype), _heads(v, q.dtype)
+    table, npos, R, pos = _rope_args(rope, positions, T)
+    rc = _lib.kda_qk_norm_rope_append(
+        _dt(q), _dt(q_out), slot.numel(), T, Hq, Hkv, qp, qs, kp, ks, vp, vs, _f32(q_weight),
+        _f32(k_weight), float(eps), int(norm), table, npos, R, int(interleaved), pos, P, page,
+        page_table.shape[0], page_table.shape[1], _i32(page_table), _i32(slot), _i32(cu_tokens),
+        _i32(kv_len), _p(kv_pool), _p(q_out), _stream(stream))
+    _check("kda_qk_norm_rope_append", rc)
+    return q_out
+
+
+def kda_window_attention(q, kv_pool, page_table, slot, cu_tokens, kv_len, window, sinks=0,
+                         scale=DEFAULT_SCALE, *, max_tokens=None, o=None, stream=None):
+    """Attention of q [T, Hq, 128] over the requests' rows of the cache, with a sliding window and
+    the first `sinks` tokens always visible (window None: plain causal).  max_tokens: no request
+    brings more (default: T); small values let the call split long rows.  Returns o."""
+    T, Hq, _ = q.shape
+    P, Hkv, page = _pool_shape(kv_pool)
+    if kv_pool.dtype != q.dtype:
+        raise TypeError("q and kv_pool must have one type")
+    if cu_tokens.numel() != slot.numel() + 1 or page_table.shape[0] != kv_len.numel():
+        raise ValueError("cu_tokens must have one entry more than slot, kv_len one per table row")
+    if o is None:
+        o = torch.empty_like(q)
+    elif o.shape != q.shape or o.dtype != q.dtype:
+        raise ValueError("o must have q's shape and type")
+    rc = _lib.kda_window_attention(
+        _dt(q), slot.numel(), T, max(T, 1) if max_tokens is None else int(max_tokens), Hq, Hkv, P,
+        page, page_table.shape[0], page_table.shape[1],
+        0x7fffffff if window is None else int(window), int(sinks), _p(q), _p(kv_pool),
+        _i32(page_table), _i32(slot), _i32(cu_tokens), _i32(kv_len), float(scale), _p(o),
+        _stream(stream))
+    _check("kda_window_attention", rc)
+    return o
+
+
+def _layers(pool):
+    """(layers, pages, bytes of a page) of [layers, pages, ...]."""
+    if pool.dim() < 3:
+        raise ValueError("pool must be [layers, pages, ...]")
+    L, P = pool.shape[0], pool.shape[1]
+    return L, P, pool.numel() // max(1, L * P) * pool.element_size()
+
+
+def kda_pages_copy(pool, src, dst, *, stream=None):
+    """Pages dst[i] := pages src[i] in every layer of pool [layers, pages, ...] (rows of a
+    recurrent-state pool as well); src, dst int32 on the device."""
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst must have one length")
+    L, P, nbytes = _layers(pool)
+    _check("kda_pages_copy", _lib.kda_pages_copy(L, P, nbytes, src.numel(), _i32(src), _i32(dst),
+                                                 _p(pool), _stream(stream)))
+
+
+def kda_pages_workspace_size(num_pages: int, table_rows: int) -> int:
+    return int(_lib.kda_pages_workspace_size(num_pages, table_rows))
+
+
+def _pages_workspace(workspace, P, rows, device):
+    if workspace is None:
+        workspace = torch.empty(kda_pages_workspace_size(P, rows), dtype=torch.uint8, device=device)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def kda_pages_fork(pool, page_table, kv_len, parent, child, page_size, *, workspace=None, stream=None):
+    """Rows child[i] become branches of rows parent[i], in place in page_table and kv_len: whole
+    pages shared, a part-filled last page copied to a fresh one in every layer of pool."""
+    if parent.numel() != child.numel() or page_table.shape[0] != kv_len.numel():
+        raise ValueError("parent and child must have one length, kv_len one entry per table row")
+    L, P, nbytes = _layers(pool)
+    R, M = page_table.shape
+    workspace, wbytes = _pages_workspace(workspace, P, R, pool.device)
+    _check("kda_pages_fork", _lib.kda_pages_fork(
+        L, P, nbytes, int(page_size), R, M, parent.numel(), _i32(parent), _i32(child),
+        _i32(page_table), _i32(kv_len), _p(pool), _p(workspace), wbytes, _stream(stream)))
+
+
+def kda_pages_release(page_table, kv_len, rows, page_size, window=0, sinks=0, *, stream=None):
+    """Empties the rows (window 0), or drops only the pages that no coming token sees with this
+    window and these sinks; in place in page_table (and kv_len)."""
+    if page_table.shape[0] != kv_len.numel():
+        raise ValueError("kv_len must have one entry per table row")
+    R, M = page_table.shape
+    _check("kda_pages_release", _lib.kda_pages_release(
+        R, M, int(page_size), rows.numel(), _i32(rows), int(window), int(sinks), _i32(page_table),
+        _i32(kv_len), _stream(stream)))
+
+
+def kda_pages_compact(pool, page_table, *, table_out=None, num_live=None, workspace=None, stream=None):
+    """Brings the pages that rows name together at the front of pool [layers, pages, ...].  Returns
+    (table_out, num_live): the table with the new names (default: in place) and how many pages are
+    live, [1] int32 on the device."""
+    L, P, nbytes = _layers(pool)
+    R, M = page_table.shape
+    table_out = page_table if table_out is None else table_out
+    if table_out.shape != page_table.shape:
+        raise ValueError("table_out must have page_table's shape")
+    if num_live is None:
+        num_live = torch.empty(1, dtype=torch.int32, device=pool.device)
+    workspace, wbytes = _pages_workspace(workspace, P, R, pool.device)
+    _check("kda_pages_compact", _lib.kda_pages_compact(
+        L, P, nbytes, R, M, _i32(page_table), _i32(table_out), _i32(num_live), _p(pool),
+        _p(workspace), wbytes, _stream(stream)))
+    return table_out, num_live
 
 
 def kda_check_prefill_inputs(cu_seqlens, log_alpha=None, total_tokens=None, num_heads=1,

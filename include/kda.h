@@ -565,6 +565,189 @@ kda_status kda_decode_layer_tokens(int32_t batch, int32_t num_heads, int32_t poo
                                    int32_t write_back, float scale, float l2_eps, float rms_eps,
                                    kda_dtype out_dtype, void *o, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Softmax attention beside the KDA layers: a paged key/value cache
+ *
+ * A stack that interleaves KDA layers with softmax-attention layers keeps two
+ * kinds of state per request: fixed recurrent blocks and a cache that grows
+ * with the sequence ("Kimi K3: Architecture and SGLang Day-0 Support", section
+ * "Memory management for two state types").  The calls below write, read and
+ * manage the second kind.  What they share:
+ *
+ *   kv_pool     [P][2][Hkv][page_size][128]: P pages, keys then values, head
+ *               by head; page_size 16, 32, 64 or 128 tokens
+ *   page_table  [R][M] int32: row r's tokens [i page_size, (i+1) page_size) are
+ *               in page page_table[r][i]; an entry outside [0, P) names no page
+ *   kv_len      [R] int32: tokens of row r, those of the current step included,
+ *               in [0, M page_size]
+ *   slot        [B] int32: the row of each request, in [0, R) (as the row of a
+ *               recurrent-state pool; several requests may read one row)
+ *   cu_tokens   [B+1] int32: request b brings tokens [cu[b], cu[b+1]) of the
+ *               step, n_b of them; token i has index p = kv_len[row] - n_b + i
+ * All are caller-owned device memory: kv_pool 16-byte aligned, the int32 arrays
+ * 4-byte.  One layer's pool is one kv_pool; the kda_pages_* calls take the
+ * pools of all layers that share a table.  No call allocates.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * kda_qk_norm_rope - queries and keys normalised per head and rotated by their
+ * position, in one pass.
+ *
+ *   y = x / sqrt(mean(x^2) + eps) * weight      (norm = 1; weight NULL: ones)
+ *   (a, b) -> (a c - b s, b c + a s),  (c, s) = rope_table[position][i]
+ * for the pairs i < rotary_dim / 2 of each head: channels (2i, 2i+1) with
+ * interleaved = 1, (i, i + rotary_dim/2) with interleaved = 0; channels from
+ * rotary_dim on are not rotated.  All in fp32, rounded once on output.
+ * Scaling for long contexts (stretched frequencies, a magnitude factor on cos
+ * and sin) is in the table, which the caller keeps.
+ *
+ *   in_dtype, out_dtype  of q, k (and v) / of the outputs (and kv_pool)
+ *   q           [T][Hq][128] in_dtype, q_stride elements from token to token
+ *               (heads dense): a slice of a fused projection is fine
+ *   k           [T][Hkv][128] in_dtype, k_stride likewise
+ *   q_weight, k_weight   [128] fp32 or NULL
+ *   rope_table  [num_positions][rotary_dim/2][2] fp32 (cos, sin), 16-byte
+ *               aligned; may be NULL when rotary_dim = 0
+ *   rotary_dim  a multiple of 16 in [0, 128]
+ *   positions   [T] int32, each in [0, num_positions) (NULL when rotary_dim = 0)
+ *   q_out       [T][Hq][128] out_dtype;  k_out [T][Hkv][128] out_dtype; each may
+ *               be its input when that is dense and of the same type
+ * Errors: KDA_ERR_INVALID_ARGUMENT (null/misaligned pointers, bad sizes, dtypes
+ * or flags, a stride below the row or not a multiple of 16 bytes),
+ * KDA_ERR_UNSUPPORTED (another rotary_dim, T * (Hq + 2 Hkv) above 2^31 - 1),
+ * KDA_ERR_CUDA.  A token whose position lies outside the table is refused by the
+ * kernel (nothing written for it; KDA_ERR_DEVICE_CHECK with detail = token).
+ */
+kda_status kda_qk_norm_rope(kda_dtype in_dtype, kda_dtype out_dtype, int32_t total_tokens,
+                            int32_t num_q_heads, int32_t num_kv_heads, const void *q,
+                            int64_t q_stride, const void *k, int64_t k_stride,
+                            const float *q_weight, const float *k_weight, float eps, int32_t norm,
+                            const float *rope_table, int32_t num_positions, int32_t rotary_dim,
+                            int32_t interleaved, const int32_t *positions, void *q_out,
+                            void *k_out, void *stream);
+
+/*
+ * kda_qk_norm_rope_append - the same, with k (normed and rotated) and v (as it
+ * is) written to the cache pages of the tokens instead of a dense k.
+ *
+ *   v           [T][Hkv][128] in_dtype, v_stride elements from token to token
+ *   kv_len      counts the tokens written here already
+ *   kv_pool     out_dtype; no two requests of the call may write the same place
+ *   (cache arguments as above, the others as kda_qk_norm_rope)
+ * A token whose request, row, index or page does not exist (cu_tokens, slot,
+ * kv_len or the table entry out of range) has its k and v refused by the kernel
+ * (KDA_ERR_DEVICE_CHECK, detail = token).
+ * KDA_ERR_UNSUPPORTED also for other page sizes, and for M page_size or
+ * 2 P Hkv page_size above 2^31 - 1.
+ */
+kda_status kda_qk_norm_rope_append(kda_dtype in_dtype, kda_dtype out_dtype, int32_t batch,
+                                   int32_t total_tokens, int32_t num_q_heads,
+                                   int32_t num_kv_heads, const void *q, int64_t q_stride,
+                                   const void *k, int64_t k_stride, const void *v,
+                                   int64_t v_stride, const float *q_weight, const float *k_weight,
+                                   float eps, int32_t norm, const float *rope_table,
+                                   int32_t num_positions, int32_t rotary_dim, int32_t interleaved,
+                                   const int32_t *positions, int32_t num_pages, int32_t page_size,
+                                   int32_t table_rows, int32_t table_width,
+                                   const int32_t *page_table, const int32_t *slot,
+                                   const int32_t *cu_tokens, const int32_t *kv_len, void *kv_pool,
+                                   void *q_out, void *stream);
+
+/*
+ * kda_window_attention - attention of the step's tokens over their rows of the
+ * cache, with a sliding window and the first `sinks` tokens always visible:
+ *
+ *   o = sum_j softmax_j(scale q . k_j) v_j  over 0 <= j <= p with
+ *       j > p - window or j < sinks, and the page of j mapped
+ * Query head h reads kv head h / (Hq / Hkv).  A token that sees no key gives 0.
+ * window = INT32_MAX: plain causal attention.  Nothing outside a token's visible
+ * keys reaches it, whatever is stored there (NaN and infinities included).
+ *
+ *   dtype       of q, kv_pool and o.  KDA_BF16: tensor cores; scores, softmax
+ *               statistics and sums in fp32, probabilities rounded to bf16 for
+ *               the second product.  KDA_FP32: fp32 throughout
+ *   max_tokens  >= 1: no request brings more (one that does is refused)
+ *   q, o        [T][Hq][128], 16-byte aligned; NULL when T = 0
+ * The same call gives the same bits again (the split of a long row over CTAs, and with it
+ * the order of its sums, goes by the sizes of the call).
+ * Errors: KDA_ERR_INVALID_ARGUMENT (null/misaligned pointers, sizes below 1,
+ * T < 0, sinks < 0, Hq not a multiple of Hkv, dtype), KDA_ERR_UNSUPPORTED
+ * (page_size, Hq / Hkv above 128, Hkv above 65535, T * Hq, M page_size or
+ * 2 P Hkv page_size above 2^31 - 1), KDA_ERR_CUDA.  A request whose slot, kv_len
+ * or token range is out of range is refused by the kernel (its rows of o stay
+ * as they are; KDA_ERR_DEVICE_CHECK with detail = b).
+ */
+kda_status kda_window_attention(kda_dtype dtype, int32_t batch, int32_t total_tokens,
+                                int32_t max_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t num_pages, int32_t page_size, int32_t table_rows,
+                                int32_t table_width, int32_t window, int32_t sinks, const void *q,
+                                const void *kv_pool, const int32_t *page_table,
+                                const int32_t *slot, const int32_t *cu_tokens,
+                                const int32_t *kv_len, float scale, void *o, void *stream);
+
+/*
+ * kda_pages_copy - pages dst[i] := pages src[i] in every layer.
+ *
+ *   pool        num_layers pools of num_pages pages of page_bytes bytes, one
+ *               after the other (page_bytes a multiple of 16; a row of a
+ *               recurrent-state pool is such a page too)
+ *   src, dst    [n] int32: an entry with src or dst outside [0, P) is skipped;
+ *               no dst may repeat or be another entry's src
+ */
+kda_status kda_pages_copy(int32_t num_layers, int32_t num_pages, int64_t page_bytes, int32_t n,
+                          const int32_t *src, const int32_t *dst, void *pool, void *stream);
+
+/* Bytes of workspace for kda_pages_fork and kda_pages_compact. */
+size_t kda_pages_workspace_size(int32_t num_pages, int32_t table_rows);
+
+/*
+ * kda_pages_fork - row child[i] becomes a branch of row parent[i]: the same
+ * length, sharing its whole pages, with a page of its own in place of a
+ * part-filled last one (copied in every layer).  A page is free when no row of
+ * the table names it; what a child row named before is released by the call.
+ * Fresh pages are the lowest free ones, in the order of i.
+ *
+ *   num_forks   F in [0, R];  parent, child [F] int32; no row is a child twice,
+ *               nor both a child and a parent
+ *   workspace   kda_pages_workspace_size() bytes, 16-byte aligned
+ * A fork with a row out of range, parent = child, a parent's kv_len out of
+ * range, or no page left, is refused by the kernel (its child row, if there is
+ * one and it is not the parent, is left empty; KDA_ERR_DEVICE_CHECK, detail = i).
+ * KDA_ERR_WORKSPACE: workspace missing or small.  KDA_ERR_UNSUPPORTED: num_pages
+ * above 2^20 or table_rows above 2^18, M page_size above 2^31 - 1.
+ */
+kda_status kda_pages_fork(int32_t num_layers, int32_t num_pages, int64_t page_bytes,
+                          int32_t page_size, int32_t table_rows, int32_t table_width,
+                          int32_t num_forks, const int32_t *parent, const int32_t *child,
+                          int32_t *page_table, int32_t *kv_len, void *pool, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/*
+ * kda_pages_release - rows give pages back.  window = 0: the row is emptied (its
+ * entries -1, its kv_len 0).  window >= 1: only the pages that no token to come
+ * (index >= kv_len) can see with this window and these sinks become -1.
+ *
+ *   rows        [n] int32; one out of range is refused (KDA_ERR_DEVICE_CHECK,
+ *               detail = i)
+ */
+kda_status kda_pages_release(int32_t table_rows, int32_t table_width, int32_t page_size,
+                             int32_t n, const int32_t *rows, int32_t window, int32_t sinks,
+                             int32_t *page_table, int32_t *kv_len, void *stream);
+
+/*
+ * kda_pages_compact - the L pages that rows name are brought into pages [0, L):
+ * those at L and above move, in order, into the unnamed ones below L, in every
+ * layer, and table_out is table_in with the new names (entries that name no page
+ * are kept; table_out may be table_in).  Pages below L stay where they are.
+ *
+ *   num_live    [1] int32 (device) out: L
+ *   workspace, errors  as kda_pages_fork
+ */
+kda_status kda_pages_compact(int32_t num_layers, int32_t num_pages, int64_t page_bytes,
+                             int32_t table_rows, int32_t table_width, const int32_t *table_in,
+                             int32_t *table_out, int32_t *num_live, void *pool, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
 /*
  * kda_check_prefill_inputs - the contents checks the host cannot make before a
  * prefill: cu_seqlens starts at 0, never decreases and ends at total_tokens;
