@@ -193,7 +193,8 @@ cudaError_t launch_window_attention_rows(const WindowAttentionArgs &a, cudaStrea
 }
 
 cudaError_t launch_window_attention(const WindowAttentionArgs &a, cudaStream_t stream) {
-    return launch_window_attention_rows(a, stream);
+    if (a.cache.total_tokens == 0) return cudaSuccess;
+    return a.dtype == KDA_BF16 ? launch_window_attention_tc(a, stream) : launch_window_attention_rows(a, stream);
 }
 
 }  // namespace kda

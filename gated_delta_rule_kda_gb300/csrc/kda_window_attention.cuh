@@ -94,5 +94,6 @@ __device__ __forceinline__ bool attn_visible(int32_t p, int32_t j, int32_t windo
 }
 
 cudaError_t launch_window_attention_rows(const WindowAttentionArgs &a, cudaStream_t stream);
+cudaError_t launch_window_attention_tc(const WindowAttentionArgs &a, cudaStream_t stream);
 
 }  // namespace kda

@@ -1,0 +1,624 @@
+// Sliding-window attention over the paged cache on the tensor cores (bf16): prefill, chunked
+// prefill, and any step whose requests bring more rows than the split-row kernel takes.
+//
+//   s = q k^T;  p = 2^(c s - c m), c = scale log2 e;  l += sum p;  o += p v;  at the end o / l
+// The reference m of a row follows its running maximum lazily: it moves (and o, l are scaled by
+// 2^(c (m_old - m_new))) only when a score exceeds it by more than 2^8 in p, so that p <= 2^8 and
+// almost every tile leaves o alone; the division by l removes the choice of m again.  s, m, l and
+// o are fp32; p enters its product rounded to bf16 (the tensor core takes both operands in one
+// type), which costs at most 2^-8 of each weight.
+//
+// A work item is 2 x 128 rows of one request and key/value head; a row is a (token, query head of
+// the group) pair, so that the heads of a group share every key and value, and a tile of 128 rows
+// spans only 128 / G tokens: the window's edges then cost few masked tiles.  Keys come in tiles of
+// 128, those of the sinks first.  One CTA per SM stays and takes items in turn.
+//   warp 8      TMA: q of the next item, then k, v tiles page by page into a ring of five 32 KB
+//               stages (a page that does not exist is an out-of-range box, which reads as zeros)
+//   warp 9      issues the MMAs: s0 = q0 k^T and s1 = q1 k^T into TMEM, o += p v with p read from
+//               TMEM (in place of s).  While one row tile's softmax runs, the tensor core works on
+//               the other's products
+//   warps 0-7   softmax, a thread a row: warps 0-3 tile 0, warps 4-7 tile 1; the epilogue
+//   warps 10-11 values behind a mask: a product with p = 0 would still turn NaN or infinity into
+//               NaN, so tiles that some row must not see are gone through first: keys that no row
+//               sees are cleared, and a non-finite value of any other key marks the item, whose
+//               rows are then computed again one by one, each from its visible keys alone.
+// TMEM: s0, s1, o0, o1 of 128 columns each.  Bound: the tensor core (two 128 x 128 x 128 products
+// a key tile and row tile).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "kda_window_attention.cuh"
+#include "tc_primitives.cuh"
+
+namespace kda {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 384;
+constexpr int kTile = 128;                    // rows of a row tile, keys of a key tile
+constexpr uint32_t kTileBytes = kTile * kD * 2;
+constexpr int kStages = 5;
+constexpr int kWarpTma = 8, kWarpMma = 9, kWarpScrub = 10;
+constexpr uint64_t kWaitNs = 2000000000ull;
+// 384 threads start with 168 registers; the softmax warps take 216, the others keep 72:
+// 256 * 216 + 128 * 72 = 384 * 168
+constexpr int kRegsSoftmax = 216, kRegsOther = 72;
+
+enum Bar {
+    B_QFULL, B_QEMPTY, B_KVFULL, B_RAW = B_KVFULL + kStages, B_KVEMPTY = B_RAW + kStages,
+    B_CLEAN = B_KVEMPTY + kStages,
+    B_S = B_CLEAN + kStages, B_P = B_S + 2, B_O = B_P + 2, B_DRAIN = B_O + 2, B_COUNT
+};
+
+constexpr uint32_t SM_Q = 0, SM_KV = 2 * kTileBytes, SM_END = SM_KV + kStages * kTileBytes;
+constexpr size_t SM_DYN = SM_END + 1024;  // the start is rounded up to 1024 bytes
+
+struct Params {
+    CUtensorMap tm_q;   // [T][Hq][128], boxes of tq tokens x G heads x 64 channels
+    CUtensorMap tm_kv;  // [2 P Hkv page_size][128], boxes of a page x 64 channels
+    WindowAttentionArgs a;
+    int32_t G, tq;      // query heads a kv head, tokens of a row tile
+    int32_t kv_rows;    // 2 P Hkv page_size
+    float c;            // |scale| log2 e (1 when scale = 0)
+    int32_t sign;       // of scale
+};
+
+struct Shared {
+    uint64_t bar[B_COUNT];
+    uint32_t tmem;
+    uint32_t abort;
+    uint32_t tainted[4];  // by item % 4 (at most two are ahead of an epilogue): the number, from 1, of an
+                          // item whose masked tiles held a non-finite value
+};
+
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Waits for a phase, giving up after kWaitNs or when another warp has given up.
+__device__ __forceinline__ bool wait(Shared &sh, int bar, uint32_t parity, const Params &p) {
+    if (mbar_try_wait(sh.bar + bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        for (int i = 0; i < 4; ++i)
+            if (mbar_try_wait(sh.bar + bar, parity)) return true;
+        if (*reinterpret_cast<volatile uint32_t *>(&sh.abort)) return false;
+        if (global_timer_ns() - t0 > kWaitNs) {
+            atomicExch(&sh.abort, 1u);
+            record_status(p.a.status, KDA_ERR_DEVICE_TIMEOUT, (uint32_t)(64 + bar));
+            return false;
+        }
+    }
+}
+
+// The ring of k, v stages: tile loads in order, stage n % kStages, phase n / kStages.  A load
+// completes B_KVFULL of its stage, or B_RAW when the tile is values to be gone through first
+// (B_CLEAN follows); those barriers' phases are counted by use, a bit a stage.
+struct Ring {
+    int stage = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// One work item.  Every warp walks the items by itself, in the same order.
+struct Item {
+    AttnRequest req;
+    int32_t h, t0;         // kv head, first token
+    int32_t p_min, p_max;  // indices of its first and last token
+    bool two;              // the second row tile has tokens
+    AttnKeys keys{0, -1, 1, 0, kTile};
+
+    // false past the last item
+    __device__ __forceinline__ bool load(const Params &p, AttnWalk &walk, int64_t w) {
+        const int32_t Hkv = p.a.num_kv_heads, tokens = 2 * p.tq;
+        int32_t index;
+        if (!walk.find(p.a, w / Hkv, 1, tokens, req, index)) return false;
+        h = (int32_t)(w % Hkv);
+        // the last tokens of a request first: with little out of the window they see most keys
+        t0 = ((req.n + tokens - 1) / tokens - 1 - index) * tokens;
+        p_min = req.len - req.n + t0;
+        p_max = req.len - req.n + min(t0 + tokens, req.n) - 1;
+        two = req.n - t0 > p.tq;
+        keys = AttnKeys(p_min, p_max, p.a.window, p.a.sinks, kTile);
+        return true;
+    }
+    // Some row of the item must not see some key of the tile that starts at j0.
+    __device__ __forceinline__ bool masked(int32_t j0, const Params &p) const {
+        return masked(j0, p_min, p_max, p);
+    }
+    static __device__ __forceinline__ bool masked(int32_t j0, int32_t lo, int32_t hi, const Params &p) {
+        return j0 + kTile - 1 > lo || (hi - j0 >= p.a.window && j0 + kTile > p.a.sinks);
+    }
+    // Page number i of the row, or -1 where the row has no page or no token up to p_max.
+    __device__ __forceinline__ int32_t page(int32_t i, const Params &p) const {
+        return page(p, req.row, p_max, i);
+    }
+    static __device__ __forceinline__ int32_t page(const Params &p, int32_t row, int32_t last, int32_t i) {
+        const CacheArgs &c = p.a.cache;
+        if (i >= c.table_width || i * c.page_size > last) return -1;
+        const int32_t id = c.page_table[(int64_t)row * c.table_width + i];
+        return (uint32_t)id < (uint32_t)c.num_pages ? id : -1;
+    }
+};
+
+// ---------------------------------------------------------------------------
+// TMA
+// ---------------------------------------------------------------------------
+__device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
+    const int lane = threadIdx.x & 31;
+    const int32_t page = p.a.cache.page_size, pages = kTile / page;  // pages of a tile
+    Ring ring;
+    uint32_t loads = 0, items = 0, uses[2] = {0, 0};  // bit s: parity of the uses of KVFULL, RAW + s
+    bool ok = true;
+    AttnWalk walk;
+    Item it;
+    for (int64_t w = blockIdx.x; ok && it.load(p, walk, w); w += gridDim.x) {
+        const int32_t n = it.keys.count();
+        if (n == 0) continue;
+        if (items > 0 && !(ok = wait(sh, B_QEMPTY, (items - 1) & 1, p))) break;
+        if (lane == 0) {
+            const uint32_t bytes = (uint32_t)(p.tq * p.G * 64 * 2);
+            mbar_arrive_expect_tx(sh.bar + B_QFULL, bytes * (it.two ? 4u : 2u));
+            for (int r = 0; r < (it.two ? 2 : 1); ++r)
+                for (int half = 0; half < 2; ++half)
+                    tma_load_3d(smem_u32(sm + SM_Q + r * kTileBytes + half * (kTileBytes / 2)), &p.tm_q,
+                                64 * half, it.h * p.G, it.req.first + it.t0 + r * p.tq, sh.bar + B_QFULL);
+        }
+        ++items;
+        for (int32_t i = 0; ok && i < n; ++i) {
+            const int32_t j0 = it.keys.tile(i) * kTile;
+            // lane = 2 page + half: that page's rows of the tile, 64 channels
+            int32_t id = -1;
+            if (lane < 2 * pages) id = it.page(j0 / page + (lane >> 1), p);
+            for (int kv = 0; kv < 2; ++kv) {
+                if (loads >= kStages && !(ok = wait(sh, B_KVEMPTY + ring.stage, ring.phase ^ 1, p))) break;
+                const int raw = kv == 1 && it.masked(j0, p) ? 1 : 0;
+                uint64_t *full = sh.bar + (raw ? B_RAW : B_KVFULL) + ring.stage;
+                uses[raw] ^= 1u << ring.stage;
+                if (lane == 0) mbar_arrive_expect_tx(full, kTileBytes);
+                __syncwarp();
+                if (lane < 2 * pages) {
+                    const int32_t y = id < 0 ? p.kv_rows  // out of range: zeros
+                                             : ((id * 2 + kv) * p.a.num_kv_heads + it.h) * page;
+                    tma_load_2d(smem_u32(sm + SM_KV + ring.stage * kTileBytes + (lane & 1) * (kTileBytes / 2) +
+                                         (lane >> 1) * page * 128),
+                                &p.tm_kv, 64 * (lane & 1), y, full);
+                }
+                ring.next();
+                ++loads;
+            }
+        }
+    }
+    if (!ok && lane == 0) {  // gave up: the copies in flight still land before the CTA leaves
+        if (items > 0) mbar_wait_bounded(sh.bar + B_QFULL, (items - 1) & 1, kWaitNs);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_wait_bounded(sh.bar + B_KVFULL + s, ~(uses[0] >> s) & 1, kWaitNs);
+            mbar_wait_bounded(sh.bar + B_RAW + s, ~(uses[1] >> s) & 1, kWaitNs);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// MMA
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void mma_scores(uint32_t tmem, uint32_t q, uint32_t k, int r) {
+#pragma unroll
+    for (int s = 0; s < kD / 16; ++s)
+        mma_bf16(tmem + 128 * r, sw128_desc_k(q + r * kTileBytes, kTile, s), sw128_desc_k(k, kTile, s),
+                 idesc_bf16_f32(kTile, kTile), s > 0);
+}
+__device__ __forceinline__ void mma_values(uint32_t tmem, uint32_t v, int r, bool first) {
+#pragma unroll
+    for (int s = 0; s < kTile / 16; ++s)
+        mma_bf16_tmem_a(tmem + 256 + 128 * r, tmem + 128 * r + 8 * s, sw128_desc_mn(v + 2048 * s, kTileBytes / 2),
+                        idesc_bf16_f32(kTile, kD) | kIdescBMN, !first || s > 0);
+}
+
+__device__ void mma_warp(const Params &p, Shared &sh, unsigned char *sm) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t tmem = sh.tmem, q = smem_u32(sm + SM_Q), kv = smem_u32(sm + SM_KV);
+    Ring ring;               // the next tile to be used
+    uint32_t full_phase = 0, clean_phase = 0;  // bit s: phase of B_KVFULL, B_CLEAN + s
+    uint32_t items = 0, p_phase[2] = {0, 0};
+    bool ok = true;
+    AttnWalk walk;
+    Item it;
+    for (int64_t w = blockIdx.x; ok && it.load(p, walk, w); w += gridDim.x) {
+        const int32_t n = it.keys.count();
+        if (n == 0) continue;
+        if (!(ok = wait(sh, B_QFULL, items & 1, p))) break;
+        ++items;
+        if (!(ok = wait(sh, B_KVFULL + ring.stage, full_phase >> ring.stage & 1, p))) break;
+        full_phase ^= 1u << ring.stage;
+        fence_after_sync();
+        if (lane == 0) {
+            mma_scores(tmem, q, kv + ring.stage * kTileBytes, 0);
+            mma_commit(sh.bar + B_S);
+            if (it.two) {
+                mma_scores(tmem, q, kv + ring.stage * kTileBytes, 1);
+                mma_commit(sh.bar + B_S + 1);
+            }
+            mma_commit(sh.bar + B_KVEMPTY + ring.stage);
+            if (n == 1) mma_commit(sh.bar + B_QEMPTY);
+        }
+        ring.next();
+        for (int32_t i = 0; i < n; ++i) {
+            const Ring v = ring;
+            Ring k = ring;
+            k.next();
+            const bool more = i + 1 < n;
+            if (it.masked(it.keys.tile(i) * kTile, p)) {
+                ok = wait(sh, B_CLEAN + v.stage, clean_phase >> v.stage & 1, p);
+                clean_phase ^= 1u << v.stage;
+            } else {
+                ok = wait(sh, B_KVFULL + v.stage, full_phase >> v.stage & 1, p);
+                full_phase ^= 1u << v.stage;
+            }
+            for (int r = 0; ok && r < (it.two ? 2 : 1); ++r) {
+                if (!(ok = wait(sh, B_P + r, p_phase[r], p))) break;
+                p_phase[r] ^= 1;
+                if (r == 0 && more) {
+                    if (!(ok = wait(sh, B_KVFULL + k.stage, full_phase >> k.stage & 1, p))) break;
+                    full_phase ^= 1u << k.stage;
+                }
+                fence_after_sync();
+                if (lane == 0) {
+                    mma_values(tmem, kv + v.stage * kTileBytes, r, i == 0);
+                    if (!more) mma_commit(sh.bar + B_O + r);
+                    if (r == 1 || !it.two) mma_commit(sh.bar + B_KVEMPTY + v.stage);
+                    if (more) {
+                        mma_scores(tmem, q, kv + k.stage * kTileBytes, r);
+                        mma_commit(sh.bar + B_S + r);
+                        if (r == 1 || !it.two) {
+                            mma_commit(sh.bar + B_KVEMPTY + k.stage);
+                            if (i + 2 == n) mma_commit(sh.bar + B_QEMPTY);
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            ring.next();
+            if (more) ring.next();
+        }
+    }
+    if (!ok && lane == 0) {  // gave up: the MMAs in flight finish before TMEM is freed
+        mma_commit(sh.bar + B_DRAIN);
+        mbar_wait_bounded(sh.bar + B_DRAIN, 0, kWaitNs);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Values behind a mask
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t any_nonfinite(uint32_t x) {
+    return ((x & 0x7f80u) == 0x7f80u) | ((x & 0x7f800000u) == 0x7f800000u);
+}
+
+__device__ void scrub_warps(const Params &p, Shared &sh, unsigned char *sm) {
+    const int t = threadIdx.x - kWarpScrub * 32, lane = t & 31;
+    Ring ring;
+    uint32_t items = 0, raw_phase = 0;  // bit s: phase of B_RAW + s
+    AttnWalk walk;
+    Item it;
+    for (int64_t w = blockIdx.x; it.load(p, walk, w); w += gridDim.x) {
+        const int32_t n = it.keys.count();
+        if (n == 0) continue;
+        ++items;
+        for (int32_t i = 0; i < n; ++i) {
+            ring.next();  // k
+            const Ring v = ring;
+            ring.next();
+            const int32_t j0 = it.keys.tile(i) * kTile;
+            if (!it.masked(j0, p)) continue;
+            if (!wait(sh, B_RAW + v.stage, raw_phase >> v.stage & 1, p)) return;
+            raw_phase ^= 1u << v.stage;
+            unsigned char *tile = sm + SM_KV + v.stage * kTileBytes;
+            uint32_t bad = 0;
+#pragma unroll 4
+            for (int c = t; c < (int)kTileBytes / 16; c += 64) {  // 16-byte chunk c of the tile
+                const int32_t j = j0 + ((c >> 3) & (kTile - 1));  // its key
+                uint4 *x = reinterpret_cast<uint4 *>(tile + 16 * c);
+                // seen by some row: not past the last token, and within its first token's reach
+                if (j <= it.p_max && (it.p_min - j < p.a.window || j < p.a.sinks)) {
+                    const uint4 y = *x;
+                    bad |= any_nonfinite(y.x) | any_nonfinite(y.y) | any_nonfinite(y.z) | any_nonfinite(y.w);
+                } else {
+                    *x = make_uint4(0, 0, 0, 0);
+                }
+            }
+            if (bad) *reinterpret_cast<volatile uint32_t *>(&sh.tainted[items & 3]) = items;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sh.bar + B_CLEAN + v.stage);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Softmax and epilogue
+// ---------------------------------------------------------------------------
+// The lowest n bits.
+__device__ __forceinline__ uint32_t low_bits(int32_t n) {
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// One row from its visible keys alone, fp32 throughout; a warp a row, four channels a lane.  Runs
+// only when a masked tile held a non-finite value.
+__device__ __noinline__ void attention_row(const Params &p, int64_t q_row, int32_t h, int32_t table_row, int32_t pos) {
+    const int lane = threadIdx.x & 31;
+    const WindowAttentionArgs &a = p.a;
+    const int32_t page = a.cache.page_size;
+    const int64_t row = q_row * kD + 4 * lane;
+    const float4 q = load4(static_cast<const __nv_bfloat16 *>(a.q) + row);
+    const int64_t kv_stride = (int64_t)a.num_kv_heads * page * kD;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = -INFINITY, l = 0.f;
+    for (int32_t j = 0; j <= pos; ++j) {
+        if (!attn_visible(pos, j, a.window, a.sinks)) {
+            j = max(j, pos - a.window);  // the gap between the sinks and the window
+            continue;
+        }
+        const int32_t id = Item::page(p, table_row, pos, j / page);
+        if (id < 0) continue;
+        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.kv_pool) + (int64_t)id * 2 * kv_stride +
+                                   ((int64_t)h * page + j % page) * kD + 4 * lane;
+        const float4 k = load4(src), v = load4(src + kv_stride);
+        float s = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        s *= a.scale;
+        const float top = fmaxf(m, s), keep = top == -INFINITY ? 1.f : expf(m - top);
+        const float e = top == -INFINITY ? 0.f : expf(s - top);
+        l = l * keep + e;
+        o = make_float4(o.x * keep + e * v.x, o.y * keep + e * v.y, o.z * keep + e * v.z, o.w * keep + e * v.w);
+        m = top;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    store4(static_cast<__nv_bfloat16 *>(a.o) + row, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+}
+
+__device__ void softmax_warps(const Params &p, Shared &sh, int r) {
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
+    const int row = 32 * quarter + lane;  // of the row tile
+    const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+    const uint32_t s_tmem = sh.tmem + lanes + 128 * r, o_tmem = sh.tmem + lanes + 256 + 128 * r;
+    const WindowAttentionArgs &a = p.a;
+    const int32_t page = a.cache.page_size, pages = kTile / page;
+    uint32_t s_phase = 0, o_phase = 0, items = 0;
+    AttnWalk walk;
+    Item it;
+    for (int64_t w = blockIdx.x; it.load(p, walk, w); w += gridDim.x) {
+        const int32_t n = it.keys.count();
+        if (n > 0) ++items;
+        if (r == 1 && !it.two) continue;
+        // this row's token, and the tile's first and last (rows past the last token see nothing)
+        const int32_t first = it.t0 + r * p.tq, token = first + row / p.G, g = row % p.G;
+        const bool live = row < p.tq * p.G && token < it.req.n;
+        const int32_t p0 = it.req.len - it.req.n;
+        const int32_t pos = live ? p0 + token : -1;
+        const int32_t tile_min = p0 + first, tile_max = p0 + min(first + p.tq, it.req.n) - 1;
+        float m = -INFINITY, l = 0.f;
+        for (int32_t i = 0; i < n; ++i) {
+            const int32_t j0 = it.keys.tile(i) * kTile;
+            int32_t id = 0;
+            if (lane < pages) id = it.page(j0 / page + lane, p);
+            const uint32_t mapped = __ballot_sync(0xffffffffu, id >= 0);  // lanes from `pages` on: 1
+            if (!wait(sh, B_S + r, s_phase, p)) return;
+            s_phase ^= 1;
+            fence_after_sync();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32_async(s_tmem + 32 * c, s[c]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld_wait32(s[c]);
+            if (p.sign <= 0) {  // a negative scale turns the order round; zero weighs all keys alike
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) s[c][k] = p.sign < 0 ? s[c][k] ^ 0x80000000u : 0u;
+            }
+            if (mapped != 0xffffffffu || Item::masked(j0, tile_min, tile_max, p)) {
+                const int32_t hi = pos - j0 + 1, lo = pos < a.window ? 0 : pos - a.window + 1 - j0;
+                const int32_t sk = a.sinks - j0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t bits = low_bits(hi - 32 * c) & (~low_bits(lo - 32 * c) | low_bits(sk - 32 * c));
+                    if (page == 16) bits &= (mapped >> (2 * c) & 1 ? 0xffffu : 0u) | (mapped >> (2 * c + 1) & 1 ? 0xffff0000u : 0u);
+                    else if (!(mapped >> (32 * c / page) & 1)) bits = 0;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (!(bits >> k & 1)) s[c][k] = 0xff800000u;  // -inf
+                }
+            }
+            float top[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                top[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+#pragma unroll
+                for (int k = 2; k < 32; k += 2)
+                    top[c] = fmaxf(top[c], fmaxf(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])));
+            }
+            const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+            // lazily: only past 2^8 (from -inf at the row's first visible key)
+            const bool move = (now - m) * p.c > 8.f;
+            if (__any_sync(0xffffffffu, move)) {
+                const float f = move ? ex2_approx((m - now) * p.c) : 1.f;
+                if (move) m = now;
+                l *= f;
+                // s of this tile is complete, so the products issued before it are as well
+                if (i > 0) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        float o[16];
+                        tmem_ld16(o_tmem + 16 * c, o);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] *= f;
+                        tmem_st16(o_tmem + 16 * c, o);
+                    }
+                }
+            }
+            const float base = m == -INFINITY ? 0.f : -m * p.c;
+            const float2 c2 = make_float2(p.c, p.c), b2 = make_float2(base, base);
+            float2 sum = make_float2(0.f, 0.f), sum2 = sum;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t out[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const float2 x = fma2(make_float2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), c2, b2);
+                    const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                    if (k & 1) sum2 = fma2(e, make_float2(1.f, 1.f), sum2);
+                    else sum = fma2(e, make_float2(1.f, 1.f), sum);
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(e.x, e.y);
+                    out[k] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+                tmem_st16u(s_tmem + 16 * c, out);
+            }
+            l += (sum.x + sum.y) + (sum2.x + sum2.y);
+            tmem_wait_st();
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sh.bar + B_P + r);
+        }
+
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        bool tainted = false;
+        if (n > 0) {
+            if (!wait(sh, B_O + r, o_phase, p)) return;
+            o_phase ^= 1;
+            fence_after_sync();
+            tainted = *reinterpret_cast<volatile uint32_t *>(&sh.tainted[items & 3]) == items;
+        }
+        if (tainted) {
+            for (int k = 0; k < 32; ++k) {
+                const int32_t rr = 32 * quarter + k, tk = first + rr / p.G;
+                if (rr < p.tq * p.G && tk < it.req.n) 
+                    attention_row(p, (int64_t)(it.req.first + tk) * a.num_q_heads + it.h * p.G + rr % p.G, it.h,
+                                  it.req.row, p0 + tk);
+            }
+            continue;
+        }
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.o) +
+                             ((int64_t)(it.req.first + token) * a.num_q_heads + it.h * p.G + g) * kD;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            float o[32];
+            if (n > 0) tmem_ld32(o_tmem + 32 * c, o);
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+                uint4 x = make_uint4(0, 0, 0, 0);
+                uint32_t *y = &x.x;
+                if (l != 0.f) {  // (a NaN sum stays one)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(o[k + 2 * u] * inv, o[k + 2 * u + 1] * inv);
+                        y[u] = *reinterpret_cast<const uint32_t *>(&h);
+                    }
+                }
+                if (live) *reinterpret_cast<uint4 *>(dst + 32 * c + k) = x;
+            }
+        }
+        fence_before_sync();  // the next item's products write o after this row tile's next p
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_constant__ Params p) {
+    extern __shared__ unsigned char dyn[];
+    __shared__ Shared sh;
+    unsigned char *sm = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < B_COUNT; ++i)
+            mbar_init(sh.bar + i, i >= B_CLEAN && i < B_S ? 2 : i >= B_P && i < B_O ? 4 : 1);
+        sh.abort = 0;
+        for (int i = 0; i < 4; ++i) sh.tainted[i] = 0;
+        fence_mbar_init();
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(&sh.tmem, 512);
+        tmem_relinquish();
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        softmax_warps(p, sh, warp >> 2);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        if (warp == kWarpTma) tma_warp(p, sh, sm);
+        else if (warp == kWarpMma) mma_warp(p, sh, sm);
+        else scrub_warps(p, sh, sm);
+    }
+    __syncthreads();
+    if (warp == kWarpMma) tmem_dealloc(sh.tmem, 512);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+        return nullptr;
+    }();
+    return fn;
+}
+
+}  // namespace
+
+bool encode_kv_map(CUtensorMap *m, const WindowAttentionArgs &a, int32_t box_rows) {
+    auto fn = tensor_map_encoder();
+    if (fn == nullptr) return false;
+    const CacheArgs &c = a.cache;
+    const cuuint64_t dims[2] = {kD, 2ull * c.num_pages * a.num_kv_heads * c.page_size};
+    const cuuint64_t strides[1] = {kD * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(a.kv_pool), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_window_attention_tc(const WindowAttentionArgs &a, cudaStream_t stream) {
+    Params p;
+    p.a = a;
+    p.G = a.num_q_heads / a.num_kv_heads;
+    p.tq = kTile / p.G;
+    p.kv_rows = (int32_t)(2ll * a.cache.num_pages * a.num_kv_heads * a.cache.page_size);
+    p.sign = a.scale > 0.f ? 1 : a.scale < 0.f ? -1 : a.scale == 0.f ? 0 : 1;  // NaN: answers NaN
+    p.c = p.sign == 0 ? 1.f : (float)(fabs((double)a.scale) * 1.4426950408889634);
+    auto fn = tensor_map_encoder();
+    if (fn == nullptr || !encode_kv_map(&p.tm_kv, a, a.cache.page_size)) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {kD, (cuuint64_t)a.num_q_heads, (cuuint64_t)a.cache.total_tokens};
+    const cuuint64_t strides[2] = {kD * 2, (cuuint64_t)a.num_q_heads * kD * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.tq}, estr[3] = {1, 1, 1};
+    if (fn(&p.tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dims, strides, box, estr,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorNotSupported;
+    cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SM_DYN);
+    if (e != cudaSuccess) return e;
+    // each request rounds up to whole items at most once
+    const int64_t items = ((int64_t)a.cache.total_tokens / (2 * p.tq) + a.cache.batch) * a.num_kv_heads;
+    const int64_t sms = device_sm_count();
+    attention_tc_kernel<<<(unsigned)(items < sms ? items : sms), kThreads, SM_DYN, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace kda
