@@ -41,9 +41,9 @@ constexpr uint32_t kTileBytes = kTile * kD * 2;
 constexpr int kStages = 5;
 constexpr int kWarpTma = 8, kWarpMma = 9, kWarpScrub = 10;
 constexpr uint64_t kWaitNs = 2000000000ull;
-// 384 threads start with 168 registers; the softmax warps take 216, the others keep 72:
-// 256 * 216 + 128 * 72 = 384 * 168
-constexpr int kRegsSoftmax = 216, kRegsOther = 72;
+// 384 threads start with 168 registers; the softmax warps take 184, the others keep 136:
+// 256 * 184 + 128 * 136 = 384 * 168
+constexpr int kRegsSoftmax = 184, kRegsOther = 136;
 
 enum Bar {
     B_QFULL, B_QEMPTY, B_KVFULL, B_RAW = B_KVFULL + kStages, B_KVEMPTY = B_RAW + kStages,
@@ -420,39 +420,41 @@ __device__ void softmax_warps(const Params &p, Shared &sh, int r) {
             if (!wait(sh, B_S + r, s_phase, p)) return;
             s_phase ^= 1;
             fence_after_sync();
-            uint32_t s[4][32];
+            // Two passes over the row's 128 scores, 32 at a time (TMEM is read twice, which costs
+            // less than holding them all): the maximum, then the exponentials.
+            const bool masked = mapped != 0xffffffffu || Item::masked(j0, tile_min, tile_max, p);
+            const int32_t hi = pos - j0 + 1, lo = pos < a.window ? 0 : pos - a.window + 1 - j0;
+            const int32_t sk = a.sinks - j0;
+            auto scores = [&](uint32_t (&s)[32], int c) {
+                if (p.sign <= 0) {  // a negative scale turns the order round; zero weighs all keys alike
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32_async(s_tmem + 32 * c, s[c]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld_wait32(s[c]);
-            if (p.sign <= 0) {  // a negative scale turns the order round; zero weighs all keys alike
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) s[c][k] = p.sign < 0 ? s[c][k] ^ 0x80000000u : 0u;
-            }
-            if (mapped != 0xffffffffu || Item::masked(j0, tile_min, tile_max, p)) {
-                const int32_t hi = pos - j0 + 1, lo = pos < a.window ? 0 : pos - a.window + 1 - j0;
-                const int32_t sk = a.sinks - j0;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                    for (int k = 0; k < 32; ++k) s[k] = p.sign < 0 ? s[k] ^ 0x80000000u : 0u;
+                }
+                if (masked) {
                     uint32_t bits = low_bits(hi - 32 * c) & (~low_bits(lo - 32 * c) | low_bits(sk - 32 * c));
                     if (page == 16) bits &= (mapped >> (2 * c) & 1 ? 0xffffu : 0u) | (mapped >> (2 * c + 1) & 1 ? 0xffff0000u : 0u);
                     else if (!(mapped >> (32 * c / page) & 1)) bits = 0;
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
-                        if (!(bits >> k & 1)) s[c][k] = 0xff800000u;  // -inf
+                        if (!(bits >> k & 1)) s[k] = 0xff800000u;  // -inf
                 }
-            }
-            float top[4];
+            };
+            uint32_t s[2][32];
+            float now = -INFINITY;
+            tmem_ld32_async(s_tmem, s[0]);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                top[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+                tmem_ld_wait32(s[c & 1]);
+                tmem_ld32_async(s_tmem + 32 * ((c + 1) & 3), s[~c & 1]);  // at last the first again
+                scores(s[c & 1], c);
+                float top[2] = {__uint_as_float(s[c & 1][0]), __uint_as_float(s[c & 1][1])};
 #pragma unroll
-                for (int k = 2; k < 32; k += 2)
-                    top[c] = fmaxf(top[c], fmaxf(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])));
+                for (int k = 2; k < 32; k += 2) {
+                    top[0] = fmaxf(top[0], __uint_as_float(s[c & 1][k]));
+                    top[1] = fmaxf(top[1], __uint_as_float(s[c & 1][k + 1]));
+                }
+                now = fmaxf(now, fmaxf(top[0], top[1]));
             }
-            const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
             // lazily: only past 2^8 (from -inf at the row's first visible key)
             const bool move = (now - m) * p.c > 8.f;
             if (__any_sync(0xffffffffu, move)) {
@@ -477,15 +479,20 @@ __device__ void softmax_warps(const Params &p, Shared &sh, int r) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 uint32_t out[16];
+                tmem_ld_wait32(s[c & 1]);
+                if (c < 3) tmem_ld32_async(s_tmem + 32 * (c + 1), s[~c & 1]);
+                scores(s[c & 1], c);
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
-                    const float2 x = fma2(make_float2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), c2, b2);
+                    const float2 x = fma2(make_float2(__uint_as_float(s[c & 1][2 * k]), __uint_as_float(s[c & 1][2 * k + 1])), c2, b2);
                     const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
                     if (k & 1) sum2 = fma2(e, make_float2(1.f, 1.f), sum2);
                     else sum = fma2(e, make_float2(1.f, 1.f), sum);
                     const __nv_bfloat162 h = __floats2bfloat162_rn(e.x, e.y);
                     out[k] = *reinterpret_cast<const uint32_t *>(&h);
                 }
+                // p of keys 32 c .. lies over scores 16 c ..: of those, chunk c and (c < 3, in
+                // flight) c + 1 have been read
                 tmem_st16u(s_tmem + 16 * c, out);
             }
             l += (sum.x + sum.y) + (sum2.x + sum2.y);
