@@ -8,6 +8,8 @@
 // scores and 4 x 8 outputs, so that each shared-memory read feeds two to four FMAs.  A key that a
 // row does not see takes no part: its score is replaced (never computed with), its probability of
 // zero skips the product with v, and keys past the end or without a page are loaded as zeros.
+#include <cfloat>
+
 #include "kda_window_attention.cuh"
 
 namespace kda {
@@ -194,7 +196,10 @@ cudaError_t launch_window_attention_rows(const WindowAttentionArgs &a, cudaStrea
 
 cudaError_t launch_window_attention(const WindowAttentionArgs &a, cudaStream_t stream) {
     if (a.cache.total_tokens == 0) return cudaSuccess;
-    return a.dtype == KDA_BF16 ? launch_window_attention_tc(a, stream) : launch_window_attention_rows(a, stream);
+    // The tensor-core kernel keeps its running maximum on unscaled scores, in the order that a
+    // positive scale leaves alone; any other scale (and fp32) runs on the FMA units.
+    const bool tensor = a.dtype == KDA_BF16 && a.scale > 0.f && a.scale <= FLT_MAX;
+    return tensor ? launch_window_attention_tc(a, stream) : launch_window_attention_rows(a, stream);
 }
 
 }  // namespace kda

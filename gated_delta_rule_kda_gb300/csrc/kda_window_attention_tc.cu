@@ -39,16 +39,19 @@ constexpr int kThreads = 384;
 constexpr int kTile = 128;                    // rows of a row tile, keys of a key tile
 constexpr uint32_t kTileBytes = kTile * kD * 2;
 constexpr int kStages = 5;
+constexpr int kItems = 4;                     // work items announced ahead
+constexpr int kItemReaders = 11;              // warps that read them: softmax, MMA, values
 constexpr int kWarpTma = 8, kWarpMma = 9, kWarpScrub = 10;
 constexpr uint64_t kWaitNs = 2000000000ull;
-// 384 threads start with 168 registers; the softmax warps take 184, the others keep 136:
-// 256 * 184 + 128 * 136 = 384 * 168
-constexpr int kRegsSoftmax = 184, kRegsOther = 136;
+// 384 threads start with 168 registers; the softmax warps take 208, the others keep 88:
+// 256 * 208 + 128 * 88 = 384 * 168
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;
 
 enum Bar {
     B_QFULL, B_QEMPTY, B_KVFULL, B_RAW = B_KVFULL + kStages, B_KVEMPTY = B_RAW + kStages,
     B_CLEAN = B_KVEMPTY + kStages,
-    B_S = B_CLEAN + kStages, B_P = B_S + 2, B_O = B_P + 2, B_DRAIN = B_O + 2, B_COUNT
+    B_S = B_CLEAN + kStages, B_P = B_S + 2, B_O = B_P + 2, B_ITEM = B_O + 2, B_ITEMFREE = B_ITEM + kItems,
+    B_DRAIN = B_ITEMFREE + kItems, B_COUNT
 };
 
 constexpr uint32_t SM_Q = 0, SM_KV = 2 * kTileBytes, SM_END = SM_KV + kStages * kTileBytes;
@@ -60,18 +63,13 @@ struct Params {
     WindowAttentionArgs a;
     int32_t G, tq;      // query heads a kv head, tokens of a row tile
     int32_t kv_rows;    // 2 P Hkv page_size
-    float c;            // |scale| log2 e (1 when scale = 0)
-    int32_t sign;       // of scale
+    float c;            // scale log2 e, > 0
 };
 
-struct Shared {
-    uint64_t bar[B_COUNT];
-    uint32_t tmem;
-    uint32_t abort;
-    uint32_t tainted[4];  // by item % 4 (at most two are ahead of an epilogue): the number, from 1, of an
-                          // item whose masked tiles held a non-finite value
-};
-
+// (a.x + b.x, a.y + b.y)
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    return fma2(a, make_float2(1.f, 1.f), b);
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -82,6 +80,35 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int 
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
+
+// One work item, found by the TMA warp and left in shared memory for the others.
+struct Item {
+    int32_t first, tokens;     // its tokens: rows [first, first + tokens) of q and o
+    int32_t h, row;            // kv head, row of the table
+    int32_t p_min, p_max;      // indices of its first and last token
+    int32_t n;                 // key tiles; < 0: no more items
+    int32_t sink_tiles, skip;  // tile i starts at key 128 (i < sink_tiles ? i : i + skip)
+
+    __device__ __forceinline__ int32_t key(int32_t i) const { return kTile * (i < sink_tiles ? i : i + skip); }
+    __device__ __forceinline__ bool two(const Params &p) const { return tokens > p.tq; }  // a second row tile
+    // Some row of the item must not see some key of the tile that starts at j0.
+    __device__ __forceinline__ bool masked(int32_t j0, const Params &p) const {
+        return masked(j0, p_min, p_max, p);
+    }
+    static __device__ __forceinline__ bool masked(int32_t j0, int32_t lo, int32_t hi, const Params &p) {
+        return j0 + kTile - 1 > lo || (hi - j0 >= p.a.window && j0 + kTile > p.a.sinks);
+    }
+};
+
+struct Shared {
+    uint64_t bar[B_COUNT];
+    Item items[kItems];
+    uint32_t mapped[8];   // by key tile % 8: bit i: the tile's page i exists
+    uint32_t tainted[4];  // by item % 4 (at most two are ahead of an epilogue): the number, from 1, of an
+                          // item whose masked tiles held a non-finite value
+    uint32_t tmem;
+    uint32_t abort;
+};
 
 // Waits for a phase, giving up after kWaitNs or when another warp has given up.
 __device__ __forceinline__ bool wait(Shared &sh, int bar, uint32_t parity, const Params &p) {
@@ -113,82 +140,102 @@ struct Ring {
     }
 };
 
-// One work item.  Every warp walks the items by itself, in the same order.
-struct Item {
-    AttnRequest req;
-    int32_t h, t0;         // kv head, first token
-    int32_t p_min, p_max;  // indices of its first and last token
-    bool two;              // the second row tile has tokens
-    AttnKeys keys{0, -1, 1, 0, kTile};
-
-    // false past the last item
-    __device__ __forceinline__ bool load(const Params &p, AttnWalk &walk, int64_t w) {
-        const int32_t Hkv = p.a.num_kv_heads, tokens = 2 * p.tq;
-        int32_t index;
-        if (!walk.find(p.a, w / Hkv, 1, tokens, req, index)) return false;
-        h = (int32_t)(w % Hkv);
-        // the last tokens of a request first: with little out of the window they see most keys
-        t0 = ((req.n + tokens - 1) / tokens - 1 - index) * tokens;
-        p_min = req.len - req.n + t0;
-        p_max = req.len - req.n + min(t0 + tokens, req.n) - 1;
-        two = req.n - t0 > p.tq;
-        keys = AttnKeys(p_min, p_max, p.a.window, p.a.sinks, kTile);
-        return true;
-    }
-    // Some row of the item must not see some key of the tile that starts at j0.
-    __device__ __forceinline__ bool masked(int32_t j0, const Params &p) const {
-        return masked(j0, p_min, p_max, p);
-    }
-    static __device__ __forceinline__ bool masked(int32_t j0, int32_t lo, int32_t hi, const Params &p) {
-        return j0 + kTile - 1 > lo || (hi - j0 >= p.a.window && j0 + kTile > p.a.sinks);
-    }
-    // Page number i of the row, or -1 where the row has no page or no token up to p_max.
-    __device__ __forceinline__ int32_t page(int32_t i, const Params &p) const {
-        return page(p, req.row, p_max, i);
-    }
-    static __device__ __forceinline__ int32_t page(const Params &p, int32_t row, int32_t last, int32_t i) {
-        const CacheArgs &c = p.a.cache;
-        if (i >= c.table_width || i * c.page_size > last) return -1;
-        const int32_t id = c.page_table[(int64_t)row * c.table_width + i];
-        return (uint32_t)id < (uint32_t)c.num_pages ? id : -1;
+// The items in turn, for the warps that read them.
+struct Items {
+    uint32_t k = 0;
+    // The next item; false after the last one or when a wait gave up.
+    __device__ __forceinline__ bool next(Shared &sh, const Params &p, Item &it) {
+        const uint32_t slot = k % kItems;
+        if (!wait(sh, B_ITEM + slot, k / kItems & 1, p)) return false;
+        it = sh.items[slot];
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(sh.bar + B_ITEMFREE + slot);
+        ++k;
+        return it.n >= 0;
     }
 };
 
 // ---------------------------------------------------------------------------
 // TMA
 // ---------------------------------------------------------------------------
+// Work item w, or n = -1 past the last one.
+__device__ __forceinline__ Item find_item(const Params &p, AttnWalk &walk, int64_t w, AttnRequest &req) {
+    const int32_t Hkv = p.a.num_kv_heads, tokens = 2 * p.tq;
+    Item it;
+    int32_t index;
+    it.n = -1;
+    if (!walk.find(p.a, w / Hkv, 1, tokens, req, index)) return it;
+    // the last tokens of a request first: with little out of the window they see most keys
+    const int32_t t0 = ((req.n + tokens - 1) / tokens - 1 - index) * tokens;
+    it.first = req.first + t0;
+    it.tokens = min(tokens, req.n - t0);
+    it.h = (int32_t)(w % Hkv);
+    it.row = req.row;
+    it.p_min = req.len - req.n + t0;
+    it.p_max = it.p_min + it.tokens - 1;
+    const AttnKeys keys(it.p_min, it.p_max, p.a.window, p.a.sinks, kTile);
+    it.n = keys.count();
+    it.sink_tiles = keys.sink_tiles;
+    it.skip = keys.low_tile - keys.sink_tiles;
+    return it;
+}
+
+// Page i of a row, or -1 where there is none or it starts past index `last`.
+__device__ __forceinline__ int32_t page_of(const Params &p, int32_t row, int32_t last, int32_t i) {
+    const CacheArgs &c = p.a.cache;
+    if (i >= c.table_width || i * c.page_size > last) return -1;
+    const int32_t id = c.page_table[(int64_t)row * c.table_width + i];
+    return (uint32_t)id < (uint32_t)c.num_pages ? id : -1;
+}
+
 __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
     const int lane = threadIdx.x & 31;
     const int32_t page = p.a.cache.page_size, pages = kTile / page;  // pages of a tile
     Ring ring;
-    uint32_t loads = 0, items = 0, uses[2] = {0, 0};  // bit s: parity of the uses of KVFULL, RAW + s
+    uint32_t loads = 0, items = 0, tiles = 0, uses[2] = {0, 0};  // bit s: parity of the uses of KVFULL, RAW + s
     bool ok = true;
     AttnWalk walk;
-    Item it;
-    for (int64_t w = blockIdx.x; ok && it.load(p, walk, w); w += gridDim.x) {
-        const int32_t n = it.keys.count();
-        if (n == 0) continue;
+    AttnRequest req;
+    int64_t w = blockIdx.x;
+    for (uint32_t k = 0; ok; ++k, w += gridDim.x) {
+        const Item it = find_item(p, walk, w, req);
+        if (k >= kItems && !(ok = wait(sh, B_ITEMFREE + k % kItems, (k / kItems - 1) & 1, p))) break;
+        if (lane == 0) {
+            sh.items[k % kItems] = it;
+            mbar_arrive(sh.bar + B_ITEM + k % kItems);
+        }
+        if (it.n < 0) break;
+        if (it.n == 0) continue;
+        const bool two = it.two(p);
         if (items > 0 && !(ok = wait(sh, B_QEMPTY, (items - 1) & 1, p))) break;
         if (lane == 0) {
             const uint32_t bytes = (uint32_t)(p.tq * p.G * 64 * 2);
-            mbar_arrive_expect_tx(sh.bar + B_QFULL, bytes * (it.two ? 4u : 2u));
-            for (int r = 0; r < (it.two ? 2 : 1); ++r)
+            mbar_arrive_expect_tx(sh.bar + B_QFULL, bytes * (two ? 4u : 2u));
+            for (int r = 0; r < (two ? 2 : 1); ++r)
                 for (int half = 0; half < 2; ++half)
                     tma_load_3d(smem_u32(sm + SM_Q + r * kTileBytes + half * (kTileBytes / 2)), &p.tm_q,
-                                64 * half, it.h * p.G, it.req.first + it.t0 + r * p.tq, sh.bar + B_QFULL);
+                                64 * half, it.h * p.G, it.first + r * p.tq, sh.bar + B_QFULL);
         }
         ++items;
-        for (int32_t i = 0; ok && i < n; ++i) {
-            const int32_t j0 = it.keys.tile(i) * kTile;
+        for (int32_t i = 0; ok && i < it.n; ++i) {
+            const int32_t j0 = it.key(i);
             // lane = 2 page + half: that page's rows of the tile, 64 channels
             int32_t id = -1;
-            if (lane < 2 * pages) id = it.page(j0 / page + (lane >> 1), p);
+            if (lane < 2 * pages) id = page_of(p, it.row, it.p_max, j0 / page + (lane >> 1));
+            const uint32_t exist = __ballot_sync(0xffffffffu, id >= 0);
             for (int kv = 0; kv < 2; ++kv) {
                 if (loads >= kStages && !(ok = wait(sh, B_KVEMPTY + ring.stage, ring.phase ^ 1, p))) break;
                 const int raw = kv == 1 && it.masked(j0, p) ? 1 : 0;
                 uint64_t *full = sh.bar + (raw ? B_RAW : B_KVFULL) + ring.stage;
                 uses[raw] ^= 1u << ring.stage;
-                if (lane == 0) mbar_arrive_expect_tx(full, kTileBytes);
+                if (lane == 0) {
+                    if (kv == 0) {  // at most three tiles are ahead of a softmax: eight words do
+                        uint32_t bits = 0;
+                        for (int32_t u = 0; u < pages; ++u) bits |= (exist >> (2 * u) & 1) << u;
+                        sh.mapped[tiles & 7] = bits;
+                    }
+                    mbar_arrive_expect_tx(full, kTileBytes);
+                }
                 __syncwarp();
                 if (lane < 2 * pages) {
                     const int32_t y = id < 0 ? p.kv_rows  // out of range: zeros
@@ -200,6 +247,7 @@ __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
                 ring.next();
                 ++loads;
             }
+            ++tiles;
         }
     }
     if (!ok && lane == 0) {  // gave up: the copies in flight still land before the CTA leaves
@@ -234,10 +282,11 @@ __device__ void mma_warp(const Params &p, Shared &sh, unsigned char *sm) {
     uint32_t full_phase = 0, clean_phase = 0;  // bit s: phase of B_KVFULL, B_CLEAN + s
     uint32_t items = 0, p_phase[2] = {0, 0};
     bool ok = true;
-    AttnWalk walk;
+    Items queue;
     Item it;
-    for (int64_t w = blockIdx.x; ok && it.load(p, walk, w); w += gridDim.x) {
-        const int32_t n = it.keys.count();
+    while (ok && queue.next(sh, p, it)) {
+        const int32_t n = it.n;
+        const bool two = it.two(p);
         if (n == 0) continue;
         if (!(ok = wait(sh, B_QFULL, items & 1, p))) break;
         ++items;
@@ -247,7 +296,7 @@ __device__ void mma_warp(const Params &p, Shared &sh, unsigned char *sm) {
         if (lane == 0) {
             mma_scores(tmem, q, kv + ring.stage * kTileBytes, 0);
             mma_commit(sh.bar + B_S);
-            if (it.two) {
+            if (two) {
                 mma_scores(tmem, q, kv + ring.stage * kTileBytes, 1);
                 mma_commit(sh.bar + B_S + 1);
             }
@@ -260,14 +309,14 @@ __device__ void mma_warp(const Params &p, Shared &sh, unsigned char *sm) {
             Ring k = ring;
             k.next();
             const bool more = i + 1 < n;
-            if (it.masked(it.keys.tile(i) * kTile, p)) {
+            if (it.masked(it.key(i), p)) {
                 ok = wait(sh, B_CLEAN + v.stage, clean_phase >> v.stage & 1, p);
                 clean_phase ^= 1u << v.stage;
             } else {
                 ok = wait(sh, B_KVFULL + v.stage, full_phase >> v.stage & 1, p);
                 full_phase ^= 1u << v.stage;
             }
-            for (int r = 0; ok && r < (it.two ? 2 : 1); ++r) {
+            for (int r = 0; ok && r < (two ? 2 : 1); ++r) {
                 if (!(ok = wait(sh, B_P + r, p_phase[r], p))) break;
                 p_phase[r] ^= 1;
                 if (r == 0 && more) {
@@ -278,11 +327,11 @@ __device__ void mma_warp(const Params &p, Shared &sh, unsigned char *sm) {
                 if (lane == 0) {
                     mma_values(tmem, kv + v.stage * kTileBytes, r, i == 0);
                     if (!more) mma_commit(sh.bar + B_O + r);
-                    if (r == 1 || !it.two) mma_commit(sh.bar + B_KVEMPTY + v.stage);
+                    if (r == 1 || !two) mma_commit(sh.bar + B_KVEMPTY + v.stage);
                     if (more) {
                         mma_scores(tmem, q, kv + k.stage * kTileBytes, r);
                         mma_commit(sh.bar + B_S + r);
-                        if (r == 1 || !it.two) {
+                        if (r == 1 || !two) {
                             mma_commit(sh.bar + B_KVEMPTY + k.stage);
                             if (i + 2 == n) mma_commit(sh.bar + B_QEMPTY);
                         }
@@ -312,17 +361,17 @@ __device__ void scrub_warps(const Params &p, Shared &sh, unsigned char *sm) {
     const int t = threadIdx.x - kWarpScrub * 32, lane = t & 31;
     Ring ring;
     uint32_t items = 0, raw_phase = 0;  // bit s: phase of B_RAW + s
-    AttnWalk walk;
+    Items queue;
     Item it;
-    for (int64_t w = blockIdx.x; it.load(p, walk, w); w += gridDim.x) {
-        const int32_t n = it.keys.count();
+    while (queue.next(sh, p, it)) {
+        const int32_t n = it.n;
         if (n == 0) continue;
         ++items;
         for (int32_t i = 0; i < n; ++i) {
             ring.next();  // k
             const Ring v = ring;
             ring.next();
-            const int32_t j0 = it.keys.tile(i) * kTile;
+            const int32_t j0 = it.key(i);
             if (!it.masked(j0, p)) continue;
             if (!wait(sh, B_RAW + v.stage, raw_phase >> v.stage & 1, p)) return;
             raw_phase ^= 1u << v.stage;
@@ -372,7 +421,7 @@ __device__ __noinline__ void attention_row(const Params &p, int64_t q_row, int32
             j = max(j, pos - a.window);  // the gap between the sinks and the window
             continue;
         }
-        const int32_t id = Item::page(p, table_row, pos, j / page);
+        const int32_t id = page_of(p, table_row, pos, j / page);
         if (id < 0) continue;
         const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.kv_pool) + (int64_t)id * 2 * kv_stride +
                                    ((int64_t)h * page + j % page) * kD + 4 * lane;
@@ -397,64 +446,59 @@ __device__ void softmax_warps(const Params &p, Shared &sh, int r) {
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const uint32_t s_tmem = sh.tmem + lanes + 128 * r, o_tmem = sh.tmem + lanes + 256 + 128 * r;
     const WindowAttentionArgs &a = p.a;
-    const int32_t page = a.cache.page_size, pages = kTile / page;
-    uint32_t s_phase = 0, o_phase = 0, items = 0;
-    AttnWalk walk;
+    const int32_t page = a.cache.page_size;
+    const uint32_t all_pages = low_bits(kTile / page);
+    // this row: its token of the item and query head (rows from tq G on are empty)
+    const int32_t token = r * p.tq + row / p.G, g = row % p.G;
+    uint32_t s_phase = 0, o_phase = 0, items = 0, tiles = 0;
+    Items queue;
     Item it;
-    for (int64_t w = blockIdx.x; it.load(p, walk, w); w += gridDim.x) {
-        const int32_t n = it.keys.count();
+    while (queue.next(sh, p, it)) {
+        const int32_t n = it.n;
         if (n > 0) ++items;
-        if (r == 1 && !it.two) continue;
-        // this row's token, and the tile's first and last (rows past the last token see nothing)
-        const int32_t first = it.t0 + r * p.tq, token = first + row / p.G, g = row % p.G;
-        const bool live = row < p.tq * p.G && token < it.req.n;
-        const int32_t p0 = it.req.len - it.req.n;
-        const int32_t pos = live ? p0 + token : -1;
-        const int32_t tile_min = p0 + first, tile_max = p0 + min(first + p.tq, it.req.n) - 1;
+        if (r == 1 && !it.two(p)) {
+            tiles += n;
+            continue;
+        }
+        const bool live = row < p.tq * p.G && token < it.tokens;
+        const int32_t pos = live ? it.p_min + token : -1;  // -1 sees nothing
+        const int32_t tile_min = it.p_min + r * p.tq, tile_max = min(tile_min + p.tq - 1, it.p_max);
         float m = -INFINITY, l = 0.f;
-        for (int32_t i = 0; i < n; ++i) {
-            const int32_t j0 = it.keys.tile(i) * kTile;
-            int32_t id = 0;
-            if (lane < pages) id = it.page(j0 / page + lane, p);
-            const uint32_t mapped = __ballot_sync(0xffffffffu, id >= 0);  // lanes from `pages` on: 1
+        for (int32_t i = 0; i < n; ++i, ++tiles) {
+            const int32_t j0 = it.key(i);
             if (!wait(sh, B_S + r, s_phase, p)) return;
             s_phase ^= 1;
             fence_after_sync();
-            // Two passes over the row's 128 scores, 32 at a time (TMEM is read twice, which costs
-            // less than holding them all): the maximum, then the exponentials.
-            const bool masked = mapped != 0xffffffffu || Item::masked(j0, tile_min, tile_max, p);
-            const int32_t hi = pos - j0 + 1, lo = pos < a.window ? 0 : pos - a.window + 1 - j0;
-            const int32_t sk = a.sinks - j0;
-            auto scores = [&](uint32_t (&s)[32], int c) {
-                if (p.sign <= 0) {  // a negative scale turns the order round; zero weighs all keys alike
+            uint32_t s[4][32];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) s[k] = p.sign < 0 ? s[k] ^ 0x80000000u : 0u;
-                }
-                if (masked) {
+            for (int c = 0; c < 4; ++c) tmem_ld32_async(s_tmem + 32 * c, s[c]);
+            const uint32_t mapped = *reinterpret_cast<volatile uint32_t *>(&sh.mapped[tiles & 7]);
+            const bool masked = mapped != all_pages || Item::masked(j0, tile_min, tile_max, p);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld_wait32(s[c]);
+            if (masked) {
+                const int32_t hi = pos - j0 + 1, lo = pos < a.window ? 0 : pos - a.window + 1 - j0;
+                const int32_t sk = a.sinks - j0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
                     uint32_t bits = low_bits(hi - 32 * c) & (~low_bits(lo - 32 * c) | low_bits(sk - 32 * c));
                     if (page == 16) bits &= (mapped >> (2 * c) & 1 ? 0xffffu : 0u) | (mapped >> (2 * c + 1) & 1 ? 0xffff0000u : 0u);
                     else if (!(mapped >> (32 * c / page) & 1)) bits = 0;
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
-                        if (!(bits >> k & 1)) s[k] = 0xff800000u;  // -inf
+                        if (!(bits >> k & 1)) s[c][k] = 0xff800000u;  // -inf
                 }
-            };
-            uint32_t s[2][32];
-            float now = -INFINITY;
-            tmem_ld32_async(s_tmem, s[0]);
+            }
+            float top[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                tmem_ld_wait32(s[c & 1]);
-                tmem_ld32_async(s_tmem + 32 * ((c + 1) & 3), s[~c & 1]);  // at last the first again
-                scores(s[c & 1], c);
-                float top[2] = {__uint_as_float(s[c & 1][0]), __uint_as_float(s[c & 1][1])};
+                top[c] = __uint_as_float(s[c][0]);
 #pragma unroll
-                for (int k = 2; k < 32; k += 2) {
-                    top[0] = fmaxf(top[0], __uint_as_float(s[c & 1][k]));
-                    top[1] = fmaxf(top[1], __uint_as_float(s[c & 1][k + 1]));
-                }
-                now = fmaxf(now, fmaxf(top[0], top[1]));
+                for (int k = 1; k < 31; k += 2)
+                    top[c] = fmaxf(fmaxf(top[c], __uint_as_float(s[c][k])), __uint_as_float(s[c][k + 1]));
+                top[c] = fmaxf(top[c], __uint_as_float(s[c][31]));
             }
+            const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
             // lazily: only past 2^8 (from -inf at the row's first visible key)
             const bool move = (now - m) * p.c > 8.f;
             if (__any_sync(0xffffffffu, move)) {
@@ -463,14 +507,16 @@ __device__ void softmax_warps(const Params &p, Shared &sh, int r) {
                 l *= f;
                 // s of this tile is complete, so the products issued before it are as well
                 if (i > 0) {
+#pragma unroll 1
+                    for (int c = 0; c < 16; ++c) {
+                        float o[8];
+                        tmem_ld8(o_tmem + 8 * c, o);
+                        uint32_t u[8];
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        float o[16];
-                        tmem_ld16(o_tmem + 16 * c, o);
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] *= f;
-                        tmem_st16(o_tmem + 16 * c, o);
+                        for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(o[k] * f);
+                        tmem_st8u(o_tmem + 8 * c, u);
                     }
+                    tmem_wait_st();
                 }
             }
             const float base = m == -INFINITY ? 0.f : -m * p.c;
@@ -479,20 +525,15 @@ __device__ void softmax_warps(const Params &p, Shared &sh, int r) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 uint32_t out[16];
-                tmem_ld_wait32(s[c & 1]);
-                if (c < 3) tmem_ld32_async(s_tmem + 32 * (c + 1), s[~c & 1]);
-                scores(s[c & 1], c);
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
-                    const float2 x = fma2(make_float2(__uint_as_float(s[c & 1][2 * k]), __uint_as_float(s[c & 1][2 * k + 1])), c2, b2);
+                    const float2 x = fma2(make_float2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), c2, b2);
                     const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-                    if (k & 1) sum2 = fma2(e, make_float2(1.f, 1.f), sum2);
-                    else sum = fma2(e, make_float2(1.f, 1.f), sum);
+                    if (k & 1) sum2 = add2(e, sum2);
+                    else sum = add2(e, sum);
                     const __nv_bfloat162 h = __floats2bfloat162_rn(e.x, e.y);
                     out[k] = *reinterpret_cast<const uint32_t *>(&h);
                 }
-                // p of keys 32 c .. lies over scores 16 c ..: of those, chunk c and (c < 3, in
-                // flight) c + 1 have been read
                 tmem_st16u(s_tmem + 16 * c, out);
             }
             l += (sum.x + sum.y) + (sum2.x + sum2.y);
@@ -512,15 +553,15 @@ __device__ void softmax_warps(const Params &p, Shared &sh, int r) {
         }
         if (tainted) {
             for (int k = 0; k < 32; ++k) {
-                const int32_t rr = 32 * quarter + k, tk = first + rr / p.G;
-                if (rr < p.tq * p.G && tk < it.req.n) 
-                    attention_row(p, (int64_t)(it.req.first + tk) * a.num_q_heads + it.h * p.G + rr % p.G, it.h,
-                                  it.req.row, p0 + tk);
+                const int32_t rr = 32 * quarter + k, tk = r * p.tq + rr / p.G;
+                if (rr < p.tq * p.G && tk < it.tokens)
+                    attention_row(p, (int64_t)(it.first + tk) * a.num_q_heads + it.h * p.G + rr % p.G, it.h, it.row,
+                                  it.p_min + tk);
             }
             continue;
         }
         __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.o) +
-                             ((int64_t)(it.req.first + token) * a.num_q_heads + it.h * p.G + g) * kD;
+                             ((int64_t)(it.first + token) * a.num_q_heads + it.h * p.G + g) * kD;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             float o[32];
@@ -550,7 +591,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < B_COUNT; ++i)
-            mbar_init(sh.bar + i, i >= B_CLEAN && i < B_S ? 2 : i >= B_P && i < B_O ? 4 : 1);
+            mbar_init(sh.bar + i, i >= B_CLEAN && i < B_S ? 2 : i >= B_P && i < B_O ? 4
+                                  : i >= B_ITEMFREE && i < B_DRAIN ? kItemReaders : 1);
         sh.abort = 0;
         for (int i = 0; i < 4; ++i) sh.tainted[i] = 0;
         fence_mbar_init();
@@ -608,8 +650,7 @@ cudaError_t launch_window_attention_tc(const WindowAttentionArgs &a, cudaStream_
     p.G = a.num_q_heads / a.num_kv_heads;
     p.tq = kTile / p.G;
     p.kv_rows = (int32_t)(2ll * a.cache.num_pages * a.num_kv_heads * a.cache.page_size);
-    p.sign = a.scale > 0.f ? 1 : a.scale < 0.f ? -1 : a.scale == 0.f ? 0 : 1;  // NaN: answers NaN
-    p.c = p.sign == 0 ? 1.f : (float)(fabs((double)a.scale) * 1.4426950408889634);
+    p.c = (float)((double)a.scale * 1.4426950408889634);
     auto fn = tensor_map_encoder();
     if (fn == nullptr || !encode_kv_map(&p.tm_kv, a, a.cache.page_size)) return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {kD, (cuuint64_t)a.num_q_heads, (cuuint64_t)a.cache.total_tokens};

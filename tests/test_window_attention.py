@@ -239,6 +239,18 @@ def test_another_stream_and_scale(kda, new):
     check(o, q, c, new, 50, 2, 0.03)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("scale", [-0.09, 0.0, 1e-30, 2.0])
+@pytest.mark.parametrize("new", [[1, 1], [100, 30]])
+def test_any_scale(kda, new, scale, dtype):
+    """A negative scale turns the order of the keys round; zero weighs the visible ones alike."""
+    c = build_cache([n + 60 for n in new], 32, 2, dtype, seed=33)
+    q = queries(sum(new), 4, dtype, 33)
+    if scale == 2.0:
+        q = q * 0.25
+    check(call(kda, q, c, new, 50, 2, scale=scale), q, c, new, 50, 2, scale)
+
+
 def test_no_tokens_and_many_requests(kda):
     c = build_cache([3] * 100, 16, 1, BF16, seed=37)
     q = queries(0, 4, BF16, 37)
