@@ -262,22 +262,28 @@ __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
 // ---------------------------------------------------------------------------
 // MMA
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void mma_scores(uint32_t tmem, uint32_t q, uint32_t k, int r) {
+// One 128-wide product is eight MMAs of 64 cycles each, all issued by one thread: their matrix
+// descriptors differ from the first one's by constants (16-byte units of the address field).
+__device__ __forceinline__ void mma_scores(uint32_t tmem, uint64_t q_desc, uint64_t k_desc, int r) {
 #pragma unroll
-    for (int s = 0; s < kD / 16; ++s)
-        mma_bf16(tmem + 128 * r, sw128_desc_k(q + r * kTileBytes, kTile, s), sw128_desc_k(k, kTile, s),
-                 idesc_bf16_f32(kTile, kTile), s > 0);
+    for (int s = 0; s < kD / 16; ++s) {
+        const uint64_t step = ((s >> 2) * (kTileBytes / 2) + (s & 3) * 32) / 16;
+        mma_bf16(tmem + 128 * r, q_desc + step, k_desc + step, idesc_bf16_f32(kTile, kTile), s > 0);
+    }
 }
-__device__ __forceinline__ void mma_values(uint32_t tmem, uint32_t v, int r, bool first) {
+__device__ __forceinline__ void mma_values(uint32_t tmem, uint64_t v_desc, int r, bool first) {
 #pragma unroll
     for (int s = 0; s < kTile / 16; ++s)
-        mma_bf16_tmem_a(tmem + 256 + 128 * r, tmem + 128 * r + 8 * s, sw128_desc_mn(v + 2048 * s, kTileBytes / 2),
-                        idesc_bf16_f32(kTile, kD) | kIdescBMN, !first || s > 0);
+        mma_bf16_tmem_a(tmem + 256 + 128 * r, tmem + 128 * r + 8 * s, v_desc + s * (2048 / 16),
+                        idesc_bf16_f32(kTile, kD) | kIdescBMN, s > 0 ? 1u : !first);
 }
 
 __device__ void mma_warp(const Params &p, Shared &sh, unsigned char *sm) {
     const int lane = threadIdx.x & 31;
-    const uint32_t tmem = sh.tmem, q = smem_u32(sm + SM_Q), kv = smem_u32(sm + SM_KV);
+    const uint32_t tmem = sh.tmem;
+    const uint64_t q_desc = sw128_desc(smem_u32(sm + SM_Q));
+    const uint64_t k_desc = sw128_desc(smem_u32(sm + SM_KV)), v_desc = sw128_desc_mn(smem_u32(sm + SM_KV), kTileBytes / 2);
+    constexpr uint64_t kTileStep = kTileBytes / 16;
     Ring ring;               // the next tile to be used
     uint32_t full_phase = 0, clean_phase = 0;  // bit s: phase of B_KVFULL, B_CLEAN + s
     uint32_t items = 0, p_phase[2] = {0, 0};
@@ -294,10 +300,10 @@ __device__ void mma_warp(const Params &p, Shared &sh, unsigned char *sm) {
         full_phase ^= 1u << ring.stage;
         fence_after_sync();
         if (lane == 0) {
-            mma_scores(tmem, q, kv + ring.stage * kTileBytes, 0);
+            mma_scores(tmem, q_desc, k_desc + ring.stage * kTileStep, 0);
             mma_commit(sh.bar + B_S);
             if (two) {
-                mma_scores(tmem, q, kv + ring.stage * kTileBytes, 1);
+                mma_scores(tmem, q_desc + kTileStep, k_desc + ring.stage * kTileStep, 1);
                 mma_commit(sh.bar + B_S + 1);
             }
             mma_commit(sh.bar + B_KVEMPTY + ring.stage);
@@ -325,11 +331,11 @@ __device__ void mma_warp(const Params &p, Shared &sh, unsigned char *sm) {
                 }
                 fence_after_sync();
                 if (lane == 0) {
-                    mma_values(tmem, kv + v.stage * kTileBytes, r, i == 0);
+                    mma_values(tmem, v_desc + v.stage * kTileStep, r, i == 0);
                     if (!more) mma_commit(sh.bar + B_O + r);
                     if (r == 1 || !two) mma_commit(sh.bar + B_KVEMPTY + v.stage);
                     if (more) {
-                        mma_scores(tmem, q, kv + k.stage * kTileBytes, r);
+                        mma_scores(tmem, q_desc + r * kTileStep, k_desc + k.stage * kTileStep, r);
                         mma_commit(sh.bar + B_S + r);
                         if (r == 1 || !two) {
                             mma_commit(sh.bar + B_KVEMPTY + k.stage);
