@@ -12,13 +12,13 @@
 // the group) pair, so that the heads of a group share every key and value, and a tile of 128 rows
 // spans only 128 / G tokens: the window's edges then cost few masked tiles.  Keys come in tiles of
 // 128, those of the sinks first.  One CTA per SM stays and takes items in turn.
-//   warp 8      TMA: q of the next item, then k, v tiles page by page into a ring of five 32 KB
+//   warp 8      TMA: q of the next item, then k, v tiles page by page into a ring of four 32 KB
 //               stages (a page that does not exist is an out-of-range box, which reads as zeros)
-//   warp 9      issues the MMAs: s0 = q0 k^T and s1 = q1 k^T into TMEM, o += p v with p read from
+//   warps 9, 10 issue the MMAs of row tiles 0 and 1: s = q k^T into TMEM, o += p v with p read from
 //               TMEM (in place of s).  While one row tile's softmax runs, the tensor core works on
 //               the other's products
 //   warps 0-7   softmax, a thread a row: warps 0-3 tile 0, warps 4-7 tile 1; the epilogue
-//   warps 10-11 values behind a mask: a product with p = 0 would still turn NaN or infinity into
+//   warp 11     values behind a mask: a product with p = 0 would still turn NaN or infinity into
 //               NaN, so tiles that some row must not see are gone through first: keys that no row
 //               sees are cleared, and a non-finite value of any other key marks the item, whose
 //               rows are then computed again one by one, each from its visible keys alone.
@@ -41,7 +41,7 @@ constexpr uint32_t kTileBytes = kTile * kD * 2;
 constexpr int kStages = 5;
 constexpr int kItems = 4;                     // work items announced ahead
 constexpr int kItemReaders = 11;              // warps that read them: softmax, MMA, values
-constexpr int kWarpTma = 8, kWarpMma = 9, kWarpScrub = 10;
+constexpr int kWarpTma = 8, kWarpMma = 9, kWarpScrub = 11;
 constexpr uint64_t kWaitNs = 2000000000ull;
 // 384 threads start with 168 registers; the softmax warps take 208, the others keep 88:
 // 256 * 208 + 128 * 88 = 384 * 168
@@ -50,11 +50,12 @@ constexpr int kRegsSoftmax = 208, kRegsOther = 88;
 enum Bar {
     B_QFULL, B_QEMPTY, B_KVFULL, B_RAW = B_KVFULL + kStages, B_KVEMPTY = B_RAW + kStages,
     B_CLEAN = B_KVEMPTY + kStages,
-    B_S = B_CLEAN + kStages, B_P = B_S + 2, B_O = B_P + 2, B_ITEM = B_O + 2, B_ITEMFREE = B_ITEM + kItems,
-    B_DRAIN = B_ITEMFREE + kItems, B_COUNT
+    B_S = B_CLEAN + kStages, B_P = B_S + 2, B_O = B_P + 4, B_ITEM = B_O + 2, B_ITEMFREE = B_ITEM + kItems,
+    B_DRAIN = B_ITEMFREE + kItems, B_TURN = B_DRAIN + 2, B_COUNT = B_TURN + 2
 };
 
-constexpr uint32_t SM_Q = 0, SM_KV = 2 * kTileBytes, SM_END = SM_KV + kStages * kTileBytes;
+constexpr uint32_t SM_Q = 0, SM_KV = 2 * kTileBytes, SM_OUT = SM_KV + kStages * kTileBytes,
+                   SM_END = SM_OUT;  // SM_OUT: 4 KB a softmax warp
 constexpr size_t SM_DYN = SM_END + 1024;  // the start is rounded up to 1024 bytes
 
 struct Params {
@@ -62,6 +63,7 @@ struct Params {
     CUtensorMap tm_kv;  // [2 P Hkv page_size][128], boxes of a page x 64 channels
     WindowAttentionArgs a;
     int32_t G, tq;      // query heads a kv head, tokens of a row tile
+    uint32_t inv_g;     // ceil(2^16 / G): x / G = x inv_g >> 16 for x < 128
     int32_t kv_rows;    // 2 P Hkv page_size
     float c;            // scale log2 e, > 0
 };
@@ -144,12 +146,12 @@ struct Ring {
 struct Items {
     uint32_t k = 0;
     // The next item; false after the last one or when a wait gave up.
-    __device__ __forceinline__ bool next(Shared &sh, const Params &p, Item &it) {
+    __device__ __forceinline__ bool next(Shared &sh, const Params &p, Item &it, bool one_thread = false) {
         const uint32_t slot = k % kItems;
         if (!wait(sh, B_ITEM + slot, k / kItems & 1, p)) return false;
         it = sh.items[slot];
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(sh.bar + B_ITEMFREE + slot);
+        if (!one_thread) __syncwarp();
+        if (one_thread || (threadIdx.x & 31) == 0) mbar_arrive(sh.bar + B_ITEMFREE + slot);
         ++k;
         return it.n >= 0;
     }
@@ -264,95 +266,107 @@ __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
 // ---------------------------------------------------------------------------
 // One 128-wide product is eight MMAs of 64 cycles each, all issued by one thread: their matrix
 // descriptors differ from the first one's by constants (16-byte units of the address field).
-__device__ __forceinline__ void mma_scores(uint32_t tmem, uint64_t q_desc, uint64_t k_desc, int r) {
+__device__ __forceinline__ void mma_scores(uint32_t tmem, uint64_t q_desc, uint64_t k_desc, int r, int from, int to) {
 #pragma unroll
-    for (int s = 0; s < kD / 16; ++s) {
+    for (int s = from; s < to; ++s) {
         const uint64_t step = ((s >> 2) * (kTileBytes / 2) + (s & 3) * 32) / 16;
         mma_bf16(tmem + 128 * r, q_desc + step, k_desc + step, idesc_bf16_f32(kTile, kTile), s > 0);
     }
 }
-__device__ __forceinline__ void mma_values(uint32_t tmem, uint64_t v_desc, int r, bool first) {
+// Keys 64 half .. 64 half + 63 of a tile.
+__device__ __forceinline__ void mma_values(uint32_t tmem, uint64_t v_desc, int r, int half, bool first) {
 #pragma unroll
-    for (int s = 0; s < kTile / 16; ++s)
+    for (int s = 4 * half; s < 4 * half + 4; ++s)
         mma_bf16_tmem_a(tmem + 256 + 128 * r, tmem + 128 * r + 8 * s, v_desc + s * (2048 / 16),
                         idesc_bf16_f32(kTile, kD) | kIdescBMN, s > 0 ? 1u : !first);
 }
 
-__device__ void mma_warp(const Params &p, Shared &sh, unsigned char *sm) {
-    const int lane = threadIdx.x & 31;
+// Row tile r's products, by one thread.  The tensor core runs them as they are issued, so what a
+// thread does between two products (waits, bookkeeping) is hidden by the other row tile's thread.
+// The two take turns, a tile's p v and the next one's q k^T at a time: left to interleave, both
+// row tiles would wait for their products at once (2.03 ms for the 2 x 16384-token chunk at window
+// 4096, against 1.52).  The turn passes kPass MMAs into the second product, about the 250 cycles
+// ahead that the other thread takes to see it (all 8 done: 1.63 ms, none: 1.65).
+constexpr int kPass = 5;
+__device__ void mma_thread(const Params &p, Shared &sh, unsigned char *sm, int r) {
     const uint32_t tmem = sh.tmem;
-    const uint64_t q_desc = sw128_desc(smem_u32(sm + SM_Q));
+    const uint64_t q_desc = sw128_desc(smem_u32(sm + SM_Q + r * kTileBytes));
     const uint64_t k_desc = sw128_desc(smem_u32(sm + SM_KV)), v_desc = sw128_desc_mn(smem_u32(sm + SM_KV), kTileBytes / 2);
     constexpr uint64_t kTileStep = kTileBytes / 16;
-    Ring ring;               // the next tile to be used
+    Ring ring;                                 // the next tile to be used
     uint32_t full_phase = 0, clean_phase = 0;  // bit s: phase of B_KVFULL, B_CLEAN + s
-    uint32_t items = 0, p_phase[2] = {0, 0};
+    uint32_t items = 0, p_phase = 0;
     bool ok = true;
+    // frees what both threads use: by this one's products, or at once when it has none
+    const auto release = [&](int bar, bool two) {
+        if (r == 0 || two) mma_commit(sh.bar + bar);
+        else mbar_arrive(sh.bar + bar);
+    };
+    const auto full = [&](int stage) {
+        const uint32_t phase = full_phase >> stage & 1;
+        full_phase ^= 1u << stage;
+        return wait(sh, B_KVFULL + stage, phase, p);
+    };
+    uint32_t turns = 0;
+    const auto turn = [&] { return wait(sh, B_TURN + r, (turns++ + 1 + r) & 1, p); };  // row tile 0 begins
     Items queue;
     Item it;
-    while (ok && queue.next(sh, p, it)) {
+    while (ok && queue.next(sh, p, it, true)) {
         const int32_t n = it.n;
-        const bool two = it.two(p);
+        const bool two = it.two(p), mine = r == 0 || two;
         if (n == 0) continue;
-        if (!(ok = wait(sh, B_QFULL, items & 1, p))) break;
+        if (!(ok = wait(sh, B_QFULL, items & 1, p) && full(ring.stage))) break;
         ++items;
-        if (!(ok = wait(sh, B_KVFULL + ring.stage, full_phase >> ring.stage & 1, p))) break;
-        full_phase ^= 1u << ring.stage;
         fence_after_sync();
-        if (lane == 0) {
-            mma_scores(tmem, q_desc, k_desc + ring.stage * kTileStep, 0);
-            mma_commit(sh.bar + B_S);
-            if (two) {
-                mma_scores(tmem, q_desc + kTileStep, k_desc + ring.stage * kTileStep, 1);
-                mma_commit(sh.bar + B_S + 1);
-            }
-            mma_commit(sh.bar + B_KVEMPTY + ring.stage);
-            if (n == 1) mma_commit(sh.bar + B_QEMPTY);
+        if (mine) {
+            if (two && !(ok = turn())) break;
+            mma_scores(tmem, q_desc, k_desc + ring.stage * kTileStep, r, 0, kD / 16);
+            mma_commit(sh.bar + B_S + r);
+            if (two) mbar_arrive(sh.bar + B_TURN + 1 - r);
         }
+        release(B_KVEMPTY + ring.stage, two);
+        if (n == 1) release(B_QEMPTY, two);
         ring.next();
         for (int32_t i = 0; i < n; ++i) {
-            const Ring v = ring;
-            Ring k = ring;
-            k.next();
+            const int v = ring.stage;
+            ring.next();
+            const int k = ring.stage;
             const bool more = i + 1 < n;
             if (it.masked(it.key(i), p)) {
-                ok = wait(sh, B_CLEAN + v.stage, clean_phase >> v.stage & 1, p);
-                clean_phase ^= 1u << v.stage;
+                ok = wait(sh, B_CLEAN + v, clean_phase >> v & 1, p);
+                clean_phase ^= 1u << v;
             } else {
-                ok = wait(sh, B_KVFULL + v.stage, full_phase >> v.stage & 1, p);
-                full_phase ^= 1u << v.stage;
+                ok = full(v);
             }
-            for (int r = 0; ok && r < (two ? 2 : 1); ++r) {
-                if (!(ok = wait(sh, B_P + r, p_phase[r], p))) break;
-                p_phase[r] ^= 1;
-                if (r == 0 && more) {
-                    if (!(ok = wait(sh, B_KVFULL + k.stage, full_phase >> k.stage & 1, p))) break;
-                    full_phase ^= 1u << k.stage;
-                }
+            if (!ok || (more && !(ok = full(k)))) break;
+            if (mine) {
+                if (two && !(ok = turn())) break;
+                if (!(ok = wait(sh, B_P + 2 * r, p_phase, p))) break;
                 fence_after_sync();
-                if (lane == 0) {
-                    mma_values(tmem, v_desc + v.stage * kTileStep, r, i == 0);
-                    if (!more) mma_commit(sh.bar + B_O + r);
-                    if (r == 1 || !two) mma_commit(sh.bar + B_KVEMPTY + v.stage);
-                    if (more) {
-                        mma_scores(tmem, q_desc + r * kTileStep, k_desc + k.stage * kTileStep, r);
-                        mma_commit(sh.bar + B_S + r);
-                        if (r == 1 || !two) {
-                            mma_commit(sh.bar + B_KVEMPTY + k.stage);
-                            if (i + 2 == n) mma_commit(sh.bar + B_QEMPTY);
-                        }
-                    }
+                mma_values(tmem, v_desc + v * kTileStep, r, 0, i == 0);
+                if (!(ok = wait(sh, B_P + 2 * r + 1, p_phase, p))) break;
+                p_phase ^= 1;
+                fence_after_sync();
+                mma_values(tmem, v_desc + v * kTileStep, r, 1, false);
+                if (!more) mma_commit(sh.bar + B_O + r);
+                if (more) mma_scores(tmem, q_desc, k_desc + k * kTileStep, r, 0, kPass);
+                if (two) mbar_arrive(sh.bar + B_TURN + 1 - r);
+                if (more) {
+                    mma_scores(tmem, q_desc, k_desc + k * kTileStep, r, kPass, kD / 16);
+                    mma_commit(sh.bar + B_S + r);
                 }
-                __syncwarp();
             }
-            if (!ok) break;
-            ring.next();
-            if (more) ring.next();
+            release(B_KVEMPTY + v, two);
+            if (more) {
+                release(B_KVEMPTY + k, two);
+                if (i + 2 == n) release(B_QEMPTY, two);
+                ring.next();
+            }
         }
     }
-    if (!ok && lane == 0) {  // gave up: the MMAs in flight finish before TMEM is freed
-        mma_commit(sh.bar + B_DRAIN);
-        mbar_wait_bounded(sh.bar + B_DRAIN, 0, kWaitNs);
+    if (!ok) {  // gave up: the MMAs in flight finish before TMEM is freed
+        mma_commit(sh.bar + B_DRAIN + r);
+        mbar_wait_bounded(sh.bar + B_DRAIN + r, 0, kWaitNs);
     }
 }
 
@@ -363,8 +377,8 @@ __device__ __forceinline__ uint32_t any_nonfinite(uint32_t x) {
     return ((x & 0x7f80u) == 0x7f80u) | ((x & 0x7f800000u) == 0x7f800000u);
 }
 
-__device__ void scrub_warps(const Params &p, Shared &sh, unsigned char *sm) {
-    const int t = threadIdx.x - kWarpScrub * 32, lane = t & 31;
+__device__ void scrub_warp(const Params &p, Shared &sh, unsigned char *sm) {
+    const int t = threadIdx.x & 31;
     Ring ring;
     uint32_t items = 0, raw_phase = 0;  // bit s: phase of B_RAW + s
     Items queue;
@@ -383,22 +397,30 @@ __device__ void scrub_warps(const Params &p, Shared &sh, unsigned char *sm) {
             raw_phase ^= 1u << v.stage;
             unsigned char *tile = sm + SM_KV + v.stage * kTileBytes;
             uint32_t bad = 0;
-#pragma unroll 4
-            for (int c = t; c < (int)kTileBytes / 16; c += 64) {  // 16-byte chunk c of the tile
-                const int32_t j = j0 + ((c >> 3) & (kTile - 1));  // its key
-                uint4 *x = reinterpret_cast<uint4 *>(tile + 16 * c);
-                // seen by some row: not past the last token, and within its first token's reach
-                if (j <= it.p_max && (it.p_min - j < p.a.window || j < p.a.sinks)) {
-                    const uint4 y = *x;
-                    bad |= any_nonfinite(y.x) | any_nonfinite(y.y) | any_nonfinite(y.z) | any_nonfinite(y.w);
-                } else {
-                    *x = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+            for (int key = t; key < kTile; key += 32) {
+                const int32_t j = j0 + key;
+                const bool sink = j < p.a.sinks;
+                if (j <= it.p_min && (sink || it.p_max - j < p.a.window)) continue;  // every row sees it
+                // some row sees it: not past the last token, and within the first token's reach
+                const bool seen = j <= it.p_max && (sink || it.p_min - j < p.a.window);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {  // its 16-byte chunks, apart in the banks from lane to lane
+                    uint4 *x = reinterpret_cast<uint4 *>(tile + (c >> 3) * (kTileBytes / 2) + 128 * key +
+                                                         16 * ((c ^ key) & 7));
+                    if (seen) {
+                        const uint4 y = *x;
+                        bad |= any_nonfinite(y.x) | any_nonfinite(y.y) | any_nonfinite(y.z) | any_nonfinite(y.w);
+                    } else {
+                        *x = make_uint4(0, 0, 0, 0);
+                    }
                 }
             }
+            __syncwarp();
             if (bad) *reinterpret_cast<volatile uint32_t *>(&sh.tainted[items & 3]) = items;
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(sh.bar + B_CLEAN + v.stage);
+            if (t == 0) mbar_arrive(sh.bar + B_CLEAN + v.stage);
         }
     }
 }
@@ -409,6 +431,16 @@ __device__ void scrub_warps(const Params &p, Shared &sh, unsigned char *sm) {
 // The lowest n bits.
 __device__ __forceinline__ uint32_t low_bits(int32_t n) {
     return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+__device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
+    float a = __uint_as_float(s[0]), b = __uint_as_float(s[1]);
+#pragma unroll
+    for (int k = 2; k < 30; k += 4) {
+        a = fmaxf(fmaxf(a, __uint_as_float(s[k])), __uint_as_float(s[k + 1]));
+        b = fmaxf(fmaxf(b, __uint_as_float(s[k + 2])), __uint_as_float(s[k + 3]));
+    }
+    return fmaxf(fmaxf(a, b), fmaxf(__uint_as_float(s[30]), __uint_as_float(s[31])));
 }
 
 // One row from its visible keys alone, fp32 throughout; a warp a row, four channels a lane.  Runs
@@ -446,16 +478,17 @@ __device__ __noinline__ void attention_row(const Params &p, int64_t q_row, int32
     store4(static_cast<__nv_bfloat16 *>(a.o) + row, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
 }
 
-__device__ void softmax_warps(const Params &p, Shared &sh, int r) {
+__device__ void softmax_warps(const Params &p, Shared &sh, unsigned char *sm, int r) {
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
     const int row = 32 * quarter + lane;  // of the row tile
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const uint32_t s_tmem = sh.tmem + lanes + 128 * r, o_tmem = sh.tmem + lanes + 256 + 128 * r;
     const WindowAttentionArgs &a = p.a;
     const int32_t page = a.cache.page_size;
+    unsigned char *stage = sm + SM_OUT + 4096 * (threadIdx.x >> 5);
     const uint32_t all_pages = low_bits(kTile / page);
     // this row: its token of the item and query head (rows from tq G on are empty)
-    const int32_t token = r * p.tq + row / p.G, g = row % p.G;
+    const int32_t token = r * p.tq + row / p.G;
     uint32_t s_phase = 0, o_phase = 0, items = 0, tiles = 0;
     Items queue;
     Item it;
@@ -476,12 +509,21 @@ __device__ void softmax_warps(const Params &p, Shared &sh, int r) {
             s_phase ^= 1;
             fence_after_sync();
             uint32_t s[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32_async(s_tmem + 32 * c, s[c]);
+            float top[4];
+            tmem_ld32_async(s_tmem, s[0]);
+            tmem_ld32_async(s_tmem + 32, s[1]);
             const uint32_t mapped = *reinterpret_cast<volatile uint32_t *>(&sh.mapped[tiles & 7]);
             const bool masked = mapped != all_pages || Item::masked(j0, tile_min, tile_max, p);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld_wait32(s[c]);
+            tmem_ld_wait32(s[0]);
+            tmem_ld_wait32(s[1]);
+            tmem_ld32_async(s_tmem + 64, s[2]);
+            tmem_ld32_async(s_tmem + 96, s[3]);
+            if (!masked) {
+                top[0] = max32(s[0]);
+                top[1] = max32(s[1]);
+            }
+            tmem_ld_wait32(s[2]);
+            tmem_ld_wait32(s[3]);
             if (masked) {
                 const int32_t hi = pos - j0 + 1, lo = pos < a.window ? 0 : pos - a.window + 1 - j0;
                 const int32_t sk = a.sinks - j0;
@@ -490,20 +532,18 @@ __device__ void softmax_warps(const Params &p, Shared &sh, int r) {
                     uint32_t bits = low_bits(hi - 32 * c) & (~low_bits(lo - 32 * c) | low_bits(sk - 32 * c));
                     if (page == 16) bits &= (mapped >> (2 * c) & 1 ? 0xffffu : 0u) | (mapped >> (2 * c + 1) & 1 ? 0xffff0000u : 0u);
                     else if (!(mapped >> (32 * c / page) & 1)) bits = 0;
+                    if (__all_sync(0xffffffffu, bits == 0xffffffffu)) continue;  // most chunks of an edge tile
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
                         if (!(bits >> k & 1)) s[c][k] = 0xff800000u;  // -inf
                 }
             }
-            float top[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                top[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-                for (int k = 1; k < 31; k += 2)
-                    top[c] = fmaxf(fmaxf(top[c], __uint_as_float(s[c][k])), __uint_as_float(s[c][k + 1]));
-                top[c] = fmaxf(top[c], __uint_as_float(s[c][31]));
+            if (masked) {
+                top[0] = max32(s[0]);
+                top[1] = max32(s[1]);
             }
+            top[2] = max32(s[2]);
+            top[3] = max32(s[3]);
             const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
             // lazily: only past 2^8 (from -inf at the row's first visible key)
             const bool move = (now - m) * p.c > 8.f;
@@ -541,12 +581,14 @@ __device__ void softmax_warps(const Params &p, Shared &sh, int r) {
                     out[k] = *reinterpret_cast<const uint32_t *>(&h);
                 }
                 tmem_st16u(s_tmem + 16 * c, out);
+                if (c & 1) {  // half of p is there: its products may start
+                    tmem_wait_st();
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sh.bar + B_P + 2 * r + (c >> 1));
+                }
             }
             l += (sum.x + sum.y) + (sum2.x + sum2.y);
-            tmem_wait_st();
-            fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(sh.bar + B_P + r);
         }
 
         const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -566,6 +608,7 @@ __device__ void softmax_warps(const Params &p, Shared &sh, int r) {
             }
             continue;
         }
+        const int32_t g = row % p.G;
         __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.o) +
                              ((int64_t)(it.first + token) * a.num_q_heads + it.h * p.G + g) * kD;
 #pragma unroll
@@ -597,8 +640,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < B_COUNT; ++i)
-            mbar_init(sh.bar + i, i >= B_CLEAN && i < B_S ? 2 : i >= B_P && i < B_O ? 4
-                                  : i >= B_ITEMFREE && i < B_DRAIN ? kItemReaders : 1);
+            mbar_init(sh.bar + i, i == B_QEMPTY || (i >= B_KVEMPTY && i < B_CLEAN) ? 2
+                                  : i >= B_P && i < B_O                             ? 4
+                                  : i >= B_ITEMFREE && i < B_DRAIN                  ? kItemReaders
+                                                                                    : 1);
         sh.abort = 0;
         for (int i = 0; i < 4; ++i) sh.tainted[i] = 0;
         fence_mbar_init();
@@ -612,12 +657,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
     fence_after_sync();
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-        softmax_warps(p, sh, warp >> 2);
+        softmax_warps(p, sh, sm, warp >> 2);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         if (warp == kWarpTma) tma_warp(p, sh, sm);
-        else if (warp == kWarpMma) mma_warp(p, sh, sm);
-        else scrub_warps(p, sh, sm);
+        else if (warp == kWarpScrub) scrub_warp(p, sh, sm);
+        else if ((threadIdx.x & 31) == 0) mma_thread(p, sh, sm, warp - kWarpMma);
     }
     __syncthreads();
     if (warp == kWarpMma) tmem_dealloc(sh.tmem, 512);
@@ -655,6 +700,7 @@ cudaError_t launch_window_attention_tc(const WindowAttentionArgs &a, cudaStream_
     p.a = a;
     p.G = a.num_q_heads / a.num_kv_heads;
     p.tq = kTile / p.G;
+    p.inv_g = (65536u + p.G - 1) / p.G;
     p.kv_rows = (int32_t)(2ll * a.cache.num_pages * a.num_kv_heads * a.cache.page_size);
     p.c = (float)((double)a.scale * 1.4426950408889634);
     auto fn = tensor_map_encoder();
