@@ -12,7 +12,7 @@
 // the group) pair, so that the heads of a group share every key and value, and a tile of 128 rows
 // spans only 128 / G tokens: the window's edges then cost few masked tiles.  Keys come in tiles of
 // 128, those of the sinks first.  One CTA per SM stays and takes items in turn.
-//   warp 8      TMA: q of the next item, then k, v tiles page by page into a ring of four 32 KB
+//   warp 8      TMA: q of the next item, then k, v tiles page by page into a ring of five 32 KB
 //               stages (a page that does not exist is an out-of-range box, which reads as zeros)
 //   warps 9, 10 issue the MMAs of row tiles 0 and 1: s = q k^T into TMEM, o += p v with p read from
 //               TMEM (in place of s).  While one row tile's softmax runs, the tensor core works on
@@ -21,7 +21,7 @@
 //   warp 11     values behind a mask: a product with p = 0 would still turn NaN or infinity into
 //               NaN, so tiles that some row must not see are gone through first: keys that no row
 //               sees are cleared, and a non-finite value of any other key marks the item, whose
-//               rows are then computed again one by one, each from its visible keys alone.
+//               rows are at the end computed again one by one, each from its visible keys alone.
 // TMEM: s0, s1, o0, o1 of 128 columns each.  Bound: the tensor core (two 128 x 128 x 128 products
 // a key tile and row tile).
 #include <cuda.h>
@@ -40,6 +40,7 @@ constexpr int kTile = 128;                    // rows of a row tile, keys of a k
 constexpr uint32_t kTileBytes = kTile * kD * 2;
 constexpr int kStages = 5;
 constexpr int kItems = 4;                     // work items announced ahead
+constexpr int kTaintWords = 32;
 constexpr int kItemReaders = 11;              // warps that read them: softmax, MMA, values
 constexpr int kWarpTma = 8, kWarpMma = 9, kWarpScrub = 11;
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -54,8 +55,7 @@ enum Bar {
     B_DRAIN = B_ITEMFREE + kItems, B_TURN = B_DRAIN + 2, B_COUNT = B_TURN + 2
 };
 
-constexpr uint32_t SM_Q = 0, SM_KV = 2 * kTileBytes, SM_OUT = SM_KV + kStages * kTileBytes,
-                   SM_END = SM_OUT;  // SM_OUT: 4 KB a softmax warp
+constexpr uint32_t SM_Q = 0, SM_KV = 2 * kTileBytes, SM_END = SM_KV + kStages * kTileBytes;
 constexpr size_t SM_DYN = SM_END + 1024;  // the start is rounded up to 1024 bytes
 
 struct Params {
@@ -105,9 +105,10 @@ struct Item {
 struct Shared {
     uint64_t bar[B_COUNT];
     Item items[kItems];
-    uint32_t mapped[8];   // by key tile % 8: bit i: the tile's page i exists
-    uint32_t tainted[4];  // by item % 4 (at most two are ahead of an epilogue): the number, from 1, of an
-                          // item whose masked tiles held a non-finite value
+    int2 tiles[8];  // by key tile % 8: its first key; bit i: its page i exists, bit 16 + r: some row of row tile r
+                    // must not see some key of it
+    uint32_t tainted[kTaintWords + 1];  // bit k: masked tiles of item k held a non-finite value (the last
+                                        // word: of an item past those)
     uint32_t tmem;
     uint32_t abort;
 };
@@ -145,16 +146,15 @@ struct Ring {
 // The items in turn, for the warps that read them.
 struct Items {
     uint32_t k = 0;
-    // The next item; false after the last one or when a wait gave up.
-    __device__ __forceinline__ bool next(Shared &sh, const Params &p, Item &it, bool one_thread = false) {
+    // The next item, in its place until done(); null after the last one or when a wait gave up.
+    __device__ __forceinline__ const Item *next(Shared &sh, const Params &p) {
         const uint32_t slot = k % kItems;
-        if (!wait(sh, B_ITEM + slot, k / kItems & 1, p)) return false;
-        it = sh.items[slot];
-        if (!one_thread) __syncwarp();
-        if (one_thread || (threadIdx.x & 31) == 0) mbar_arrive(sh.bar + B_ITEMFREE + slot);
+        if (!wait(sh, B_ITEM + slot, k / kItems & 1, p)) return nullptr;
         ++k;
-        return it.n >= 0;
+        return sh.items[slot].n >= 0 ? &sh.items[slot] : nullptr;
     }
+    // By one thread of the warp, which has read all it wants.
+    __device__ __forceinline__ void done(Shared &sh) { mbar_arrive(sh.bar + B_ITEMFREE + (k - 1) % kItems); }
 };
 
 // ---------------------------------------------------------------------------
@@ -193,6 +193,7 @@ __device__ __forceinline__ int32_t page_of(const Params &p, int32_t row, int32_t
 __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
     const int lane = threadIdx.x & 31;
     const int32_t page = p.a.cache.page_size, pages = kTile / page;  // pages of a tile
+    const uint32_t all_pages = (1u << pages) - 1u;
     Ring ring;
     uint32_t loads = 0, items = 0, tiles = 0, uses[2] = {0, 0};  // bit s: parity of the uses of KVFULL, RAW + s
     bool ok = true;
@@ -209,16 +210,18 @@ __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
         if (it.n < 0) break;
         if (it.n == 0) continue;
         const bool two = it.two(p);
-        if (items > 0 && !(ok = wait(sh, B_QEMPTY, (items - 1) & 1, p))) break;
-        if (lane == 0) {
+        const auto load_q = [&] {  // when the last item's scores are done
+            if (items > 0 && !wait(sh, B_QEMPTY, (items - 1) & 1, p)) return false;
+            ++items;
+            if (lane != 0) return true;
             const uint32_t bytes = (uint32_t)(p.tq * p.G * 64 * 2);
             mbar_arrive_expect_tx(sh.bar + B_QFULL, bytes * (two ? 4u : 2u));
             for (int r = 0; r < (two ? 2 : 1); ++r)
                 for (int half = 0; half < 2; ++half)
                     tma_load_3d(smem_u32(sm + SM_Q + r * kTileBytes + half * (kTileBytes / 2)), &p.tm_q,
                                 64 * half, it.h * p.G, it.first + r * p.tq, sh.bar + B_QFULL);
-        }
-        ++items;
+            return true;
+        };
         for (int32_t i = 0; ok && i < it.n; ++i) {
             const int32_t j0 = it.key(i);
             // lane = 2 page + half: that page's rows of the tile, 64 channels
@@ -231,10 +234,14 @@ __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
                 uint64_t *full = sh.bar + (raw ? B_RAW : B_KVFULL) + ring.stage;
                 uses[raw] ^= 1u << ring.stage;
                 if (lane == 0) {
-                    if (kv == 0) {  // at most three tiles are ahead of a softmax: eight words do
+                    if (kv == 0) {  // at most three tiles are ahead of a softmax: eight places do
                         uint32_t bits = 0;
                         for (int32_t u = 0; u < pages; ++u) bits |= (exist >> (2 * u) & 1) << u;
-                        sh.mapped[tiles & 7] = bits;
+                        for (int32_t r = 0; r < 2; ++r) {
+                            const int32_t lo = it.p_min + r * p.tq, hi = min(lo + p.tq - 1, it.p_max);
+                            if (bits != all_pages || Item::masked(j0, lo, hi, p)) bits |= 0x10000u << r;
+                        }
+                        sh.tiles[tiles & 7] = make_int2(j0, (int)bits);
                     }
                     mbar_arrive_expect_tx(full, kTileBytes);
                 }
@@ -248,6 +255,7 @@ __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
                 }
                 ring.next();
                 ++loads;
+                if (i == 0 && kv == 0 && !(ok = load_q())) break;  // q behind the first keys
             }
             ++tiles;
         }
@@ -310,8 +318,11 @@ __device__ void mma_thread(const Params &p, Shared &sh, unsigned char *sm, int r
     uint32_t turns = 0;
     const auto turn = [&] { return wait(sh, B_TURN + r, (turns++ + 1 + r) & 1, p); };  // row tile 0 begins
     Items queue;
-    Item it;
-    while (ok && queue.next(sh, p, it, true)) {
+    while (ok) {
+        const Item *at = queue.next(sh, p);
+        if (at == nullptr) break;
+        const Item it = *at;
+        queue.done(sh);
         const int32_t n = it.n;
         const bool two = it.two(p), mine = r == 0 || two;
         if (n == 0) continue;
@@ -380,14 +391,13 @@ __device__ __forceinline__ uint32_t any_nonfinite(uint32_t x) {
 __device__ void scrub_warp(const Params &p, Shared &sh, unsigned char *sm) {
     const int t = threadIdx.x & 31;
     Ring ring;
-    uint32_t items = 0, raw_phase = 0;  // bit s: phase of B_RAW + s
+    uint32_t raw_phase = 0;  // bit s: phase of B_RAW + s
     Items queue;
-    Item it;
-    while (queue.next(sh, p, it)) {
-        const int32_t n = it.n;
-        if (n == 0) continue;
-        ++items;
-        for (int32_t i = 0; i < n; ++i) {
+    while (const Item *at = queue.next(sh, p)) {
+        const Item it = *at;
+        __syncwarp();
+        if (t == 0) queue.done(sh);
+        for (int32_t i = 0; i < it.n; ++i) {
             ring.next();  // k
             const Ring v = ring;
             ring.next();
@@ -417,7 +427,10 @@ __device__ void scrub_warp(const Params &p, Shared &sh, unsigned char *sm) {
                 }
             }
             __syncwarp();
-            if (bad) *reinterpret_cast<volatile uint32_t *>(&sh.tainted[items & 3]) = items;
+            if (bad) {
+                const uint32_t k = queue.k - 1;
+                atomicOr(&sh.tainted[min(k / 32, (uint32_t)kTaintWords)], 1u << (k & 31));
+            }
             fence_proxy_async_smem();
             __syncwarp();
             if (t == 0) mbar_arrive(sh.bar + B_CLEAN + v.stage);
@@ -445,7 +458,7 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
 
 // One row from its visible keys alone, fp32 throughout; a warp a row, four channels a lane.  Runs
 // only when a masked tile held a non-finite value.
-__device__ __noinline__ void attention_row(const Params &p, int64_t q_row, int32_t h, int32_t table_row, int32_t pos) {
+__device__ void attention_row(const Params &p, int64_t q_row, int32_t h, int32_t table_row, int32_t pos) {
     const int lane = threadIdx.x & 31;
     const WindowAttentionArgs &a = p.a;
     const int32_t page = a.cache.page_size;
@@ -478,33 +491,78 @@ __device__ __noinline__ void attention_row(const Params &p, int64_t q_row, int32
     store4(static_cast<__nv_bfloat16 *>(a.o) + row, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
 }
 
-__device__ void softmax_warps(const Params &p, Shared &sh, unsigned char *sm, int r) {
+// Writes a row tile's outputs.  Four lanes (rows) exchange 16-byte chunks so that each store covers
+// 64 contiguous bytes of eight rows; a row a thread, the 32 lines of every store kept the load/store
+// unit busy for 4,000 cycles an item.
+__device__ __forceinline__ void store_rows(const Params &p, uint32_t o_tmem, bool any, float l, __nv_bfloat16 *o_item,
+                                           int32_t token0, int32_t tokens) {
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __nv_bfloat16 *out = o_item + 8 * (lane & 3);
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {  // 32 channels: chunks 0 .. 3
+        uint32_t x[4][4];
+        {
+            uint32_t o[32];
+            if (any) {
+                tmem_ld32_async(o_tmem + 32 * c, o);
+                tmem_ld_wait32(o);
+            }
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                const __nv_bfloat162 h =
+                    __floats2bfloat162_rn(__uint_as_float(o[2 * u]) * inv, __uint_as_float(o[2 * u + 1]) * inv);
+                // no key: 0, whatever o holds (a NaN sum stays one)
+                x[u >> 2][u & 3] = l == 0.f ? 0u : *reinterpret_cast<const uint32_t *>(&h);
+            }
+        }
+#pragma unroll
+        for (int bit = 2; bit > 0; bit >>= 1)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (!(u & bit)) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const bool upper = lane & bit;
+                        const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? x[u][k] : x[u ^ bit][k], bit);
+                        if (upper) x[u][k] = got;
+                        else x[u ^ bit][k] = got;
+                    }
+                }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {  // chunk lane % 4 of row 4 (lane / 4) + u
+            const int rt = 32 * quarter + (lane & ~3) + u;
+            const int tk = (int)((uint32_t)rt * p.inv_g >> 16), tt = token0 + tk;
+            if (tk < p.tq && tt < tokens)
+                *reinterpret_cast<uint4 *>(out + ((int64_t)tt * p.a.num_q_heads + rt - tk * p.G) * kD + 32 * c) =
+                    make_uint4(x[u][0], x[u][1], x[u][2], x[u][3]);
+        }
+    }
+}
+
+__device__ void softmax_warps(const Params &p, Shared &sh, int r) {
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
     const int row = 32 * quarter + lane;  // of the row tile
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const uint32_t s_tmem = sh.tmem + lanes + 128 * r, o_tmem = sh.tmem + lanes + 256 + 128 * r;
     const WindowAttentionArgs &a = p.a;
     const int32_t page = a.cache.page_size;
-    unsigned char *stage = sm + SM_OUT + 4096 * (threadIdx.x >> 5);
-    const uint32_t all_pages = low_bits(kTile / page);
     // this row: its token of the item and query head (rows from tq G on are empty)
     const int32_t token = r * p.tq + row / p.G;
-    uint32_t s_phase = 0, o_phase = 0, items = 0, tiles = 0;
+    uint32_t s_phase = 0, o_phase = 0, tiles = 0;
     Items queue;
-    Item it;
-    while (queue.next(sh, p, it)) {
-        const int32_t n = it.n;
-        if (n > 0) ++items;
-        if (r == 1 && !it.two(p)) {
+    while (const Item *it = queue.next(sh, p)) {
+        const int32_t n = it->n;
+        if (r == 1 && !it->two(p)) {
             tiles += n;
+            __syncwarp();
+            if (lane == 0) queue.done(sh);
             continue;
         }
-        const bool live = row < p.tq * p.G && token < it.tokens;
-        const int32_t pos = live ? it.p_min + token : -1;  // -1 sees nothing
-        const int32_t tile_min = it.p_min + r * p.tq, tile_max = min(tile_min + p.tq - 1, it.p_max);
+        // the row's index (-1 sees nothing)
+        const int32_t pos = row < p.tq * p.G && token < it->tokens ? it->p_min + token : -1;
         float m = -INFINITY, l = 0.f;
         for (int32_t i = 0; i < n; ++i, ++tiles) {
-            const int32_t j0 = it.key(i);
             if (!wait(sh, B_S + r, s_phase, p)) return;
             s_phase ^= 1;
             fence_after_sync();
@@ -512,8 +570,8 @@ __device__ void softmax_warps(const Params &p, Shared &sh, unsigned char *sm, in
             float top[4];
             tmem_ld32_async(s_tmem, s[0]);
             tmem_ld32_async(s_tmem + 32, s[1]);
-            const uint32_t mapped = *reinterpret_cast<volatile uint32_t *>(&sh.mapped[tiles & 7]);
-            const bool masked = mapped != all_pages || Item::masked(j0, tile_min, tile_max, p);
+            const uint32_t mapped = *reinterpret_cast<volatile uint32_t *>(&sh.tiles[tiles & 7].y);
+            const bool masked = mapped & 0x10000u << r;
             tmem_ld_wait32(s[0]);
             tmem_ld_wait32(s[1]);
             tmem_ld32_async(s_tmem + 64, s[2]);
@@ -525,6 +583,7 @@ __device__ void softmax_warps(const Params &p, Shared &sh, unsigned char *sm, in
             tmem_ld_wait32(s[2]);
             tmem_ld_wait32(s[3]);
             if (masked) {
+                const int32_t j0 = *reinterpret_cast<volatile int32_t *>(&sh.tiles[tiles & 7].x);
                 const int32_t hi = pos - j0 + 1, lo = pos < a.window ? 0 : pos - a.window + 1 - j0;
                 const int32_t sk = a.sinks - j0;
 #pragma unroll
@@ -591,45 +650,31 @@ __device__ void softmax_warps(const Params &p, Shared &sh, unsigned char *sm, in
             l += (sum.x + sum.y) + (sum2.x + sum2.y);
         }
 
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        bool tainted = false;
         if (n > 0) {
             if (!wait(sh, B_O + r, o_phase, p)) return;
             o_phase ^= 1;
             fence_after_sync();
-            tainted = *reinterpret_cast<volatile uint32_t *>(&sh.tainted[items & 3]) == items;
         }
-        if (tainted) {
-            for (int k = 0; k < 32; ++k) {
-                const int32_t rr = 32 * quarter + k, tk = r * p.tq + rr / p.G;
-                if (rr < p.tq * p.G && tk < it.tokens)
-                    attention_row(p, (int64_t)(it.first + tk) * a.num_q_heads + it.h * p.G + rr % p.G, it.h, it.row,
-                                  it.p_min + tk);
-            }
-            continue;
-        }
-        const int32_t g = row % p.G;
-        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.o) +
-                             ((int64_t)(it.first + token) * a.num_q_heads + it.h * p.G + g) * kD;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            float o[32];
-            if (n > 0) tmem_ld32(o_tmem + 32 * c, o);
-#pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-                uint4 x = make_uint4(0, 0, 0, 0);
-                uint32_t *y = &x.x;
-                if (l != 0.f) {  // (a NaN sum stays one)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(o[k + 2 * u] * inv, o[k + 2 * u + 1] * inv);
-                        y[u] = *reinterpret_cast<const uint32_t *>(&h);
-                    }
-                }
-                if (live) *reinterpret_cast<uint4 *>(dst + 32 * c + k) = x;
-            }
-        }
+        store_rows(p, o_tmem, n > 0, l, static_cast<__nv_bfloat16 *>(a.o) + ((int64_t)it->first * a.num_q_heads + it->h * p.G) * kD,
+                   r * p.tq, it->tokens);
+        if (lane == 0) queue.done(sh);
         fence_before_sync();  // the next item's products write o after this row tile's next p
+    }
+}
+
+// The rows of this CTA's marked items again, by all warps.
+__device__ __noinline__ void redo_tainted(const Params &p, const Shared &sh, int warp) {
+    AttnWalk walk;
+    AttnRequest req;
+    for (uint32_t k = 0;; ++k) {
+        const Item it = find_item(p, walk, blockIdx.x + (int64_t)k * gridDim.x, req);
+        if (it.n < 0) return;
+        const bool marked = k < 32 * kTaintWords ? sh.tainted[k / 32] >> (k & 31) & 1 : sh.tainted[kTaintWords] != 0;
+        for (int32_t row = warp; marked && row < it.tokens * p.G; row += kThreads / 32) {
+            const int32_t token = row / p.G;
+            attention_row(p, (int64_t)(it.first + token) * p.a.num_q_heads + it.h * p.G + row % p.G, it.h, it.row,
+                          it.p_min + token);
+        }
     }
 }
 
@@ -645,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                                   : i >= B_ITEMFREE && i < B_DRAIN                  ? kItemReaders
                                                                                     : 1);
         sh.abort = 0;
-        for (int i = 0; i < 4; ++i) sh.tainted[i] = 0;
+        for (int i = 0; i <= kTaintWords; ++i) sh.tainted[i] = 0;
         fence_mbar_init();
     }
     if (warp == kWarpMma) {
@@ -657,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
     fence_after_sync();
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-        softmax_warps(p, sh, sm, warp >> 2);
+        softmax_warps(p, sh, warp >> 2);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         if (warp == kWarpTma) tma_warp(p, sh, sm);
@@ -666,6 +711,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
     }
     __syncthreads();
     if (warp == kWarpMma) tmem_dealloc(sh.tmem, 512);
+    uint32_t any = 0;
+    for (int i = 0; i <= kTaintWords; ++i) any |= sh.tainted[i];
+    if (any != 0) redo_tainted(p, sh, warp);  // after every store of the first pass
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
