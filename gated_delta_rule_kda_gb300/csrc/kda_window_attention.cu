@@ -199,7 +199,12 @@ cudaError_t launch_window_attention(const WindowAttentionArgs &a, cudaStream_t s
     // The tensor-core kernel keeps its running maximum on unscaled scores, in the order that a
     // positive scale leaves alone; any other scale (and fp32) runs on the FMA units.
     const bool tensor = a.dtype == KDA_BF16 && a.scale > 0.f && a.scale <= FLT_MAX;
-    return tensor ? launch_window_attention_tc(a, stream) : launch_window_attention_rows(a, stream);
+    if (!tensor) return launch_window_attention_rows(a, stream);
+    // Up to 64 rows a request and kv head fit the split kernel (which wants them in one grid of
+    // at most 65535 requests); more make a 128-row tile worth its while.
+    const int64_t rows = (int64_t)a.max_tokens * (a.num_q_heads / a.num_kv_heads);
+    return rows <= 64 && a.cache.batch <= 65535 ? launch_window_attention_split(a, stream)
+                                                : launch_window_attention_tc(a, stream);
 }
 
 }  // namespace kda

@@ -2,6 +2,8 @@
 // tokens of a work item can see.
 #pragma once
 
+#include <cuda.h>
+
 #include "kda_common.cuh"
 
 namespace kda {
@@ -93,7 +95,63 @@ __device__ __forceinline__ bool attn_visible(int32_t p, int32_t j, int32_t windo
     return j <= p && (p - j < window || j < sinks);
 }
 
+// Page i of a row of the table, or -1 where there is none or it starts past index `last`.
+__device__ __forceinline__ int32_t attn_page(const CacheArgs &c, int32_t row, int32_t last, int32_t i) {
+    if (i >= c.table_width || i * c.page_size > last) return -1;
+    const int32_t id = c.page_table[(int64_t)row * c.table_width + i];
+    return (uint32_t)id < (uint32_t)c.num_pages ? id : -1;
+}
+
+// Whether either of two packed bf16 values is an infinity or NaN.
+__device__ __forceinline__ uint32_t any_nonfinite(uint32_t x) {
+    return ((x & 0x7f80u) == 0x7f80u) | ((x & 0x7f800000u) == 0x7f800000u);
+}
+
+// The lowest n bits.
+__device__ __forceinline__ uint32_t low_bits(int32_t n) {
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// One row (query q_row of [T][Hq], index pos) from its visible keys alone, fp32 throughout; a warp a
+// row, four channels a lane.  Runs only where a masked tile held a non-finite value.
+__device__ __noinline__ inline void attn_row(const WindowAttentionArgs &a, int64_t q_row, int32_t h,
+                                             int32_t table_row, int32_t pos) {
+    const int lane = threadIdx.x & 31;
+    const int32_t page = a.cache.page_size;
+    const int64_t row = q_row * kD + 4 * lane;
+    const float4 q = load4(static_cast<const __nv_bfloat16 *>(a.q) + row);
+    const int64_t kv_stride = (int64_t)a.num_kv_heads * page * kD;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = -INFINITY, l = 0.f;
+    for (int32_t j = 0; j <= pos; ++j) {
+        if (!attn_visible(pos, j, a.window, a.sinks)) {
+            j = max(j, pos - a.window);  // the gap between the sinks and the window
+            continue;
+        }
+        const int32_t id = attn_page(a.cache, table_row, pos, j / page);
+        if (id < 0) continue;
+        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.kv_pool) + (int64_t)id * 2 * kv_stride +
+                                   ((int64_t)h * page + j % page) * kD + 4 * lane;
+        const float4 k = load4(src), v = load4(src + kv_stride);
+        float s = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        s *= a.scale;
+        const float top = fmaxf(m, s), keep = top == -INFINITY ? 1.f : expf(m - top);
+        const float e = s == -INFINITY ? 0.f : expf(s - top);  // (a NaN score stays one)
+        l = l * keep + e;
+        o = make_float4(o.x * keep + e * v.x, o.y * keep + e * v.y, o.z * keep + e * v.z, o.w * keep + e * v.w);
+        m = top;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    store4(static_cast<__nv_bfloat16 *>(a.o) + row, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+}
+
 cudaError_t launch_window_attention_rows(const WindowAttentionArgs &a, cudaStream_t stream);
 cudaError_t launch_window_attention_tc(const WindowAttentionArgs &a, cudaStream_t stream);
+cudaError_t launch_window_attention_split(const WindowAttentionArgs &a, cudaStream_t stream);
+
+// A tensor map over kv_pool as rows of 128 channels, 64 channels x box_rows a box, 128-byte swizzle.
+bool encode_kv_map(CUtensorMap *m, const WindowAttentionArgs &a, int32_t box_rows);
 
 }  // namespace kda

@@ -182,14 +182,6 @@ __device__ __forceinline__ Item find_item(const Params &p, AttnWalk &walk, int64
     return it;
 }
 
-// Page i of a row, or -1 where there is none or it starts past index `last`.
-__device__ __forceinline__ int32_t page_of(const Params &p, int32_t row, int32_t last, int32_t i) {
-    const CacheArgs &c = p.a.cache;
-    if (i >= c.table_width || i * c.page_size > last) return -1;
-    const int32_t id = c.page_table[(int64_t)row * c.table_width + i];
-    return (uint32_t)id < (uint32_t)c.num_pages ? id : -1;
-}
-
 __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
     const int lane = threadIdx.x & 31;
     const int32_t page = p.a.cache.page_size, pages = kTile / page;  // pages of a tile
@@ -226,7 +218,7 @@ __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
             const int32_t j0 = it.key(i);
             // lane = 2 page + half: that page's rows of the tile, 64 channels
             int32_t id = -1;
-            if (lane < 2 * pages) id = page_of(p, it.row, it.p_max, j0 / page + (lane >> 1));
+            if (lane < 2 * pages) id = attn_page(p.a.cache, it.row, it.p_max, j0 / page + (lane >> 1));
             const uint32_t exist = __ballot_sync(0xffffffffu, id >= 0);
             for (int kv = 0; kv < 2; ++kv) {
                 if (loads >= kStages && !(ok = wait(sh, B_KVEMPTY + ring.stage, ring.phase ^ 1, p))) break;
@@ -384,10 +376,6 @@ __device__ void mma_thread(const Params &p, Shared &sh, unsigned char *sm, int r
 // ---------------------------------------------------------------------------
 // Values behind a mask
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t any_nonfinite(uint32_t x) {
-    return ((x & 0x7f80u) == 0x7f80u) | ((x & 0x7f800000u) == 0x7f800000u);
-}
-
 __device__ void scrub_warp(const Params &p, Shared &sh, unsigned char *sm) {
     const int t = threadIdx.x & 31;
     Ring ring;
@@ -441,11 +429,6 @@ __device__ void scrub_warp(const Params &p, Shared &sh, unsigned char *sm) {
 // ---------------------------------------------------------------------------
 // Softmax and epilogue
 // ---------------------------------------------------------------------------
-// The lowest n bits.
-__device__ __forceinline__ uint32_t low_bits(int32_t n) {
-    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
-}
-
 __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
     float a = __uint_as_float(s[0]), b = __uint_as_float(s[1]);
 #pragma unroll
@@ -454,41 +437,6 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
         b = fmaxf(fmaxf(b, __uint_as_float(s[k + 2])), __uint_as_float(s[k + 3]));
     }
     return fmaxf(fmaxf(a, b), fmaxf(__uint_as_float(s[30]), __uint_as_float(s[31])));
-}
-
-// One row from its visible keys alone, fp32 throughout; a warp a row, four channels a lane.  Runs
-// only when a masked tile held a non-finite value.
-__device__ void attention_row(const Params &p, int64_t q_row, int32_t h, int32_t table_row, int32_t pos) {
-    const int lane = threadIdx.x & 31;
-    const WindowAttentionArgs &a = p.a;
-    const int32_t page = a.cache.page_size;
-    const int64_t row = q_row * kD + 4 * lane;
-    const float4 q = load4(static_cast<const __nv_bfloat16 *>(a.q) + row);
-    const int64_t kv_stride = (int64_t)a.num_kv_heads * page * kD;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float m = -INFINITY, l = 0.f;
-    for (int32_t j = 0; j <= pos; ++j) {
-        if (!attn_visible(pos, j, a.window, a.sinks)) {
-            j = max(j, pos - a.window);  // the gap between the sinks and the window
-            continue;
-        }
-        const int32_t id = page_of(p, table_row, pos, j / page);
-        if (id < 0) continue;
-        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.kv_pool) + (int64_t)id * 2 * kv_stride +
-                                   ((int64_t)h * page + j % page) * kD + 4 * lane;
-        const float4 k = load4(src), v = load4(src + kv_stride);
-        float s = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s *= a.scale;
-        const float top = fmaxf(m, s), keep = top == -INFINITY ? 1.f : expf(m - top);
-        const float e = top == -INFINITY ? 0.f : expf(s - top);
-        l = l * keep + e;
-        o = make_float4(o.x * keep + e * v.x, o.y * keep + e * v.y, o.z * keep + e * v.z, o.w * keep + e * v.w);
-        m = top;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    store4(static_cast<__nv_bfloat16 *>(a.o) + row, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
 }
 
 // Writes a row tile's outputs.  Four lanes (rows) exchange 16-byte chunks so that each store covers
@@ -672,7 +620,7 @@ __device__ __noinline__ void redo_tainted(const Params &p, const Shared &sh, int
         const bool marked = k < 32 * kTaintWords ? sh.tainted[k / 32] >> (k & 31) & 1 : sh.tainted[kTaintWords] != 0;
         for (int32_t row = warp; marked && row < it.tokens * p.G; row += kThreads / 32) {
             const int32_t token = row / p.G;
-            attention_row(p, (int64_t)(it.first + token) * p.a.num_q_heads + it.h * p.G + row % p.G, it.h, it.row,
+            attn_row(p.a, (int64_t)(it.first + token) * p.a.num_q_heads + it.h * p.G + row % p.G, it.h, it.row,
                           it.p_min + token);
         }
     }
