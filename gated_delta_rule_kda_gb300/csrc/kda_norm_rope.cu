@@ -2,12 +2,13 @@
 //
 //   y = x / sqrt(mean(x^2) + eps) * w;  (a, b) -> (a c - b s, b c + a s) for each rotated pair
 //
-// HBM-bound: every element is read once and written once, about eight operations each.  A group
-// of 16 lanes takes kRows head rows of one token, eight channels a lane (16-byte accesses in
-// bf16): the sum of squares is four shuffles, and the token's cosines and sines stay in registers
-// for the group's rows.  rotary_dim is a multiple of 16, so with half-split pairs channel c of
-// lane l meets channel c of one other lane (a shuffle); interleaved pairs lie within a lane.
-// The rows of a token are its query heads, its key heads, and with a cache its value heads.
+// HBM-bound: every element is read once and written once, about eight operations each.  A group of
+// 16 lanes takes up to kRows head rows of one token and kind (query, key or value), so that the
+// token's cosines and sines, the weights and the place in the cache are fetched once for all of
+// them, and the rows' loads are in flight together.  A lane holds two pieces of four channels, at
+// ca and cb: with half-split pairs the pieces are the two halves of four pairs (channel i and
+// i + rotary_dim / 2), with interleaved pairs they are neighbours; either way both channels of a
+// pair are in one lane, and the channels that do not rotate fall to the lanes past rotary_dim / 8.
 #include "kda_common.cuh"
 
 namespace kda {
@@ -15,38 +16,21 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kGroup = 16;  // lanes of a head row
-constexpr int kRows = 4;    // head rows of a group
-constexpr int kVec = kD / kGroup;
+constexpr int kRows = 8;    // head rows of a group
+constexpr int kBatch = 4;   // rows whose loads are in flight together
 
-__device__ __forceinline__ void load8(const float *p, float (&x)[kVec]) {
-    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p));
-    const float4 b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+__device__ __forceinline__ float4 load_piece(const float *p) {
+    return __ldcs(reinterpret_cast<const float4 *>(p));
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[kVec]) {
-    const uint4 r = __ldcs(reinterpret_cast<const uint4 *>(p));
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+__device__ __forceinline__ float4 load_piece(const __nv_bfloat16 *p) {
+    const uint2 r = __ldcs(reinterpret_cast<const uint2 *>(p));
+    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
+                       __uint_as_float(r.y & 0xffff0000u));
 }
-__device__ __forceinline__ void store8(float *p, const float (&x)[kVec]) {
-    store4(p, make_float4(x[0], x[1], x[2], x[3]));
-    store4(p + 4, make_float4(x[4], x[5], x[6], x[7]));
+__device__ __forceinline__ float4 mul4(float4 x, float4 y) {
+    return make_float4(x.x * y.x, x.y * y.y, x.z * y.z, x.w * y.w);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[kVec]) {
-    uint4 r;
-    uint32_t *w = &r.x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-    *reinterpret_cast<uint4 *>(p) = r;
-}
+__device__ __forceinline__ float dot4(float4 x) { return x.x * x.x + x.y * x.y + x.z * x.z + x.w * x.w; }
 
 // Where the keys of token t go: the page and the place in it, or page -1.
 struct Place {
@@ -70,125 +54,124 @@ __device__ __forceinline__ Place place_of(const CacheArgs &c, int32_t t) {
 }
 
 template <typename Tin, typename Tout, bool kAppend, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs a, int32_t chunks) {
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs a, uint32_t q_chunks, uint32_t kv_chunks) {
     const int lane = threadIdx.x & (kGroup - 1);
-    const int64_t group = (int64_t)blockIdx.x * (kThreads / kGroup) + threadIdx.x / kGroup;
-    const int32_t T = a.cache.total_tokens, Hq = a.num_q_heads, Hkv = a.num_kv_heads;
-    const int32_t rows = Hq + (kAppend ? 2 : 1) * Hkv;
-    const bool in = group < (int64_t)T * chunks;  // every lane stays for the shuffles
-    const int32_t t = in ? (int32_t)(group / chunks) : 0;
-    const int32_t r0 = in ? (int32_t)(group % chunks) * kRows : rows;
-
-    float x[kRows][kVec];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int32_t r = r0 + i;
-        if (r < rows) {
-            const Tin *src = r < Hq ? static_cast<const Tin *>(a.q) + t * a.q_stride + (int64_t)r * kD
-                             : r < Hq + Hkv
-                                 ? static_cast<const Tin *>(a.k) + t * a.k_stride + (int64_t)(r - Hq) * kD
-                                 : static_cast<const Tin *>(a.v) + t * a.v_stride + (int64_t)(r - Hq - Hkv) * kD;
-            load8(src + lane * kVec, x[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) x[i][j] = 0.f;
-        }
+    const uint32_t group = blockIdx.x * (kThreads / kGroup) + threadIdx.x / kGroup;
+    const uint32_t per_token = q_chunks + (kAppend ? 2 : 1) * kv_chunks;
+    const uint32_t token = group / per_token;
+    uint32_t chunk = group - token * per_token;
+    const bool in = token < (uint32_t)a.cache.total_tokens;  // the others stay for the shuffles
+    const int32_t t = in ? (int32_t)token : 0;
+    // the kind of this group's rows: 0 queries, 1 keys, 2 values
+    int kind = 0;
+    if (chunk >= q_chunks) {
+        chunk -= q_chunks;
+        kind = chunk >= kv_chunks ? 2 : 1;
+        if (kind == 2) chunk -= kv_chunks;
     }
+    const int32_t heads = kind == 0 ? a.num_q_heads : a.num_kv_heads, h0 = (int32_t)chunk * kRows;
+    const int32_t rows = in ? min(kRows, heads - h0) : 0;
 
-    // this lane's pairs: cosines and sines of channels 8 lane .. 8 lane + 7
-    const int32_t half_lanes = a.rotary_dim / (2 * kVec);  // lanes of the first elements (half-split)
-    const bool rotated = lane < 2 * half_lanes;
-    float c[kInterleaved ? kVec / 2 : kVec], s[kInterleaved ? kVec / 2 : kVec];
+    const int32_t turning = a.rotary_dim / 8;  // lanes with channels to rotate
+    const bool rotated = kind != 2 && lane < turning;
+    int32_t ca = 8 * lane, cb = 8 * lane + 4;
+    if (!kInterleaved && lane < turning) {
+        ca = 4 * lane;
+        cb = a.rotary_dim / 2 + 4 * lane;
+    }
+    const Tin *src = static_cast<const Tin *>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
+                     t * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) + (int64_t)h0 * kD;
+
+    float4 cs0 = make_float4(1.f, 0.f, 1.f, 0.f), cs1 = cs0;  // (c, s) of this lane's four pairs
+    float4 wa = make_float4(1.f, 1.f, 1.f, 1.f), wb = wa;
     bool ok = in;
     if (in && a.rotary_dim > 0) {
         const int32_t pos = a.positions[t];
         ok = (uint32_t)pos < (uint32_t)a.num_positions;
-        if (!ok && lane == 0 && r0 == 0) record_status(a.status, KDA_ERR_DEVICE_CHECK, (uint32_t)t);
+        if (!ok && lane == 0) record_status(a.status, KDA_ERR_DEVICE_CHECK, (uint32_t)t);
         if (ok && rotated) {
-            constexpr int n = kInterleaved ? kVec / 2 : kVec;
-            const int32_t first = kInterleaved ? lane * n : (lane < half_lanes ? lane : lane - half_lanes) * n;
-            const float4 *cs = reinterpret_cast<const float4 *>(
-                a.rope_table + ((int64_t)pos * (a.rotary_dim / 2) + first) * 2);
-#pragma unroll
-            for (int i = 0; i < n / 2; ++i) {
-                const float4 y = cs[i];
-                c[2 * i] = y.x; s[2 * i] = y.y;
-                c[2 * i + 1] = y.z; s[2 * i + 1] = y.w;
-            }
+            const float4 *cs = reinterpret_cast<const float4 *>(a.rope_table + ((int64_t)pos * (a.rotary_dim / 2) + 4 * lane) * 2);
+            cs0 = cs[0];
+            cs1 = cs[1];
         }
     }
-    Place place{-1, 0};
-    if (kAppend && in && r0 + kRows > Hq) {
-        place = place_of(a.cache, t);
-        if (place.page < 0 && lane == 0) record_status(a.status, KDA_ERR_DEVICE_CHECK, (uint32_t)t);
+    const float *w = kind == 0 ? a.q_weight : a.k_weight;
+    const bool norm = a.norm && kind != 2;
+    if (norm && w != nullptr) {
+        wa = load4(w + ca);
+        wb = load4(w + cb);
+    }
+    Tout *dst;
+    int64_t pitch = kD;  // from head to head
+    if (kind == 0) {
+        dst = static_cast<Tout *>(a.q_out) + ((int64_t)t * a.num_q_heads + h0) * kD;
+    } else if (!kAppend) {
+        dst = static_cast<Tout *>(a.k_out) + ((int64_t)t * a.num_kv_heads + h0) * kD;
+    } else {
+        const Place place = in ? place_of(a.cache, t) : Place{-1, 0};
+        if (in && place.page < 0) {
+            ok = false;
+            if (lane == 0) record_status(a.status, KDA_ERR_DEVICE_CHECK, (uint32_t)t);
+        }
+        pitch = (int64_t)a.cache.page_size * kD;
+        dst = static_cast<Tout *>(a.kv_pool) + (((int64_t)max(place.page, 0) * 2 + kind - 1) * a.num_kv_heads + h0) * pitch +
+              (int64_t)place.at * kD;
     }
 
-    const int partner = lane < half_lanes ? lane + half_lanes : lane - half_lanes;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int32_t r = r0 + i;
-        const bool value = kAppend && r >= Hq + Hkv;
-        if (a.norm) {  // a kernel argument: the same for every lane
-            float ss = 0.f;
+    for (int b = 0; b < kRows; b += kBatch) {
+        float4 xa[kBatch], xb[kBatch];
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) ss = fmaf(x[i][j], x[i][j], ss);
+        for (int i = 0; i < kBatch; ++i) {
+            xa[i] = xb[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (b + i < rows) {
+                xa[i] = load_piece(src + (b + i) * kD + ca);
+                xb[i] = load_piece(src + (b + i) * kD + cb);
+            }
+        }
 #pragma unroll
-            for (int off = kGroup / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-            if (!value) {
-                const float inv = 1.f / sqrtf(ss * (1.f / kD) + a.eps);
-                const float *w = r < Hq ? a.q_weight : a.k_weight;
-                if (w != nullptr) {
-                    const float4 w0 = load4(w + lane * kVec), w1 = load4(w + lane * kVec + 4);
-                    const float wv[kVec] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        for (int i = 0; i < kBatch; ++i) {
+            float inv = 1.f;
+            if (a.norm) {  // a kernel argument: the same for every lane
+                float ss = dot4(xa[i]) + dot4(xb[i]);
 #pragma unroll
-                    for (int j = 0; j < kVec; ++j) x[i][j] = x[i][j] * inv * wv[j];
+                for (int off = kGroup / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+                if (norm) inv = rsqrtf(ss * (1.f / kD) + a.eps);
+            }
+            if (kind != 2) {
+                const float4 u = mul4(xa[i], make_float4(inv * wa.x, inv * wa.y, inv * wa.z, inv * wa.w));
+                const float4 v = mul4(xb[i], make_float4(inv * wb.x, inv * wb.y, inv * wb.z, inv * wb.w));
+                if (kInterleaved) {
+                    xa[i] = make_float4(u.x * cs0.x - u.y * cs0.y, u.y * cs0.x + u.x * cs0.y,
+                                        u.z * cs0.z - u.w * cs0.w, u.w * cs0.z + u.z * cs0.w);
+                    xb[i] = make_float4(v.x * cs1.x - v.y * cs1.y, v.y * cs1.x + v.x * cs1.y,
+                                        v.z * cs1.z - v.w * cs1.w, v.w * cs1.z + v.z * cs1.w);
                 } else {
-#pragma unroll
-                    for (int j = 0; j < kVec; ++j) x[i][j] *= inv;
+                    xa[i] = make_float4(u.x * cs0.x - v.x * cs0.y, u.y * cs0.z - v.y * cs0.w,
+                                        u.z * cs1.x - v.z * cs1.y, u.w * cs1.z - v.w * cs1.w);
+                    xb[i] = make_float4(v.x * cs0.x + u.x * cs0.y, v.y * cs0.z + u.y * cs0.w,
+                                        v.z * cs1.x + u.z * cs1.y, v.w * cs1.z + u.w * cs1.w);
+                }
+                if (!rotated) {  // 1 and 0 would turn an infinity into NaN
+                    xa[i] = u;
+                    xb[i] = v;
                 }
             }
-        }
-        if (kInterleaved) {
-            if (rotated && !value) {
-#pragma unroll
-                for (int j = 0; j < kVec / 2; ++j) {
-                    const float u = x[i][2 * j], v = x[i][2 * j + 1];
-                    x[i][2 * j] = u * c[j] - v * s[j];
-                    x[i][2 * j + 1] = v * c[j] + u * s[j];
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                const float other = __shfl_sync(0xffffffffu, x[i][j], partner & (kGroup - 1), kGroup);
-                if (rotated && !value)
-                    x[i][j] = lane < half_lanes ? x[i][j] * c[j] - other * s[j] : x[i][j] * c[j] + other * s[j];
+            if (ok && b + i < rows) {
+                store4(dst + (b + i) * pitch + ca, xa[i]);
+                store4(dst + (b + i) * pitch + cb, xb[i]);
             }
         }
-        if (!ok || r >= rows) continue;  // no shuffle of this row is left
-        Tout *dst;
-        if (r < Hq) {
-            dst = static_cast<Tout *>(a.q_out) + ((int64_t)t * Hq + r) * kD;
-        } else if (kAppend) {
-            if (place.page < 0) continue;
-            const int32_t kv = value ? 1 : 0, h = r - Hq - kv * Hkv;
-            dst = static_cast<Tout *>(a.kv_pool) +
-                  ((((int64_t)place.page * 2 + kv) * Hkv + h) * a.cache.page_size + place.at) * kD;
-        } else {
-            dst = static_cast<Tout *>(a.k_out) + ((int64_t)t * Hkv + (r - Hq)) * kD;
-        }
-        store8(dst + lane * kVec, x[i]);
     }
 }
 
 template <typename Tin, typename Tout, bool kAppend>
 cudaError_t launch(const NormRopeArgs &a, cudaStream_t stream) {
-    const int32_t rows = a.num_q_heads + (kAppend ? 2 : 1) * a.num_kv_heads;
-    const int32_t chunks = (rows + kRows - 1) / kRows;
-    const int64_t groups = (int64_t)a.cache.total_tokens * chunks;
+    const uint32_t q_chunks = (a.num_q_heads + kRows - 1) / kRows, kv_chunks = (a.num_kv_heads + kRows - 1) / kRows;
+    const int64_t groups = (int64_t)a.cache.total_tokens * (q_chunks + (kAppend ? 2 : 1) * kv_chunks);
     const unsigned grid = (unsigned)((groups + kThreads / kGroup - 1) / (kThreads / kGroup));
-    if (a.interleaved) norm_rope_kernel<Tin, Tout, kAppend, true><<<grid, kThreads, 0, stream>>>(a, chunks);
-    else norm_rope_kernel<Tin, Tout, kAppend, false><<<grid, kThreads, 0, stream>>>(a, chunks);
+    if (a.interleaved) norm_rope_kernel<Tin, Tout, kAppend, true><<<grid, kThreads, 0, stream>>>(a, q_chunks, kv_chunks);
+    else norm_rope_kernel<Tin, Tout, kAppend, false><<<grid, kThreads, 0, stream>>>(a, q_chunks, kv_chunks);
     return cudaGetLastError();
 }
 template <typename Tin, typename Tout>

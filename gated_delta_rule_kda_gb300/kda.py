@@ -548,16 +548,22 @@ def rope_table(num_positions: int, rotary_dim: int = HEAD_DIM, base: float = 100
     return torch.stack([angle.cos(), angle.sin()], -1).mul_(magnitude).float().contiguous()
 
 
-def _i32(t: Optional[torch.Tensor]):
-    if t is not None and t.dtype != torch.int32:
-        raise TypeError(f"expected int32, got {t.dtype}")
-    return _p(t)
+# Marshalling of the calls below: plain integers for pointers, and the raw current stream (a few
+# microseconds less a call than stream and pointer objects, which is what a decode step waits for).
+def _ptr(t: Optional[torch.Tensor], dtype: Optional[torch.dtype] = None):
+    if t is None:
+        return None
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"expected {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
 
 
-def _f32(t: Optional[torch.Tensor]):
-    if t is not None and t.dtype != torch.float32:
-        raise TypeError(f"expected float32, got {t.dtype}")
-    return _p(t)
+def _raw_stream(stream, t: torch.Tensor):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else None
 
 
 def _heads(t: torch.Tensor, dtype: torch.dtype):
@@ -568,14 +574,15 @@ def _heads(t: torch.Tensor, dtype: torch.dtype):
     s = t.stride()
     if d != HEAD_DIM or s[2] != 1 or (H > 1 and s[1] != HEAD_DIM):
         raise ValueError("the heads of a token must lie side by side, 128 channels each")
-    return ctypes.c_void_p(t.data_ptr()), (s[0] if T > 1 else H * HEAD_DIM)
+    return t.data_ptr(), (s[0] if T > 1 else H * HEAD_DIM)
 
 
 def _pool_shape(kv_pool):
     """(pages, kv heads, page_size) of a cache pool [P, 2, Hkv, page_size, 128]."""
-    if kv_pool.dim() != 5 or kv_pool.shape[1] != 2 or kv_pool.shape[4] != HEAD_DIM:
+    shape = kv_pool.shape
+    if len(shape) != 5 or shape[1] != 2 or shape[4] != HEAD_DIM:
         raise ValueError("kv_pool must be [pages, 2, kv heads, page_size, 128]")
-    return kv_pool.shape[0], kv_pool.shape[2], kv_pool.shape[3]
+    return shape[0], shape[2], shape[3]
 
 
 def _rope_args(rope, positions, T):
@@ -583,7 +590,7 @@ def _rope_args(rope, positions, T):
         return None, 0, 0, None
     if positions.numel() != T:
         raise ValueError("positions must have one entry per token")
-    return _f32(rope), rope.shape[0], 2 * rope.shape[1], _i32(positions)
+    return _ptr(rope, torch.float32), rope.shape[0], 2 * rope.shape[1], _ptr(positions, torch.int32)
 
 
 def kda_qk_norm_rope(q, k, rope, positions, q_weight=None, k_weight=None, eps=1e-6, *, norm=True,
@@ -602,9 +609,9 @@ def kda_qk_norm_rope(q, k, rope, positions, q_weight=None, k_weight=None, eps=1e
         raise ValueError("q, k and their outputs must agree in tokens, heads and type")
     (qp, qs), (kp, ks) = _heads(q, q.dtype), _heads(k, q.dtype)
     table, P, R, pos = _rope_args(rope, positions, T)
-    rc = _lib.kda_qk_norm_rope(_dt(q), _dt(q_out), T, Hq, Hkv, qp, qs, kp, ks, _f32(q_weight),
-                               _f32(k_weight), float(eps), int(norm), table, P, R, int(interleaved),
-                               pos, _p(q_out), _p(k_out), _stream(stream))
+    rc = _lib.kda_qk_norm_rope(_dt(q), _dt(q_out), T, Hq, Hkv, qp, qs, kp, ks, _ptr(q_weight, torch.float32),
+                               _ptr(k_weight, torch.float32), float(eps), int(norm), table, P, R, int(interleaved),
+                               pos, _ptr(q_out), _ptr(k_out), _raw_stream(stream, q))
     _check("kda_qk_norm_rope", rc)
     return q_out, k_out
 
@@ -628,10 +635,10 @@ def kda_qk_norm_rope_append(q, k, v, rope, positions, kv_pool, page_table, slot,
     (qp, qs), (kp, ks), (vp, vs) = _heads(q, q.dtype), _heads(k, q.dtype), _heads(v, q.dtype)
     table, npos, R, pos = _rope_args(rope, positions, T)
     rc = _lib.kda_qk_norm_rope_append(
-        _dt(q), _dt(q_out), slot.numel(), T, Hq, Hkv, qp, qs, kp, ks, vp, vs, _f32(q_weight),
-        _f32(k_weight), float(eps), int(norm), table, npos, R, int(interleaved), pos, P, page,
-        page_table.shape[0], page_table.shape[1], _i32(page_table), _i32(slot), _i32(cu_tokens),
-        _i32(kv_len), _p(kv_pool), _p(q_out), _stream(stream))
+        _dt(q), _dt(q_out), slot.numel(), T, Hq, Hkv, qp, qs, kp, ks, vp, vs, _ptr(q_weight, torch.float32),
+        _ptr(k_weight, torch.float32), float(eps), int(norm), table, npos, R, int(interleaved), pos, P, page,
+        page_table.shape[0], page_table.shape[1], _ptr(page_table, torch.int32), _ptr(slot, torch.int32), _ptr(cu_tokens, torch.int32),
+        _ptr(kv_len, torch.int32), _ptr(kv_pool), _ptr(q_out), _raw_stream(stream, q))
     _check("kda_qk_norm_rope_append", rc)
     return q_out
 
@@ -654,9 +661,9 @@ def kda_window_attention(q, kv_pool, page_table, slot, cu_tokens, kv_len, window
     rc = _lib.kda_window_attention(
         _dt(q), slot.numel(), T, max(T, 1) if max_tokens is None else int(max_tokens), Hq, Hkv, P,
         page, page_table.shape[0], page_table.shape[1],
-        0x7fffffff if window is None else int(window), int(sinks), _p(q), _p(kv_pool),
-        _i32(page_table), _i32(slot), _i32(cu_tokens), _i32(kv_len), float(scale), _p(o),
-        _stream(stream))
+        0x7fffffff if window is None else int(window), int(sinks), _ptr(q), _ptr(kv_pool),
+        _ptr(page_table, torch.int32), _ptr(slot, torch.int32), _ptr(cu_tokens, torch.int32), _ptr(kv_len, torch.int32), float(scale), _ptr(o),
+        _raw_stream(stream, q))
     _check("kda_window_attention", rc)
     return o
 
@@ -675,8 +682,8 @@ def kda_pages_copy(pool, src, dst, *, stream=None):
     if src.numel() != dst.numel():
         raise ValueError("src and dst must have one length")
     L, P, nbytes = _layers(pool)
-    _check("kda_pages_copy", _lib.kda_pages_copy(L, P, nbytes, src.numel(), _i32(src), _i32(dst),
-                                                 _p(pool), _stream(stream)))
+    _check("kda_pages_copy", _lib.kda_pages_copy(L, P, nbytes, src.numel(), _ptr(src, torch.int32), _ptr(dst, torch.int32),
+                                                 _ptr(pool), _raw_stream(stream, pool)))
 
 
 def kda_pages_workspace_size(num_pages: int, table_rows: int) -> int:
@@ -698,8 +705,8 @@ def kda_pages_fork(pool, page_table, kv_len, parent, child, page_size, *, worksp
     R, M = page_table.shape
     workspace, wbytes = _pages_workspace(workspace, P, R, pool.device)
     _check("kda_pages_fork", _lib.kda_pages_fork(
-        L, P, nbytes, int(page_size), R, M, parent.numel(), _i32(parent), _i32(child),
-        _i32(page_table), _i32(kv_len), _p(pool), _p(workspace), wbytes, _stream(stream)))
+        L, P, nbytes, int(page_size), R, M, parent.numel(), _ptr(parent, torch.int32), _ptr(child, torch.int32),
+        _ptr(page_table, torch.int32), _ptr(kv_len, torch.int32), _ptr(pool), _ptr(workspace), wbytes, _raw_stream(stream, pool)))
 
 
 def kda_pages_release(page_table, kv_len, rows, page_size, window=0, sinks=0, *, stream=None):
@@ -709,8 +716,8 @@ def kda_pages_release(page_table, kv_len, rows, page_size, window=0, sinks=0, *,
         raise ValueError("kv_len must have one entry per table row")
     R, M = page_table.shape
     _check("kda_pages_release", _lib.kda_pages_release(
-        R, M, int(page_size), rows.numel(), _i32(rows), int(window), int(sinks), _i32(page_table),
-        _i32(kv_len), _stream(stream)))
+        R, M, int(page_size), rows.numel(), _ptr(rows, torch.int32), int(window), int(sinks), _ptr(page_table, torch.int32),
+        _ptr(kv_len, torch.int32), _raw_stream(stream, page_table)))
 
 
 def kda_pages_compact(pool, page_table, *, table_out=None, num_live=None, workspace=None, stream=None):
@@ -726,8 +733,8 @@ def kda_pages_compact(pool, page_table, *, table_out=None, num_live=None, worksp
         num_live = torch.empty(1, dtype=torch.int32, device=pool.device)
     workspace, wbytes = _pages_workspace(workspace, P, R, pool.device)
     _check("kda_pages_compact", _lib.kda_pages_compact(
-        L, P, nbytes, R, M, _i32(page_table), _i32(table_out), _i32(num_live), _p(pool),
-        _p(workspace), wbytes, _stream(stream)))
+        L, P, nbytes, R, M, _ptr(page_table, torch.int32), _ptr(table_out, torch.int32), _ptr(num_live, torch.int32), _ptr(pool),
+        _ptr(workspace), wbytes, _raw_stream(stream, pool)))
     return table_out, num_live
 
 
