@@ -31,9 +31,17 @@ __device__ __forceinline__ void copy_pages(const PageMoves &m, int32_t n) {
     const int64_t chunks = (m.page_bytes + kChunk - 1) / kChunk;
     const int64_t units = (int64_t)n * m.num_layers * chunks;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int64_t page = u / chunks, chunk = u % chunks;
-        const int32_t i = (int32_t)(page % n);
-        const int64_t layer = page / n;
+        int64_t page, chunk, layer;
+        int32_t i;
+        if (units <= 0xffffffffLL) {  // 32-bit divisions
+            page = (uint32_t)u / (uint32_t)chunks;
+            layer = (uint32_t)page / (uint32_t)n;
+        } else {
+            page = u / chunks;
+            layer = page / n;
+        }
+        chunk = u - page * chunks;
+        i = (int32_t)(page - layer * n);
         const int32_t s = m.src[i], d = m.dst[i];
         if (!page_ok(s, m.num_pages) || !page_ok(d, m.num_pages)) continue;
         const int64_t words = m.page_bytes / 16, first = chunk * (kChunk / 16);
@@ -53,7 +61,11 @@ __device__ __forceinline__ void copy_pages(const PageMoves &m, int32_t n) {
     }
 }
 
+// The second launch of a call comes up while the first still plans, and waits for it here.
+__device__ __forceinline__ void wait_for_plan() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const PageMoves m) {
+    wait_for_plan();  // returns at once when this is the call's only launch
     copy_pages(m, m.n);
 }
 
@@ -95,13 +107,31 @@ __device__ __forceinline__ uint32_t valid_bits(int32_t w, int32_t num_pages) {
 // Marks the pages that the rows name; rows whose bit is set in `skip` (may be null) do not count.
 __device__ __forceinline__ void mark_live(uint32_t *live, const uint32_t *skip, const int32_t *table,
                                           int32_t rows, int32_t width, int32_t num_pages) {
+    constexpr int kAhead = 8;  // entries a thread has in flight
     const int lane = threadIdx.x & 31;
-    for (int32_t r = threadIdx.x >> 5; r < rows; r += kPlanThreads / 32) {
-        if (skip != nullptr && (skip[r >> 5] >> (r & 31) & 1u)) continue;
+    const auto mark = [&](int32_t id) {
+        if (page_ok(id, num_pages)) atomicOr(live + (id >> 5), 1u << (id & 31));
+    };
+    if (skip == nullptr) {  // the whole table as one array
+        const int64_t entries = (int64_t)rows * width;
+        for (int64_t e0 = threadIdx.x; e0 < entries; e0 += kAhead * kPlanThreads) {
+            int32_t id[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) id[k] = e0 + k * kPlanThreads < entries ? table[e0 + k * kPlanThreads] : -1;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) mark(id[k]);
+        }
+        return;
+    }
+    for (int32_t r = threadIdx.x >> 5; r < rows; r += kPlanThreads / 32) {  // a warp a row
+        if (skip[r >> 5] >> (r & 31) & 1u) continue;
         const int32_t *row = table + (int64_t)r * width;
-        for (int32_t c = lane; c < width; c += 32) {
-            const int32_t id = row[c];
-            if (page_ok(id, num_pages)) atomicOr(live + (id >> 5), 1u << (id & 31));
+        for (int32_t c0 = lane; c0 < width; c0 += 32 * kAhead) {
+            int32_t id[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) id[k] = c0 + 32 * k < width ? row[c0 + 32 * k] : -1;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) mark(id[k]);
         }
     }
 }
@@ -113,6 +143,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_plan_kernel(const Pag
     const int32_t words = (P + 31) / 32, row_words = (R + 31) / 32;
     uint32_t *live = smem, *is_child = smem + words;
     const int tid = threadIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     for (int32_t i = tid; i < words + row_words; i += kPlanThreads) smem[i] = 0;
     __syncthreads();
     for (int32_t i = tid; i < F; i += kPlanThreads) {
@@ -188,6 +219,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(const 
     __shared__ int32_t warp_sums[32];
     const int32_t P = a.moves.num_pages, words = (P + 31) / 32;
     const int tid = threadIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     for (int32_t i = tid; i < words; i += kPlanThreads) smem[i] = 0;
     __syncthreads();
     mark_live(smem, nullptr, a.table_in, a.table_rows, a.table_width, P);
@@ -219,6 +251,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(const 
 }
 
 __global__ void __launch_bounds__(kCopyThreads) pages_compact_move_kernel(const PageCompactArgs a) {
+    wait_for_plan();
     const int32_t live = *a.num_live, P = a.moves.num_pages;
     const int64_t entries = (int64_t)a.table_rows * a.table_width;
     for (int64_t i = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; i < entries;
@@ -250,11 +283,24 @@ __global__ void __launch_bounds__(kReleaseThreads) pages_release_kernel(const Pa
 }
 
 unsigned copy_grid(int64_t units) {
-    const int64_t most = (int64_t)device_sm_count() * 8;
+    const int64_t most = (int64_t)device_sm_count() * 64;
     return (unsigned)(units < 1 ? 1 : units < most ? units : most);
 }
 int64_t copy_units(const PageMoves &m, int64_t n) {
     return n * m.num_layers * ((m.page_bytes + kChunk - 1) / kChunk);
+}
+template <typename Kernel, typename Args>
+cudaError_t launch_after_plan(Kernel k, unsigned grid, cudaStream_t stream, const Args &a) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kCopyThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, a);
 }
 template <typename Kernel>
 cudaError_t allow_smem(Kernel k, size_t bytes) {
@@ -276,7 +322,8 @@ cudaError_t launch_pages_fork(const PageForkArgs &a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     pages_fork_plan_kernel<<<1, kPlanThreads, smem, stream>>>(a);
     e = cudaGetLastError();
-    return e == cudaSuccess ? launch_pages_copy(a.moves, stream) : e;
+    if (e != cudaSuccess) return e;
+    return launch_after_plan(pages_copy_kernel, copy_grid(copy_units(a.moves, a.moves.n)), stream, a.moves);
 }
 
 cudaError_t launch_pages_release(const PageReleaseArgs &a, cudaStream_t stream) {
@@ -293,8 +340,7 @@ cudaError_t launch_pages_compact(const PageCompactArgs &a, cudaStream_t stream) 
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     // at most min(L, P - L) <= P / 2 pages move
     const unsigned grid = copy_grid(copy_units(a.moves, (a.moves.num_pages + 1) / 2));
-    pages_compact_move_kernel<<<grid, kCopyThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_after_plan(pages_compact_move_kernel, grid, stream, a);
 }
 
 }  // namespace kda

@@ -8,21 +8,27 @@
 // scores and 4 x 8 outputs, so that each shared-memory read feeds two to four FMAs.  A key that a
 // row does not see takes no part: its score is replaced (never computed with), its probability of
 // zero skips the product with v, and keys past the end or without a page are loaded as zeros.
+// With few items a cluster of CTAs shares each one's key tiles, and joins the partial results
+// through distributed shared memory.
 #include <cfloat>
 
 #include "kda_window_attention.cuh"
+#include "tc_primitives.cuh"
 
 namespace kda {
 namespace {
+
+using tc::smem_u32;
 
 constexpr int kThreads = 256;
 constexpr int kTile = 64;              // rows of an item, keys of a tile
 constexpr int kPitch = kD + 4;         // q, k rows: float4 reads of 16 rows hit distinct banks
 constexpr int kPitchP = kTile + 4;
+constexpr int kMaxSplits = 8;
 constexpr size_t kSmem = sizeof(float) * (2 * kTile * kPitch + kTile * kD + kTile * kPitchP);
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) attention_rows_kernel(const WindowAttentionArgs a) {
+__global__ void __launch_bounds__(kThreads) attention_rows_kernel(const WindowAttentionArgs a, int32_t splits) {
     extern __shared__ float4 smem4[];
     float *sq = reinterpret_cast<float *>(smem4), *sk = sq + kTile * kPitch;
     float *sv = sk + kTile * kPitch, *sp = sv + kTile * kD;
@@ -34,7 +40,8 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const WindowAt
     AttnRequest req;
     int32_t index;
     AttnWalk walk;
-    if (!walk.find(a, blockIdx.x, G, kTile, req, index)) return;  // the same for every warp
+    const int32_t rank = (int32_t)cluster_rank();  // a cluster is one item
+    if (!walk.find(a, blockIdx.x / splits, G, kTile, req, index)) return;  // the same for the whole cluster
     const int32_t rows = req.n * G, r0 = index * kTile;
     const int32_t p0 = req.len - req.n;  // index of the request's first token
     const T *q = static_cast<const T *>(a.q), *pool = static_cast<const T *>(a.kv_pool);
@@ -64,7 +71,8 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const WindowAt
 
     const AttnKeys keys(p0 + r0 / G, p0 + (min(r0 + kTile, rows) - 1) / G, a.window, a.sinks, kTile);
     const int32_t end = p0 + (min(r0 + kTile, rows) - 1) / G + 1;  // no row sees a key from here on
-    for (int32_t it = 0; it < keys.count(); ++it) {
+    const int32_t tiles = keys.count(), last = (int32_t)((int64_t)tiles * (rank + 1) / splits);
+    for (int32_t it = (int32_t)((int64_t)tiles * rank / splits); it < last; ++it) {
         const int32_t j0 = keys.tile(it) * kTile;
         __syncthreads();  // the previous tile has been used
         if (tid == 0) s_mapped = 0;
@@ -164,28 +172,67 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const WindowAt
     }
 
     T *out = static_cast<T *>(a.o);
+    if (splits == 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int32_t row = r0 + 4 * ty + i;
+            if (row >= rows) continue;
+            const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+            T *dst = out + ((int64_t)(req.first + row / G) * a.num_q_heads + h * G + row % G) * kD;
+            store4(dst + 4 * tx, make_float4(o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv));
+            store4(dst + 64 + 4 * tx, make_float4(o[i][4] * inv, o[i][5] * inv, o[i][6] * inv, o[i][7] * inv));
+        }
+        return;
+    }
+    // The partial results take the place of k; the cluster's CTAs join 64 / splits rows each.
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int32_t row = r0 + 4 * ty + i;
-        if (row >= rows) continue;
-        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
-        T *dst = out + ((int64_t)(req.first + row / G) * a.num_q_heads + h * G + row % G) * kD;
-        store4(dst + 4 * tx, make_float4(o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv));
-        store4(dst + 64 + 4 * tx, make_float4(o[i][4] * inv, o[i][5] * inv, o[i][6] * inv, o[i][7] * inv));
+        float *dst = sk + (4 * ty + i) * kPitch;
+        *reinterpret_cast<float4 *>(dst + 4 * tx) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+        *reinterpret_cast<float4 *>(dst + 64 + 4 * tx) = make_float4(o[i][4], o[i][5], o[i][6], o[i][7]);
+        if (tx == 0) *reinterpret_cast<float2 *>(dst + kD) = make_float2(m[i], l[i]);
     }
+    cluster_sync();
+    for (int32_t r = rank * (kTile / splits) + (tid >> 5); r < (rank + 1) * (kTile / splits); r += kThreads / 32) {
+        const int32_t row = r0 + r, lane = tid & 31;
+        if (row >= rows) break;
+        const uint32_t mine = smem_u32(sk + r * kPitch);
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < splits) ml = remote_float2(remote(mine + kD * 4, lane));
+        float top = ml.x;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : expf(ml.x - top);  // (a NaN sum stays one)
+        float sum = w * ml.y;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int32_t s = 0; s < splits; ++s) {
+            const float ws = __shfl_sync(0xffffffffu, w, s);
+            const float4 x = remote_float4(remote(mine + 16 * lane, s));
+            acc = make_float4(fmaf(ws, x.x, acc.x), fmaf(ws, x.y, acc.y), fmaf(ws, x.z, acc.z), fmaf(ws, x.w, acc.w));
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        store4(out + ((int64_t)(req.first + row / G) * a.num_q_heads + h * G + row % G) * kD + 4 * lane,
+               make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    }
+    cluster_sync();  // no CTA leaves while another reads its partials
 }
 
 template <typename T>
 cudaError_t launch_rows(const WindowAttentionArgs &a, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(attention_rows_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kSmem);
-    if (e != cudaSuccess) return e;
     // each request rounds up to whole items at most once
     const int64_t rows = (int64_t)a.cache.total_tokens * (a.num_q_heads / a.num_kv_heads);
     const int64_t items = (rows + kTile - 1) / kTile + a.cache.batch;
-    if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    attention_rows_kernel<T><<<dim3((unsigned)items, (unsigned)a.num_kv_heads), kThreads, kSmem, stream>>>(a);
-    return cudaGetLastError();
+    // Split an item's keys over a cluster until the GPU is full, with two tiles a CTA or more.
+    const int64_t reach = (int64_t)a.window + a.sinks + kTile, held = (int64_t)a.cache.table_width * a.cache.page_size;
+    const int64_t tiles = (reach < held ? reach : held) / kTile;
+    int splits = 1;
+    while (splits < kMaxSplits && items * a.num_kv_heads * splits < 2ll * device_sm_count() && tiles >= 4 * splits) splits *= 2;
+    if (items * splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    return launch_clusters(attention_rows_kernel<T>, dim3((unsigned)(items * splits), (unsigned)a.num_kv_heads), splits,
+                           kThreads, kSmem, stream, a, (int32_t)splits);
 }
 
 }  // namespace
