@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(kThreads, 8) norm_rope_kernel(const NormRopeAr
     const Tin *src = static_cast<const Tin *>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
                      t * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) + (int64_t)h0 * kD;
 
+    grid_wait();
     Raw ra[kRows], rb[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
@@ -182,9 +183,8 @@ cudaError_t launch(const NormRopeArgs &a, cudaStream_t stream) {
     const uint32_t q_chunks = (a.num_q_heads + kRows - 1) / kRows, kv_chunks = (a.num_kv_heads + kRows - 1) / kRows;
     const int64_t groups = (int64_t)a.cache.total_tokens * (q_chunks + (kAppend ? 2 : 1) * kv_chunks);
     const unsigned grid = (unsigned)((groups + kThreads / kGroup - 1) / (kThreads / kGroup));
-    if (a.interleaved) norm_rope_kernel<Tin, Tout, kAppend, true><<<grid, kThreads, 0, stream>>>(a, q_chunks, kv_chunks);
-    else norm_rope_kernel<Tin, Tout, kAppend, false><<<grid, kThreads, 0, stream>>>(a, q_chunks, kv_chunks);
-    return cudaGetLastError();
+    const auto kernel = a.interleaved ? norm_rope_kernel<Tin, Tout, kAppend, true> : norm_rope_kernel<Tin, Tout, kAppend, false>;
+    return launch_serial(kernel, dim3(grid), kThreads, 0, stream, a, q_chunks, kv_chunks);
 }
 template <typename Tin, typename Tout>
 cudaError_t launch(const NormRopeArgs &a, cudaStream_t stream) {

@@ -61,11 +61,8 @@ __device__ __forceinline__ void copy_pages(const PageMoves &m, int32_t n) {
     }
 }
 
-// The second launch of a call comes up while the first still plans, and waits for it here.
-__device__ __forceinline__ void wait_for_plan() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const PageMoves m) {
-    wait_for_plan();  // returns at once when this is the call's only launch
+    grid_wait();
     copy_pages(m, m.n);
 }
 
@@ -143,8 +140,9 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_plan_kernel(const Pag
     const int32_t words = (P + 31) / 32, row_words = (R + 31) / 32;
     uint32_t *live = smem, *is_child = smem + words;
     const int tid = threadIdx.x;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the copies come up meanwhile
     for (int32_t i = tid; i < words + row_words; i += kPlanThreads) smem[i] = 0;
+    grid_wait();
     __syncthreads();
     for (int32_t i = tid; i < F; i += kPlanThreads) {
         const int32_t c = a.child[i];
@@ -219,8 +217,9 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(const 
     __shared__ int32_t warp_sums[32];
     const int32_t P = a.moves.num_pages, words = (P + 31) / 32;
     const int tid = threadIdx.x;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the moves come up meanwhile
     for (int32_t i = tid; i < words; i += kPlanThreads) smem[i] = 0;
+    grid_wait();
     __syncthreads();
     mark_live(smem, nullptr, a.table_in, a.table_rows, a.table_width, P);
     __syncthreads();
@@ -251,7 +250,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(const 
 }
 
 __global__ void __launch_bounds__(kCopyThreads) pages_compact_move_kernel(const PageCompactArgs a) {
-    wait_for_plan();
+    grid_wait();
     const int32_t live = *a.num_live, P = a.moves.num_pages;
     const int64_t entries = (int64_t)a.table_rows * a.table_width;
     for (int64_t i = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; i < entries;
@@ -265,6 +264,7 @@ __global__ void __launch_bounds__(kCopyThreads) pages_compact_move_kernel(const 
 constexpr int kReleaseThreads = 128;
 
 __global__ void __launch_bounds__(kReleaseThreads) pages_release_kernel(const PageReleaseArgs a) {
+    grid_wait();
     const int32_t r = a.rows[blockIdx.x];
     if ((uint32_t)r >= (uint32_t)a.table_rows) {
         if (threadIdx.x == 0) record_status(a.status, KDA_ERR_DEVICE_CHECK, blockIdx.x);
@@ -289,58 +289,32 @@ unsigned copy_grid(int64_t units) {
 int64_t copy_units(const PageMoves &m, int64_t n) {
     return n * m.num_layers * ((m.page_bytes + kChunk - 1) / kChunk);
 }
-template <typename Kernel, typename Args>
-cudaError_t launch_after_plan(Kernel k, unsigned grid, cudaStream_t stream, const Args &a) {
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kCopyThreads);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k, a);
-}
-template <typename Kernel>
-cudaError_t allow_smem(Kernel k, size_t bytes) {
-    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 }  // namespace
 
 cudaError_t launch_pages_copy(const PageMoves &m, cudaStream_t stream) {
     if (m.n == 0) return cudaSuccess;
-    pages_copy_kernel<<<copy_grid(copy_units(m, m.n)), kCopyThreads, 0, stream>>>(m);
-    return cudaGetLastError();
+    return launch_serial(pages_copy_kernel, dim3(copy_grid(copy_units(m, m.n))), kCopyThreads, 0, stream, m);
 }
 
 cudaError_t launch_pages_fork(const PageForkArgs &a, cudaStream_t stream) {
     if (a.moves.n == 0) return cudaSuccess;
     const size_t smem = 4 * (((size_t)a.moves.num_pages + 31) / 32 + ((size_t)a.table_rows + 31) / 32);
-    cudaError_t e = allow_smem(pages_fork_plan_kernel, smem);
-    if (e != cudaSuccess) return e;
-    pages_fork_plan_kernel<<<1, kPlanThreads, smem, stream>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    return launch_after_plan(pages_copy_kernel, copy_grid(copy_units(a.moves, a.moves.n)), stream, a.moves);
+    const cudaError_t e = launch_serial(pages_fork_plan_kernel, dim3(1), kPlanThreads, smem, stream, a);
+    return e == cudaSuccess ? launch_pages_copy(a.moves, stream) : e;
 }
 
 cudaError_t launch_pages_release(const PageReleaseArgs &a, cudaStream_t stream) {
     if (a.n == 0) return cudaSuccess;
-    pages_release_kernel<<<(unsigned)a.n, kReleaseThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_serial(pages_release_kernel, dim3((unsigned)a.n), kReleaseThreads, 0, stream, a);
 }
 
 cudaError_t launch_pages_compact(const PageCompactArgs &a, cudaStream_t stream) {
     const size_t smem = 4 * (((size_t)a.moves.num_pages + 31) / 32);
-    cudaError_t e = allow_smem(pages_compact_plan_kernel, smem);
+    const cudaError_t e = launch_serial(pages_compact_plan_kernel, dim3(1), kPlanThreads, smem, stream, a);
     if (e != cudaSuccess) return e;
-    pages_compact_plan_kernel<<<1, kPlanThreads, smem, stream>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     // at most min(L, P - L) <= P / 2 pages move
     const unsigned grid = copy_grid(copy_units(a.moves, (a.moves.num_pages + 1) / 2));
-    return launch_after_plan(pages_compact_move_kernel, grid, stream, a);
+    return launch_serial(pages_compact_move_kernel, dim3(grid), kCopyThreads, 0, stream, a);
 }
 
 }  // namespace kda

@@ -37,6 +37,7 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const WindowAt
     const int32_t G = a.num_q_heads / a.num_kv_heads, h = blockIdx.y;
     const CacheArgs &cache = a.cache;
 
+    grid_wait();
     AttnRequest req;
     int32_t index;
     AttnWalk walk;

@@ -124,24 +124,27 @@ __device__ __forceinline__ uint32_t remote_u32(uint32_t addr) {
     return x;
 }
 
-// A launch of clusters of `size` CTAs along x (above 8: the non-portable size).
+// A launch of clusters of `size` CTAs along x (above 8: the non-portable size), which may come up early
+// as launch_serial's do: the kernel calls grid_wait().
 template <typename Kernel, typename... Args>
 cudaError_t launch_clusters(Kernel kernel, dim3 grid, int size, int threads, size_t smem, cudaStream_t stream,
                             const Args &...args) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess && size > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)size;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

@@ -131,10 +131,6 @@ __global__ void __launch_bounds__(kThreads, 2) attention_split_kernel(const __gr
     const int32_t splits = gridDim.x, h = blockIdx.y, G = p.G;
     const int32_t rank = (int32_t)cluster_rank();  // = blockIdx.x: a cluster is one row of the grid
 
-    bool bad;
-    const AttnRequest req = attn_request(a, (int32_t)blockIdx.z, &bad);
-    if (bad && rank == 0 && h == 0 && threadIdx.x == 0) record_status(a.status, KDA_ERR_DEVICE_CHECK, blockIdx.z);
-    if (req.n == 0) return;  // the whole cluster
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sh.full[i], 1);
@@ -143,6 +139,11 @@ __global__ void __launch_bounds__(kThreads, 2) attention_split_kernel(const __gr
         sh.abort = sh.tainted = 0;
         fence_mbar_init();
     }
+    grid_wait();
+    bool bad;
+    const AttnRequest req = attn_request(a, (int32_t)blockIdx.z, &bad);
+    if (bad && rank == 0 && h == 0 && threadIdx.x == 0) record_status(a.status, KDA_ERR_DEVICE_CHECK, blockIdx.z);
+    if (req.n == 0) return;  // the whole cluster
     __syncthreads();
 
     const int32_t p0 = req.len - req.n, rows = req.n * G;  // p0: index of the first token

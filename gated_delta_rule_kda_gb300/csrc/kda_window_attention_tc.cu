@@ -646,6 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
         tmem_relinquish();
     }
     fence_before_sync();
+    grid_wait();
     __syncthreads();
     fence_after_sync();
     if (warp < 8) {
@@ -708,13 +709,10 @@ cudaError_t launch_window_attention_tc(const WindowAttentionArgs &a, cudaStream_
            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorNotSupported;
-    cudaError_t e = cudaFuncSetAttribute(attention_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SM_DYN);
-    if (e != cudaSuccess) return e;
     // each request rounds up to whole items at most once
     const int64_t items = ((int64_t)a.cache.total_tokens / (2 * p.tq) + a.cache.batch) * a.num_kv_heads;
     const int64_t sms = device_sm_count();
-    attention_tc_kernel<<<(unsigned)(items < sms ? items : sms), kThreads, SM_DYN, stream>>>(p);
-    return cudaGetLastError();
+    return launch_serial(attention_tc_kernel, dim3((unsigned)(items < sms ? items : sms)), kThreads, SM_DYN, stream, p);
 }
 
 }  // namespace kda
