@@ -548,16 +548,29 @@ def rope_table(num_positions: int, rotary_dim: int = HEAD_DIM, base: float = 100
     return torch.stack([angle.cos(), angle.sin()], -1).mul_(magnitude).float().contiguous()
 
 
-# Marshalling of the calls below: plain integers for pointers, and the raw current stream (a few
-# microseconds less a call than stream and pointer objects, which is what a decode step waits for).
-def _ptr(t: Optional[torch.Tensor], dtype: Optional[torch.dtype] = None):
+# Marshalling of the calls below: plain integers for pointers, the raw current stream, and few
+# Python calls (a decode step's kernels take less time than objects for each argument would).
+_F32, _I32 = torch.float32, torch.int32
+_ELEM = {torch.bfloat16: KDA_BF16, torch.float32: KDA_FP32}
+
+
+def _ptr(t: Optional[torch.Tensor]):
     if t is None:
         return None
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"expected {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
     return t.data_ptr()
+
+
+def _ptrs(dtype: torch.dtype, *tensors):
+    """Pointers of dense tensors of one type (None for None)."""
+    for t in tensors:
+        if t is not None:
+            if t.dtype is not dtype:
+                raise TypeError(f"expected {dtype}, got {t.dtype}")
+            if not t.is_contiguous():
+                raise ValueError("tensors must be contiguous")
+    return [None if t is None else t.data_ptr() for t in tensors]
 
 
 def _raw_stream(stream, t: torch.Tensor):
@@ -566,15 +579,20 @@ def _raw_stream(stream, t: torch.Tensor):
     return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else None
 
 
-def _heads(t: torch.Tensor, dtype: torch.dtype):
-    """(pointer, elements from token to token) of [T, heads, 128] whose heads lie side by side."""
+def _elem(t: torch.Tensor) -> int:
+    code = _ELEM.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
+
+
+def _heads(t: torch.Tensor):
+    """(heads, elements from token to token) of [T, heads, 128] whose heads lie side by side."""
     T, H, d = t.shape
-    if t.dtype != dtype:
-        raise TypeError(f"expected {dtype}, got {t.dtype}")
-    s = t.stride()
-    if d != HEAD_DIM or s[2] != 1 or (H > 1 and s[1] != HEAD_DIM):
+    s0, s1, s2 = t.stride()
+    if d != HEAD_DIM or s2 != 1 or (s1 != HEAD_DIM and H > 1):
         raise ValueError("the heads of a token must lie side by side, 128 channels each")
-    return t.data_ptr(), (s[0] if T > 1 else H * HEAD_DIM)
+    return H, s0 if T > 1 else H * HEAD_DIM
 
 
 def _pool_shape(kv_pool):
@@ -590,7 +608,19 @@ def _rope_args(rope, positions, T):
         return None, 0, 0, None
     if positions.numel() != T:
         raise ValueError("positions must have one entry per token")
-    return _ptr(rope, torch.float32), rope.shape[0], 2 * rope.shape[1], _ptr(positions, torch.int32)
+    P, half, _ = rope.shape
+    if rope.dtype is not _F32 or positions.dtype is not _I32:
+        raise TypeError("the rotation table must be float32, positions int32")
+    return _ptr(rope), P, 2 * half, _ptr(positions)
+
+
+def _cache_args(page_table, slot, cu_tokens, kv_len):
+    """(requests, rows, width, pointers of the table, slots, offsets and lengths)."""
+    R, M = page_table.shape
+    B = slot.numel()
+    if cu_tokens.numel() != B + 1 or kv_len.numel() != R:
+        raise ValueError("cu_tokens must have one entry more than slot, kv_len one per table row")
+    return B, R, M, _ptrs(_I32, page_table, slot, cu_tokens, kv_len)
 
 
 def kda_qk_norm_rope(q, k, rope, positions, q_weight=None, k_weight=None, eps=1e-6, *, norm=True,
@@ -598,20 +628,21 @@ def kda_qk_norm_rope(q, k, rope, positions, q_weight=None, k_weight=None, eps=1e
     """q [T, Hq, 128] and k [T, Hkv, 128] (heads dense, any token stride) normed per head and
     rotated by rope_table(...) at positions [T] int32 (rope None: no rotation).
     Returns (q_out, k_out)."""
-    T, Hq, _ = q.shape
-    Hkv = k.shape[1]
     out_dtype = q_out.dtype if q_out is not None else out_dtype or q.dtype
     if q_out is None:
-        q_out = torch.empty((T, Hq, HEAD_DIM), dtype=out_dtype, device=q.device)
+        q_out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
     if k_out is None:
-        k_out = torch.empty((T, Hkv, HEAD_DIM), dtype=out_dtype, device=q.device)
-    if k.shape[0] != T or q_out.shape != q.shape or k_out.shape != k.shape or k_out.dtype != out_dtype:
+        k_out = torch.empty(k.shape, dtype=out_dtype, device=k.device)
+    T = q.shape[0]
+    if k.shape[0] != T or q_out.shape != q.shape or k_out.shape != k.shape or k_out.dtype != out_dtype \
+            or k.dtype != q.dtype:
         raise ValueError("q, k and their outputs must agree in tokens, heads and type")
-    (qp, qs), (kp, ks) = _heads(q, q.dtype), _heads(k, q.dtype)
+    (Hq, qs), (Hkv, ks) = _heads(q), _heads(k)
     table, P, R, pos = _rope_args(rope, positions, T)
-    rc = _lib.kda_qk_norm_rope(_dt(q), _dt(q_out), T, Hq, Hkv, qp, qs, kp, ks, _ptr(q_weight, torch.float32),
-                               _ptr(k_weight, torch.float32), float(eps), int(norm), table, P, R, int(interleaved),
-                               pos, _ptr(q_out), _ptr(k_out), _raw_stream(stream, q))
+    wq, wk = _ptrs(_F32, q_weight, k_weight)
+    rc = _lib.kda_qk_norm_rope(_elem(q), _elem(q_out), T, Hq, Hkv, q.data_ptr(), qs, k.data_ptr(), ks,
+                               wq, wk, eps, norm, table, P, R, interleaved, pos, _ptr(q_out),
+                               _ptr(k_out), _raw_stream(stream, q))
     _check("kda_qk_norm_rope", rc)
     return q_out, k_out
 
@@ -622,23 +653,21 @@ def kda_qk_norm_rope_append(q, k, v, rope, positions, kv_pool, page_table, slot,
     """kda_qk_norm_rope with k (normed and rotated) and v written to the cache pages of the tokens:
     kv_pool [P, 2, Hkv, page_size, 128], page_table [R, M], kv_len [R] (these tokens counted),
     slot [B], cu_tokens [B+1].  Outputs have the pool's type.  Returns q_out."""
-    T, Hq, _ = q.shape
-    Hkv = k.shape[1]
     P, pool_heads, page = _pool_shape(kv_pool)
     if q_out is None:
-        q_out = torch.empty((T, Hq, HEAD_DIM), dtype=kv_pool.dtype, device=q.device)
-    if k.shape[0] != T or v.shape != k.shape or pool_heads != Hkv or q_out.shape != q.shape \
-            or q_out.dtype != kv_pool.dtype:
+        q_out = torch.empty(q.shape, dtype=kv_pool.dtype, device=q.device)
+    T, k_shape, dtype = q.shape[0], k.shape, q.dtype
+    if k_shape[0] != T or v.shape != k_shape or k_shape[1] != pool_heads or q_out.shape != q.shape \
+            or q_out.dtype is not kv_pool.dtype or k.dtype is not dtype or v.dtype is not dtype:
         raise ValueError("q, k, v, q_out and kv_pool must agree in tokens, heads and type")
-    if cu_tokens.numel() != slot.numel() + 1 or page_table.shape[0] != kv_len.numel():
-        raise ValueError("cu_tokens must have one entry more than slot, kv_len one per table row")
-    (qp, qs), (kp, ks), (vp, vs) = _heads(q, q.dtype), _heads(k, q.dtype), _heads(v, q.dtype)
+    (Hq, qs), (Hkv, ks), (_, vs) = _heads(q), _heads(k), _heads(v)
     table, npos, R, pos = _rope_args(rope, positions, T)
+    B, rows, width, (pt, sl, cu, kl) = _cache_args(page_table, slot, cu_tokens, kv_len)
+    wq, wk = _ptrs(_F32, q_weight, k_weight)
     rc = _lib.kda_qk_norm_rope_append(
-        _dt(q), _dt(q_out), slot.numel(), T, Hq, Hkv, qp, qs, kp, ks, vp, vs, _ptr(q_weight, torch.float32),
-        _ptr(k_weight, torch.float32), float(eps), int(norm), table, npos, R, int(interleaved), pos, P, page,
-        page_table.shape[0], page_table.shape[1], _ptr(page_table, torch.int32), _ptr(slot, torch.int32), _ptr(cu_tokens, torch.int32),
-        _ptr(kv_len, torch.int32), _ptr(kv_pool), _ptr(q_out), _raw_stream(stream, q))
+        _elem(q), _elem(q_out), B, T, Hq, Hkv, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+        wq, wk, eps, norm, table, npos, R, interleaved, pos, P, page, rows, width, pt, sl, cu, kl,
+        _ptr(kv_pool), _ptr(q_out), _raw_stream(stream, q))
     _check("kda_qk_norm_rope_append", rc)
     return q_out
 
@@ -648,42 +677,43 @@ def kda_window_attention(q, kv_pool, page_table, slot, cu_tokens, kv_len, window
     """Attention of q [T, Hq, 128] over the requests' rows of the cache, with a sliding window and
     the first `sinks` tokens always visible (window None: plain causal).  max_tokens: no request
     brings more (default: T); small values let the call split long rows.  Returns o."""
-    T, Hq, _ = q.shape
+    T, Hq, d = q.shape
     P, Hkv, page = _pool_shape(kv_pool)
-    if kv_pool.dtype != q.dtype:
+    if kv_pool.dtype is not q.dtype:
         raise TypeError("q and kv_pool must have one type")
-    if cu_tokens.numel() != slot.numel() + 1 or page_table.shape[0] != kv_len.numel():
-        raise ValueError("cu_tokens must have one entry more than slot, kv_len one per table row")
     if o is None:
         o = torch.empty_like(q)
-    elif o.shape != q.shape or o.dtype != q.dtype:
+    elif o.shape != q.shape or o.dtype is not q.dtype:
         raise ValueError("o must have q's shape and type")
+    if d != HEAD_DIM:
+        raise ValueError("q must be [tokens, heads, 128]")
+    B, rows, width, (pt, sl, cu, kl) = _cache_args(page_table, slot, cu_tokens, kv_len)
     rc = _lib.kda_window_attention(
-        _dt(q), slot.numel(), T, max(T, 1) if max_tokens is None else int(max_tokens), Hq, Hkv, P,
-        page, page_table.shape[0], page_table.shape[1],
-        0x7fffffff if window is None else int(window), int(sinks), _ptr(q), _ptr(kv_pool),
-        _ptr(page_table, torch.int32), _ptr(slot, torch.int32), _ptr(cu_tokens, torch.int32), _ptr(kv_len, torch.int32), float(scale), _ptr(o),
-        _raw_stream(stream, q))
+        _elem(q), B, T, max(T, 1) if max_tokens is None else max_tokens, Hq, Hkv, P, page, rows, width,
+        0x7fffffff if window is None else window, sinks, _ptr(q), _ptr(kv_pool), pt, sl, cu, kl, scale,
+        _ptr(o), _raw_stream(stream, q))
     _check("kda_window_attention", rc)
     return o
 
 
 def _layers(pool):
     """(layers, pages, bytes of a page) of [layers, pages, ...]."""
-    if pool.dim() < 3:
+    shape = pool.shape
+    if len(shape) < 3:
         raise ValueError("pool must be [layers, pages, ...]")
-    L, P = pool.shape[0], pool.shape[1]
+    L, P = shape[0], shape[1]
     return L, P, pool.numel() // max(1, L * P) * pool.element_size()
 
 
 def kda_pages_copy(pool, src, dst, *, stream=None):
     """Pages dst[i] := pages src[i] in every layer of pool [layers, pages, ...] (rows of a
     recurrent-state pool as well); src, dst int32 on the device."""
-    if src.numel() != dst.numel():
+    n = src.numel()
+    if dst.numel() != n:
         raise ValueError("src and dst must have one length")
     L, P, nbytes = _layers(pool)
-    _check("kda_pages_copy", _lib.kda_pages_copy(L, P, nbytes, src.numel(), _ptr(src, torch.int32), _ptr(dst, torch.int32),
-                                                 _ptr(pool), _raw_stream(stream, pool)))
+    s, d = _ptrs(_I32, src, dst)
+    _check("kda_pages_copy", _lib.kda_pages_copy(L, P, nbytes, n, s, d, _ptr(pool), _raw_stream(stream, pool)))
 
 
 def kda_pages_workspace_size(num_pages: int, table_rows: int) -> int:
@@ -692,32 +722,35 @@ def kda_pages_workspace_size(num_pages: int, table_rows: int) -> int:
 
 def _pages_workspace(workspace, P, rows, device):
     if workspace is None:
-        workspace = torch.empty(kda_pages_workspace_size(P, rows), dtype=torch.uint8, device=device)
+        n = kda_pages_workspace_size(P, rows)
+        workspace = torch.empty(n, dtype=torch.uint8, device=device)
+        return workspace, n
     return workspace, workspace.numel() * workspace.element_size()
 
 
 def kda_pages_fork(pool, page_table, kv_len, parent, child, page_size, *, workspace=None, stream=None):
     """Rows child[i] become branches of rows parent[i], in place in page_table and kv_len: whole
     pages shared, a part-filled last page copied to a fresh one in every layer of pool."""
-    if parent.numel() != child.numel() or page_table.shape[0] != kv_len.numel():
+    F = parent.numel()
+    R, M = page_table.shape
+    if child.numel() != F or kv_len.numel() != R:
         raise ValueError("parent and child must have one length, kv_len one entry per table row")
     L, P, nbytes = _layers(pool)
-    R, M = page_table.shape
     workspace, wbytes = _pages_workspace(workspace, P, R, pool.device)
-    _check("kda_pages_fork", _lib.kda_pages_fork(
-        L, P, nbytes, int(page_size), R, M, parent.numel(), _ptr(parent, torch.int32), _ptr(child, torch.int32),
-        _ptr(page_table, torch.int32), _ptr(kv_len, torch.int32), _ptr(pool), _ptr(workspace), wbytes, _raw_stream(stream, pool)))
+    pa, ch, pt, kl = _ptrs(_I32, parent, child, page_table, kv_len)
+    _check("kda_pages_fork", _lib.kda_pages_fork(L, P, nbytes, page_size, R, M, F, pa, ch, pt, kl, _ptr(pool),
+                                                 _ptr(workspace), wbytes, _raw_stream(stream, pool)))
 
 
 def kda_pages_release(page_table, kv_len, rows, page_size, window=0, sinks=0, *, stream=None):
     """Empties the rows (window 0), or drops only the pages that no coming token sees with this
     window and these sinks; in place in page_table (and kv_len)."""
-    if page_table.shape[0] != kv_len.numel():
-        raise ValueError("kv_len must have one entry per table row")
     R, M = page_table.shape
-    _check("kda_pages_release", _lib.kda_pages_release(
-        R, M, int(page_size), rows.numel(), _ptr(rows, torch.int32), int(window), int(sinks), _ptr(page_table, torch.int32),
-        _ptr(kv_len, torch.int32), _raw_stream(stream, page_table)))
+    if kv_len.numel() != R:
+        raise ValueError("kv_len must have one entry per table row")
+    r, pt, kl = _ptrs(_I32, rows, page_table, kv_len)
+    _check("kda_pages_release", _lib.kda_pages_release(R, M, page_size, rows.numel(), r, window, sinks, pt, kl,
+                                                       _raw_stream(stream, page_table)))
 
 
 def kda_pages_compact(pool, page_table, *, table_out=None, num_live=None, workspace=None, stream=None):
@@ -730,11 +763,11 @@ def kda_pages_compact(pool, page_table, *, table_out=None, num_live=None, worksp
     if table_out.shape != page_table.shape:
         raise ValueError("table_out must have page_table's shape")
     if num_live is None:
-        num_live = torch.empty(1, dtype=torch.int32, device=pool.device)
+        num_live = torch.empty(1, dtype=_I32, device=pool.device)
     workspace, wbytes = _pages_workspace(workspace, P, R, pool.device)
-    _check("kda_pages_compact", _lib.kda_pages_compact(
-        L, P, nbytes, R, M, _ptr(page_table, torch.int32), _ptr(table_out, torch.int32), _ptr(num_live, torch.int32), _ptr(pool),
-        _ptr(workspace), wbytes, _raw_stream(stream, pool)))
+    tin, tout, live = _ptrs(_I32, page_table, table_out, num_live)
+    _check("kda_pages_compact", _lib.kda_pages_compact(L, P, nbytes, R, M, tin, tout, live, _ptr(pool),
+                                                       _ptr(workspace), wbytes, _raw_stream(stream, pool)))
     return table_out, num_live
 
 
