@@ -65,6 +65,7 @@ struct Params {
     int32_t G, tq;      // query heads a kv head, tokens of a row tile
     uint32_t inv_g;     // ceil(2^16 / G): x / G = x inv_g >> 16 for x < 128
     int32_t kv_rows;    // 2 P Hkv page_size
+    int32_t page_shift;  // log2 page_size
     float c;            // scale log2 e, > 0
 };
 
@@ -429,6 +430,15 @@ __device__ void scrub_warp(const Params &p, Shared &sh, unsigned char *sm) {
 // ---------------------------------------------------------------------------
 // Softmax and epilogue
 // ---------------------------------------------------------------------------
+constexpr uint32_t kMinusInf = 0xff800000u;
+
+// The lowest n bits (none for n < 0, all from 32 on).
+__device__ __forceinline__ uint32_t low_mask(int32_t n) {
+    uint32_t m;
+    asm("bmsk.clamp.b32 %0, 0, %1;" : "=r"(m) : "r"(max(n, 0)));
+    return m;
+}
+
 __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
     float a = __uint_as_float(s[0]), b = __uint_as_float(s[1]);
 #pragma unroll
@@ -447,6 +457,13 @@ __device__ __forceinline__ void store_rows(const Params &p, uint32_t o_tmem, boo
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     __nv_bfloat16 *out = o_item + 8 * (lane & 3);
+    int32_t to[4];  // rows 4 (lane / 4) + u of the tile, as rows of [T][Hq] from the item's first; -1: none
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int rt = 32 * quarter + (lane & ~3) + u;
+        const int tk = (int)((uint32_t)rt * p.inv_g >> 16), tt = token0 + tk;
+        to[u] = tk < p.tq && tt < tokens ? tt * p.a.num_q_heads + rt - tk * p.G : -1;
+    }
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {  // 32 channels: chunks 0 .. 3
         uint32_t x[4][4];
@@ -478,13 +495,10 @@ __device__ __forceinline__ void store_rows(const Params &p, uint32_t o_tmem, boo
                     }
                 }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {  // chunk lane % 4 of row 4 (lane / 4) + u
-            const int rt = 32 * quarter + (lane & ~3) + u;
-            const int tk = (int)((uint32_t)rt * p.inv_g >> 16), tt = token0 + tk;
-            if (tk < p.tq && tt < tokens)
-                *reinterpret_cast<uint4 *>(out + ((int64_t)tt * p.a.num_q_heads + rt - tk * p.G) * kD + 32 * c) =
+        for (int u = 0; u < 4; ++u)  // chunk lane % 4 of row 4 (lane / 4) + u
+            if (to[u] >= 0)
+                *reinterpret_cast<uint4 *>(out + (int64_t)to[u] * kD + 32 * c) =
                     make_uint4(x[u][0], x[u][1], x[u][2], x[u][3]);
-        }
     }
 }
 
@@ -494,7 +508,6 @@ __device__ void softmax_warps(const Params &p, Shared &sh, int r) {
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const uint32_t s_tmem = sh.tmem + lanes + 128 * r, o_tmem = sh.tmem + lanes + 256 + 128 * r;
     const WindowAttentionArgs &a = p.a;
-    const int32_t page = a.cache.page_size;
     // this row: its token of the item and query head (rows from tq G on are empty)
     const int32_t token = r * p.tq + row / p.G;
     uint32_t s_phase = 0, o_phase = 0, tiles = 0;
@@ -536,13 +549,14 @@ __device__ void softmax_warps(const Params &p, Shared &sh, int r) {
                 const int32_t sk = a.sinks - j0;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    uint32_t bits = low_bits(hi - 32 * c) & (~low_bits(lo - 32 * c) | low_bits(sk - 32 * c));
-                    if (page == 16) bits &= (mapped >> (2 * c) & 1 ? 0xffffu : 0u) | (mapped >> (2 * c + 1) & 1 ? 0xffff0000u : 0u);
-                    else if (!(mapped >> (32 * c / page) & 1)) bits = 0;
-                    if (__all_sync(0xffffffffu, bits == 0xffffffffu)) continue;  // most chunks of an edge tile
+                    uint32_t bits = low_mask(hi - 32 * c) & (~low_mask(lo - 32 * c) | low_mask(sk - 32 * c));
+                    if (p.page_shift == 4) bits &= (mapped >> (2 * c) & 1 ? 0xffffu : 0u) | (mapped >> (2 * c + 1) & 1 ? 0xffff0000u : 0u);
+                    else if (!(mapped >> (32 * c >> p.page_shift) & 1)) bits = 0;
+                    // most 32-key chunks of an edge tile need nothing (a way out for unseen ones too spilled)
+                    if (__all_sync(0xffffffffu, bits == 0xffffffffu)) continue;
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
-                        if (!(bits >> k & 1)) s[c][k] = 0xff800000u;  // -inf
+                        if (!(bits >> k & 1)) s[c][k] = kMinusInf;
                 }
             }
             if (masked) {
@@ -699,6 +713,7 @@ cudaError_t launch_window_attention_tc(const WindowAttentionArgs &a, cudaStream_
     p.tq = kTile / p.G;
     p.inv_g = (65536u + p.G - 1) / p.G;
     p.kv_rows = (int32_t)(2ll * a.cache.num_pages * a.num_kv_heads * a.cache.page_size);
+    p.page_shift = a.cache.page_size == 16 ? 4 : a.cache.page_size == 32 ? 5 : a.cache.page_size == 64 ? 6 : 7;
     p.c = (float)((double)a.scale * 1.4426950408889634);
     auto fn = tensor_map_encoder();
     if (fn == nullptr || !encode_kv_map(&p.tm_kv, a, a.cache.page_size)) return cudaErrorNotSupported;
