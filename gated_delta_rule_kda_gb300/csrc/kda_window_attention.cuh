@@ -211,5 +211,8 @@ cudaError_t launch_window_attention_split(const WindowAttentionArgs &a, cudaStre
 
 // A tensor map over kv_pool as rows of 128 channels, 64 channels x box_rows a box, 128-byte swizzle.
 bool encode_kv_map(CUtensorMap *m, const WindowAttentionArgs &a, int32_t box_rows);
+// The same rows seen as [k, v][half][row][64 channels] from a key row on: a box is the two halves of
+// box_rows keys, then those of their values.
+bool encode_kv_box_map(CUtensorMap *m, const WindowAttentionArgs &a, int32_t box_rows);
 
 }  // namespace kda

@@ -25,8 +25,7 @@ using namespace tc;
 constexpr int kWarps = 4;                     // consumers; one more fetches
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kTile = 64;                     // keys of a tile
-constexpr uint32_t kHalf = kTile * 128;       // bytes of 64 channels of a tile
-constexpr uint32_t kStageBytes = 4 * kHalf;   // k, then v
+constexpr uint32_t kStageBytes = kTile * 512;  // boxes of rows, each [k, v][half][row][64 channels]
 constexpr int kStages = 3;
 constexpr int kMaxSplits = 16;
 constexpr int kPitch = kD + 4;                // partial outputs: fragment stores hit distinct banks
@@ -34,15 +33,17 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr size_t kSmem = kStages * kStageBytes + 1024;  // the start is rounded up to 1024 bytes
 
 struct Params {
-    CUtensorMap tm_kv;  // boxes of min(page_size, 64) rows x 64 channels
+    // The pool as [k, v][half of the channels][row][64 channels], boxes of both halves of both:
+    CUtensorMap tm_kv;    // of min(page_size, 64) rows
+    CUtensorMap tm_edge;  // of 16 rows
     WindowAttentionArgs a;
-    int32_t G, kv_rows;
+    int32_t G, kv_rows, page_shift;
     float c;  // scale log2 e, > 0
 };
 
 struct Shared {
     uint64_t full[kStages], empty[kStages];
-    int2 tile[kStages];       // first key; bits of the tile's pages that exist
+    int2 tile[kStages];       // first key; bit g: its keys 16 g .. have a page (and some row sees some)
     float2 ml[kWarps][16];    // each warp's maximum reference and sum, by row
     uint32_t abort, tainted;
 };
@@ -84,34 +85,53 @@ __device__ __forceinline__ void arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Fetches tiles [from, to) of the request's key tiles.
+// Whether some row of a request (tokens p0 .. last) must not see some of the keys [j, j + n).
+__device__ __forceinline__ bool some_hidden(const WindowAttentionArgs &a, int32_t j, int32_t n, int32_t p0, int32_t last) {
+    return j + n - 1 > p0 || (last - j >= a.window && j + n > a.sinks);
+}
+
+__device__ __forceinline__ void tma_load_box(uint32_t dst, const void *tmap, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %2, %3, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(y), "r"(0), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Fetches tiles [from, to) of the request's key tiles: whole pages (up to a tile), except that of a
+// tile on an edge only the groups of 16 keys come that some row sees (a window of 1024 and 4 first
+// tokens over pages of 64 would otherwise read 12 % more).
 __device__ void produce(const Params &p, Shared &sh, unsigned char *sm, const AttnRequest &req, const AttnKeys &keys,
                         int32_t h, int32_t from, int32_t to) {
     const int lane = threadIdx.x & 31;
-    const int32_t page = p.a.cache.page_size, box = min(page, kTile), boxes = kTile / box;
-    // lane = ((box, k or v), half): rows of one page, 64 channels
-    const int half = lane & 1, kv = lane >> 1 & 1, b = lane >> 2;
+    const WindowAttentionArgs &a = p.a;
+    const int32_t page_shift = p.page_shift, p0 = req.len - req.n, last = req.len - 1;
     int32_t i = from;
     bool ok = true;
     for (; i < to; ++i) {
         const int32_t n = i - from, s = n % kStages, j0 = keys.tile(i) * kTile;
+        const bool edge = some_hidden(a, j0, kTile, p0, last);
+        // lane b: box b of the tile
+        const int32_t shift = edge ? 4 : min(page_shift, 6), j = j0 + (lane << shift);
+        const bool mine = lane << shift < kTile;
         int32_t id = -1;
-        const int32_t j = j0 + b * box;
-        if (b < boxes) id = attn_page(p.a.cache, req.row, req.len - 1, j / page);
+        if (mine && (!edge || (j <= last && (p0 - j - 16 < a.window - 1 || j < a.sinks))))
+            id = attn_page(a.cache, req.row, last, j >> page_shift);
         const uint32_t exist = __ballot_sync(0xffffffffu, id >= 0);
         if (n >= kStages && !(ok = wait(sh, &sh.empty[s], (n / kStages - 1) & 1, p, 96))) break;
         if (lane == 0) {
-            uint32_t bits = 0;
-            for (int u = 0; u < boxes; ++u) bits |= (exist >> (4 * u) & 1) << u;
-            sh.tile[s] = make_int2(j0, (int)bits);
+            // a bit for 16 keys
+            const uint32_t bits = shift == 4   ? exist
+                                  : shift == 5 ? (exist & 1) * 3 + (exist & 2) * 6
+                                               : exist * 15;
+            sh.tile[s] = make_int2(j0, (int)(bits | (uint32_t)shift << 8));
             mbar_arrive_expect_tx(&sh.full[s], kStageBytes);
         }
         __syncwarp();
-        if (b < boxes) {
+        if (mine) {
             const int32_t y = id < 0 ? p.kv_rows  // out of range: zeros
-                                     : ((id * 2 + kv) * p.a.num_kv_heads + h) * page + j % page;
-            tma_load_2d(smem_u32(sm + s * kStageBytes + kv * 2 * kHalf + half * kHalf + b * box * 128), &p.tm_kv,
-                        64 * half, y, &sh.full[s]);
+                                     : ((id * 2 * a.num_kv_heads + h) << page_shift) + (j & ((1 << page_shift) - 1));
+            tma_load_box(smem_u32(sm + s * kStageBytes + (lane << (shift + 9))), edge ? &p.tm_edge : &p.tm_kv, y, &sh.full[s]);
         }
     }
     if (!ok && lane == 0)  // gave up: the copies in flight still land before the CTA leaves
@@ -184,23 +204,24 @@ __global__ void __launch_bounds__(kThreads, 2) attention_split_kernel(const __gr
             if (!wait(sh, &sh.full[s], (n / kStages) & 1, p, 97)) break;
             const int2 info = sh.tile[s];
             const int32_t j0 = info.x;
-            const int32_t box = min(a.cache.page_size, kTile);
             // some row must not see some key of the tile
-            const bool masked = (uint32_t)info.y != low_bits(kTile / box) || j0 + kTile - 1 > p0 ||
-                                (req.len - 1 - j0 >= a.window && j0 + kTile > a.sinks);
-            const uint32_t k_addr = smem_u32(sm + s * kStageBytes), v_addr = k_addr + 2 * kHalf;
+            const bool masked = (info.y & 15) != 15 || some_hidden(a, j0, kTile, p0, req.len - 1);
+            const uint32_t stage = smem_u32(sm + s * kStageBytes), shift = info.y >> 8, half_bytes = 128u << shift;
 #pragma unroll
             for (int step = 0; step < kSteps; ++step) {
                 const int key0 = 16 * (group * kSteps + step);  // of the tile
+                // its box, and its place in it
+                const uint32_t k_addr = stage + ((key0 >> shift) << (shift + 9)) + ((key0 & ((1 << shift) - 1)) << 7);
+                const uint32_t v_addr = k_addr + 2 * half_bytes;
                 float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
                 {
                     // matrices: keys 0-7 / 8-15 x channels 0-7 / 8-15 of the step
-                    const int row = key0 + (lane & 7) + (lane >> 4) * 8;
+                    const int row = (lane & 7) + (lane >> 4) * 8;
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         const int chunk = 2 * (c & 3) + (lane >> 3 & 1);
                         uint32_t b[4];
-                        ldmatrix4(k_addr + (c >> 2) * kHalf + row * 128 + ((chunk ^ (row & 7)) << 4), b);
+                        ldmatrix4(k_addr + (c >> 2) * half_bytes + row * 128 + ((chunk ^ (row & 7)) << 4), b);
                         mma16816(sc[0], q[c], b[0], b[1]);
                         mma16816(sc[1], q[c], b[2], b[3]);
                     }
@@ -214,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_split_kernel(const __gr
                         for (int e = 0; e < 2; ++e) {
                             const int kk = key0 + 8 * t + 2 * (lane & 3) + e;
                             const int32_t j = j0 + kk;
-                            const bool mapped = info.y >> (kk / box) & 1;
+                            const bool mapped = info.y >> (key0 / 16) & 1;
 #pragma unroll
                             for (int u = 0; u < 2; ++u)
                                 if (!(mapped && attn_visible(pos[u], j, a.window, a.sinks))) sc[t][2 * u + e] = -INFINITY;
@@ -265,12 +286,12 @@ __global__ void __launch_bounds__(kThreads, 2) attention_split_kernel(const __gr
                     }
                 }
                 // matrices: keys 0-7 / 8-15 x channels 0-7 / 8-15, transposed
-                const int row = key0 + (lane & 15);
+                const int row = lane & 15;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     const int chunk = 2 * (c & 3) + (lane >> 4);
                     uint32_t b[4];
-                    ldmatrix4_trans(v_addr + (c >> 2) * kHalf + row * 128 + ((chunk ^ (row & 7)) << 4), b);
+                    ldmatrix4_trans(v_addr + (c >> 2) * half_bytes + row * 128 + ((chunk ^ (row & 7)) << 4), b);
                     if (masked) {
 #pragma unroll
                         for (int t = 0; t < 4; ++t) {
@@ -367,7 +388,10 @@ cudaError_t launch_window_attention_split(const WindowAttentionArgs &a, cudaStre
     p.G = a.num_q_heads / a.num_kv_heads;
     p.kv_rows = (int32_t)(2ll * a.cache.num_pages * a.num_kv_heads * a.cache.page_size);
     p.c = (float)((double)a.scale * 1.4426950408889634);
-    if (!encode_kv_map(&p.tm_kv, a, a.cache.page_size < kTile ? a.cache.page_size : kTile)) return cudaErrorNotSupported;
+    p.page_shift = a.cache.page_size == 16 ? 4 : a.cache.page_size == 32 ? 5 : a.cache.page_size == 64 ? 6 : 7;
+    if (!encode_kv_box_map(&p.tm_kv, a, a.cache.page_size < kTile ? a.cache.page_size : kTile) ||
+        !encode_kv_box_map(&p.tm_edge, a, 16))
+        return cudaErrorNotSupported;
     // Split until the GPU has about four CTAs an SM, as long as each keeps two tiles or more.
     const int64_t reach = (int64_t)a.window + a.max_tokens - 1 + a.sinks;  // keys of a request, at most
     const int64_t held = (int64_t)a.cache.table_width * a.cache.page_size;

@@ -706,6 +706,18 @@ bool encode_kv_map(CUtensorMap *m, const WindowAttentionArgs &a, int32_t box_row
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_kv_box_map(CUtensorMap *m, const WindowAttentionArgs &a, int32_t box_rows) {
+    auto fn = tensor_map_encoder();
+    if (fn == nullptr) return false;
+    const CacheArgs &c = a.cache;
+    const cuuint64_t dims[4] = {64, 2ull * c.num_pages * a.num_kv_heads * c.page_size, 2, 2};
+    const cuuint64_t strides[3] = {kD * 2, 128, (cuuint64_t)a.num_kv_heads * c.page_size * kD * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 2, 2}, estr[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(a.kv_pool), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_window_attention_tc(const WindowAttentionArgs &a, cudaStream_t stream) {
     Params p;
     p.a = a;
