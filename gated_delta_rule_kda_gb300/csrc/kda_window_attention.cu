@@ -1,6 +1,6 @@
 // Sliding-window attention over the paged cache, in fp32 on the FMA units.
 //
-// A work item is 64 rows of one request and key/value head; a row is a (token, query head of the
+// A work item is 32 rows of one request and key/value head; a row is a (token, query head of the
 // group) pair, so that the group's heads share each key and value.  Over tiles of 64 keys:
 //   s = scale q k^T;  m' = max(m, max s);  l <- l e^(m - m') + sum e^(s - m');
 //   o <- o e^(m - m') + e^(s - m') v;  at the end o / l   (l = 0: no key was visible, o = 0)
@@ -20,19 +20,22 @@ namespace {
 
 using tc::smem_u32;
 
-constexpr int kThreads = 256;
-constexpr int kTile = 64;              // rows of an item, keys of a tile
+constexpr int kThreads = 128;
+constexpr int kRows = 32;              // of an item
+constexpr int kTile = 64;              // keys of a tile
+constexpr int kWarps = kThreads / 32;
 constexpr int kPitch = kD + 4;         // q, k rows: float4 reads of 16 rows hit distinct banks
 constexpr int kPitchP = kTile + 4;
 constexpr int kMaxSplits = 8;
-constexpr size_t kSmem = sizeof(float) * (2 * kTile * kPitch + kTile * kD + kTile * kPitchP);
+constexpr size_t kSmem = sizeof(float) * ((kRows + kTile) * kPitch + kTile * kD + kRows * kPitchP);  // two CTAs an SM
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) attention_rows_kernel(const WindowAttentionArgs a, int32_t splits) {
+__global__ void __launch_bounds__(kThreads, 2) attention_rows_kernel(const WindowAttentionArgs a, int32_t splits) {
     extern __shared__ float4 smem4[];
-    float *sq = reinterpret_cast<float *>(smem4), *sk = sq + kTile * kPitch;
+    float *sq = reinterpret_cast<float *>(smem4), *sk = sq + kRows * kPitch;
     float *sv = sk + kTile * kPitch, *sp = sv + kTile * kD;
-    __shared__ uint64_t s_mapped;  // bit j: key j of the tile has a page
+    __shared__ int64_t s_at[kTile];   // the tile's keys as rows of the pool, or -1
+    __shared__ uint32_t s_mapped[2];  // bit j: key j of the tile has a page
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int32_t G = a.num_q_heads / a.num_kv_heads, h = blockIdx.y;
     const CacheArgs &cache = a.cache;
@@ -42,17 +45,23 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const WindowAt
     int32_t index;
     AttnWalk walk;
     const int32_t rank = (int32_t)cluster_rank();  // a cluster is one item
-    if (!walk.find(a, blockIdx.x / splits, G, kTile, req, index)) return;  // the same for the whole cluster
-    const int32_t rows = req.n * G, r0 = index * kTile;
+    if (!walk.find(a, blockIdx.x / splits, G, kRows, req, index)) return;  // the same for the whole cluster
+    const int32_t rows = req.n * G, r0 = index * kRows;
     const int32_t p0 = req.len - req.n;  // index of the request's first token
     const T *q = static_cast<const T *>(a.q), *pool = static_cast<const T *>(a.kv_pool);
 
-    for (int i = tid; i < kTile * (kD / 4); i += kThreads) {
-        const int r = i / (kD / 4), c = i % (kD / 4) * 4, row = r0 + r;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (row < rows)
-            x = load4(q + ((int64_t)(req.first + row / G) * a.num_q_heads + h * G + row % G) * kD + c);
-        *reinterpret_cast<float4 *>(sq + r * kPitch + c) = x;
+    // A warp loads whole rows of 128 channels.
+    const int warp = tid >> 5, c4 = (tid & 31) * 4;
+    {
+        float4 x[kRows / kWarps];
+#pragma unroll
+        for (int i = 0; i < kRows / kWarps; ++i) {
+            const int32_t row = r0 + warp + kWarps * i;
+            x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row < rows) x[i] = load4(q + ((int64_t)(req.first + row / G) * a.num_q_heads + h * G + row % G) * kD + c4);
+        }
+#pragma unroll
+        for (int i = 0; i < kRows / kWarps; ++i) *reinterpret_cast<float4 *>(sq + (warp + kWarps * i) * kPitch + c4) = x[i];
     }
 
     int32_t p[4];  // indices of this thread's rows 4 ty + i (past the last row: -1 sees nothing)
@@ -70,33 +79,41 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const WindowAt
         for (int c = 0; c < 8; ++c) o[i][c] = 0.f;
     }
 
-    const AttnKeys keys(p0 + r0 / G, p0 + (min(r0 + kTile, rows) - 1) / G, a.window, a.sinks, kTile);
-    const int32_t end = p0 + (min(r0 + kTile, rows) - 1) / G + 1;  // no row sees a key from here on
+    const AttnKeys keys(p0 + r0 / G, p0 + (min(r0 + kRows, rows) - 1) / G, a.window, a.sinks, kTile);
+    const int32_t end = p0 + (min(r0 + kRows, rows) - 1) / G + 1;  // no row sees a key from here on
     const int32_t tiles = keys.count(), last = (int32_t)((int64_t)tiles * (rank + 1) / splits);
     for (int32_t it = (int32_t)((int64_t)tiles * rank / splits); it < last; ++it) {
         const int32_t j0 = keys.tile(it) * kTile;
         __syncthreads();  // the previous tile has been used
-        if (tid == 0) s_mapped = 0;
-        __syncthreads();
-        for (int i = tid; i < kTile * (kD / 4); i += kThreads) {
-            const int r = i / (kD / 4), c = i % (kD / 4) * 4, j = j0 + r;
-            float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
+        if (tid < kTile) {  // where the tile's keys lie, and which of them exist
+            const int32_t j = j0 + tid;
+            int64_t at = -1;
             if (j < end) {  // end <= len <= table_width * page_size
                 const int32_t page = cache.page_table[(int64_t)req.row * cache.table_width + j / cache.page_size];
-                if ((uint32_t)page < (uint32_t)cache.num_pages) {
-                    const int64_t kv_stride = (int64_t)a.num_kv_heads * cache.page_size * kD;
-                    const T *src = pool + (int64_t)page * 2 * kv_stride +
-                                   ((int64_t)h * cache.page_size + j % cache.page_size) * kD + c;
-                    kx = load4(src);
-                    vx = load4(src + kv_stride);
-                    if (c == 0) atomicOr(reinterpret_cast<unsigned long long *>(&s_mapped), 1ull << r);
-                }
+                if ((uint32_t)page < (uint32_t)cache.num_pages)
+                    at = ((int64_t)page * 2 * a.num_kv_heads + h) * cache.page_size + j % cache.page_size;
             }
-            *reinterpret_cast<float4 *>(sk + r * kPitch + c) = kx;
-            *reinterpret_cast<float4 *>(sv + r * kD + c) = vx;
+            s_at[tid] = at;
+            const uint32_t exist = __ballot_sync(0xffffffffu, at >= 0);
+            if ((tid & 31) == 0) s_mapped[warp] = exist;
         }
         __syncthreads();
-        const uint64_t mapped = s_mapped;
+        const int64_t kv_stride = (int64_t)a.num_kv_heads * cache.page_size * kD;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            float4 x[kTile / kWarps];
+#pragma unroll
+            for (int i = 0; i < kTile / kWarps; ++i) {
+                const int64_t at = s_at[warp + kWarps * i];
+                x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (at >= 0) x[i] = load4(pool + at * kD + kv * kv_stride + c4);
+            }
+#pragma unroll
+            for (int i = 0; i < kTile / kWarps; ++i)
+                *reinterpret_cast<float4 *>(kv ? sv + (warp + kWarps * i) * kD + c4 : sk + (warp + kWarps * i) * kPitch + c4) = x[i];
+        }
+        __syncthreads();
+        const uint64_t mapped = (uint64_t)s_mapped[1] << 32 | s_mapped[0];
 
         float s[4][4];  // rows 4 ty + i, keys tx + 16 j
 #pragma unroll
@@ -185,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const WindowAt
         }
         return;
     }
-    // The partial results take the place of k; the cluster's CTAs join 64 / splits rows each.
+    // The partial results take the place of k; the cluster's CTAs join kRows / splits rows each.
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -195,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) attention_rows_kernel(const WindowAt
         if (tx == 0) *reinterpret_cast<float2 *>(dst + kD) = make_float2(m[i], l[i]);
     }
     cluster_sync();
-    for (int32_t r = rank * (kTile / splits) + (tid >> 5); r < (rank + 1) * (kTile / splits); r += kThreads / 32) {
+    for (int32_t r = rank * (kRows / splits) + warp; r < (rank + 1) * (kRows / splits); r += kWarps) {
         const int32_t row = r0 + r, lane = tid & 31;
         if (row >= rows) break;
         const uint32_t mine = smem_u32(sk + r * kPitch);
@@ -225,12 +242,13 @@ template <typename T>
 cudaError_t launch_rows(const WindowAttentionArgs &a, cudaStream_t stream) {
     // each request rounds up to whole items at most once
     const int64_t rows = (int64_t)a.cache.total_tokens * (a.num_q_heads / a.num_kv_heads);
-    const int64_t items = (rows + kTile - 1) / kTile + a.cache.batch;
-    // Split an item's keys over a cluster until the GPU is full, with two tiles a CTA or more.
-    const int64_t reach = (int64_t)a.window + a.sinks + kTile, held = (int64_t)a.cache.table_width * a.cache.page_size;
-    const int64_t tiles = (reach < held ? reach : held) / kTile;
+    const int64_t items = (rows + kRows - 1) / kRows + a.cache.batch;
+    // Split an item's keys over a cluster as far as the CTAs are all resident at once (two an SM) and
+    // keep two tiles each.
+    const int64_t reach = (int64_t)a.window + a.sinks + kRows, held = (int64_t)a.cache.table_width * a.cache.page_size;
+    const int64_t tiles = ((reach < held ? reach : held) + kTile - 1) / kTile;
     int splits = 1;
-    while (splits < kMaxSplits && items * a.num_kv_heads * splits < 2ll * device_sm_count() && tiles >= 4 * splits) splits *= 2;
+    while (splits < kMaxSplits && items * a.num_kv_heads * splits <= device_sm_count() && tiles >= 4 * splits) splits *= 2;
     if (items * splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     return launch_clusters(attention_rows_kernel<T>, dim3((unsigned)(items * splits), (unsigned)a.num_kv_heads), splits,
                            kThreads, kSmem, stream, a, (int32_t)splits);
