@@ -11,7 +11,9 @@
 // A work item is 2 x 128 rows of one request and key/value head; a row is a (token, query head of
 // the group) pair, so that the heads of a group share every key and value, and a tile of 128 rows
 // spans only 128 / G tokens: the window's edges then cost few masked tiles.  Keys come in tiles of
-// 128, those of the sinks first.  One CTA per SM stays and takes items in turn.
+// 128, those of the sinks first.  The grid has a CTA an item; one an SM starts and, when done with its
+// item, takes over one that has not started (cluster launch control), so that SMs that are slower at the
+// moment take fewer.
 //   warp 8      TMA: q of the next item, then k, v tiles page by page into a ring of five 32 KB
 //               stages (a page that does not exist is an out-of-range box, which reads as zeros)
 //   warps 9, 10 issue the MMAs of row tiles 0 and 1: s = q k^T into TMEM, o += p v with p read from
@@ -40,7 +42,7 @@ constexpr int kTile = 128;                    // rows of a row tile, keys of a k
 constexpr uint32_t kTileBytes = kTile * kD * 2;
 constexpr int kStages = 5;
 constexpr int kItems = 4;                     // work items announced ahead
-constexpr int kTaintWords = 32;
+constexpr int kTainted = 200;                 // marked items a CTA keeps; it takes no more work near the end
 constexpr int kItemReaders = 11;              // warps that read them: softmax, MMA, values
 constexpr int kWarpTma = 8, kWarpMma = 9, kWarpScrub = 11;
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -52,7 +54,7 @@ enum Bar {
     B_QFULL, B_QEMPTY, B_KVFULL, B_RAW = B_KVFULL + kStages, B_KVEMPTY = B_RAW + kStages,
     B_CLEAN = B_KVEMPTY + kStages,
     B_S = B_CLEAN + kStages, B_P = B_S + 2, B_O = B_P + 4, B_ITEM = B_O + 2, B_ITEMFREE = B_ITEM + kItems,
-    B_DRAIN = B_ITEMFREE + kItems, B_TURN = B_DRAIN + 2, B_COUNT = B_TURN + 2
+    B_DRAIN = B_ITEMFREE + kItems, B_TURN = B_DRAIN + 2, B_NEXT = B_TURN + 2, B_COUNT
 };
 
 constexpr uint32_t SM_Q = 0, SM_KV = 2 * kTileBytes, SM_END = SM_KV + kStages * kTileBytes;
@@ -108,8 +110,10 @@ struct Shared {
     Item items[kItems];
     int2 tiles[8];  // by key tile % 8: its first key; bit i: its page i exists, bit 16 + r: some row of row tile r
                     // must not see some key of it
-    uint32_t tainted[kTaintWords + 1];  // bit k: masked tiles of item k held a non-finite value (the last
-                                        // word: of an item past those)
+    uint4 next;                  // the answer to the load warp's request for more work
+    uint32_t work[kItems];       // numbers of the items in `items`
+    uint32_t tainted[kTainted];  // numbers of the items whose masked tiles held a non-finite value
+    uint32_t tainted_count;
     uint32_t tmem;
     uint32_t abort;
 };
@@ -167,6 +171,7 @@ __device__ __forceinline__ Item find_item(const Params &p, AttnWalk &walk, int64
     Item it;
     int32_t index;
     it.n = -1;
+    if (w / Hkv < walk.before) walk = AttnWalk();  // work comes in order, as a rule
     if (!walk.find(p.a, w / Hkv, 1, tokens, req, index)) return it;
     // the last tokens of a request first: with little out of the window they see most keys
     const int32_t t0 = ((req.n + tokens - 1) / tokens - 1 - index) * tokens;
@@ -183,6 +188,29 @@ __device__ __forceinline__ Item find_item(const Params &p, AttnWalk &walk, int64
     return it;
 }
 
+// Cluster launch control: asks the scheduler to withdraw a CTA of this grid that has not started.  The
+// answer comes to shared memory: whether there was one, and which.
+__device__ __forceinline__ void request_work(uint4 *answer, uint64_t *bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(answer)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ bool taken_work(const uint4 *answer, uint32_t &w) {
+    uint32_t ok, x;
+    asm volatile(
+        "{\n\t.reg .b128 a;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 a, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t}\n"
+        : "=r"(ok), "=r"(x)
+        : "r"(smem_u32(answer))
+        : "memory");
+    if (ok) w = x;
+    return ok != 0;
+}
+
 __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
     const int lane = threadIdx.x & 31;
     const int32_t page = p.a.cache.page_size, pages = kTile / page;  // pages of a tile
@@ -190,18 +218,20 @@ __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
     Ring ring;
     uint32_t loads = 0, items = 0, tiles = 0, uses[2] = {0, 0};  // bit s: parity of the uses of KVFULL, RAW + s
     bool ok = true;
-    AttnWalk walk;
-    AttnRequest req;
-    int64_t w = blockIdx.x;
-    for (uint32_t k = 0; ok; ++k, w += gridDim.x) {
-        const Item it = find_item(p, walk, w, req);
-        if (k >= kItems && !(ok = wait(sh, B_ITEMFREE + k % kItems, (k / kItems - 1) & 1, p))) break;
-        if (lane == 0) {
-            sh.items[k % kItems] = it;
-            mbar_arrive(sh.bar + B_ITEM + k % kItems);
+    uint32_t asked = 0;  // requests for more work
+    bool asking = false;
+    // The grid has a CTA an item: those that have not started are taken over, one at a time.
+    const auto ask = [&] {
+        const uint32_t marked = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(&sh.tainted_count), 0);
+        asking = marked + 2 * kItems < kTainted;
+        if (asking && lane == 0) {
+            fence_proxy_async_smem();  // the last answer has been read
+            mbar_arrive_expect_tx(sh.bar + B_NEXT, 16);
+            request_work(&sh.next, sh.bar + B_NEXT);
         }
-        if (it.n < 0) break;
-        if (it.n == 0) continue;
+    };
+    // q, k and v of one item
+    const auto load_item = [&](const Item &it) {
         const bool two = it.two(p);
         const auto load_q = [&] {  // when the last item's scores are done
             if (items > 0 && !wait(sh, B_QEMPTY, (items - 1) & 1, p)) return false;
@@ -251,10 +281,46 @@ __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
                 if (i == 0 && kv == 0 && !(ok = load_q())) break;  // q behind the first keys
             }
             ++tiles;
+            if (ok && i == 0) ask();  // behind the first loads
+        }
+        return ok;
+    };
+    AttnWalk walk;
+    AttnRequest req;
+    uint32_t w = blockIdx.x;
+    bool more = true;
+    for (uint32_t k = 0; ok && more;) {
+        const Item it = find_item(p, walk, w, req);
+        if (it.n >= 0) {
+            if (k >= kItems && !(ok = wait(sh, B_ITEMFREE + k % kItems, (k / kItems - 1) & 1, p))) break;
+            if (lane == 0) {
+                sh.items[k % kItems] = it;
+                sh.work[k % kItems] = w;
+                mbar_arrive(sh.bar + B_ITEM + k % kItems);
+            }
+            ++k;
+        }
+        if (it.n <= 0) ask();
+        else if (!(ok = load_item(it))) break;
+        if (asking) {
+            if (!(ok = wait(sh, B_NEXT, asked & 1, p))) break;
+            ++asked;
+            more = taken_work(&sh.next, w);
+            __syncwarp();
+        } else {
+            more = false;
+        }
+        if (!more) {
+            if (k >= kItems && !(ok = wait(sh, B_ITEMFREE + k % kItems, (k / kItems - 1) & 1, p))) break;
+            if (lane == 0) {
+                sh.items[k % kItems].n = -1;
+                mbar_arrive(sh.bar + B_ITEM + k % kItems);
+            }
         }
     }
     if (!ok && lane == 0) {  // gave up: the copies in flight still land before the CTA leaves
         if (items > 0) mbar_wait_bounded(sh.bar + B_QFULL, (items - 1) & 1, kWaitNs);
+        mbar_wait_bounded(sh.bar + B_NEXT, asked & 1, kWaitNs);
         for (int s = 0; s < kStages; ++s) {
             mbar_wait_bounded(sh.bar + B_KVFULL + s, ~(uses[0] >> s) & 1, kWaitNs);
             mbar_wait_bounded(sh.bar + B_RAW + s, ~(uses[1] >> s) & 1, kWaitNs);
@@ -384,8 +450,10 @@ __device__ void scrub_warp(const Params &p, Shared &sh, unsigned char *sm) {
     Items queue;
     while (const Item *at = queue.next(sh, p)) {
         const Item it = *at;
+        const uint32_t work = sh.work[(queue.k - 1) % kItems];
         __syncwarp();
         if (t == 0) queue.done(sh);
+        bool marked = false;
         for (int32_t i = 0; i < it.n; ++i) {
             ring.next();  // k
             const Ring v = ring;
@@ -416,13 +484,14 @@ __device__ void scrub_warp(const Params &p, Shared &sh, unsigned char *sm) {
                 }
             }
             __syncwarp();
-            if (bad) {
-                const uint32_t k = queue.k - 1;
-                atomicOr(&sh.tainted[min(k / 32, (uint32_t)kTaintWords)], 1u << (k & 31));
-            }
+            marked |= __any_sync(0xffffffffu, bad != 0);
             fence_proxy_async_smem();
             __syncwarp();
             if (t == 0) mbar_arrive(sh.bar + B_CLEAN + v.stage);
+        }
+        if (marked && t == 0 && sh.tainted_count < kTainted) {  // (always: no work is taken near the end)
+            sh.tainted[sh.tainted_count] = work;
+            *reinterpret_cast<volatile uint32_t *>(&sh.tainted_count) = sh.tainted_count + 1;
         }
     }
 }
@@ -628,14 +697,12 @@ __device__ void softmax_warps(const Params &p, Shared &sh, int r) {
 __device__ __noinline__ void redo_tainted(const Params &p, const Shared &sh, int warp) {
     AttnWalk walk;
     AttnRequest req;
-    for (uint32_t k = 0;; ++k) {
-        const Item it = find_item(p, walk, blockIdx.x + (int64_t)k * gridDim.x, req);
-        if (it.n < 0) return;
-        const bool marked = k < 32 * kTaintWords ? sh.tainted[k / 32] >> (k & 31) & 1 : sh.tainted[kTaintWords] != 0;
-        for (int32_t row = warp; marked && row < it.tokens * p.G; row += kThreads / 32) {
+    for (uint32_t k = 0; k < sh.tainted_count; ++k) {
+        const Item it = find_item(p, walk, sh.tainted[k], req);
+        for (int32_t row = warp; row < it.tokens * p.G; row += kThreads / 32) {
             const int32_t token = row / p.G;
             attn_row(p.a, (int64_t)(it.first + token) * p.a.num_q_heads + it.h * p.G + row % p.G, it.h, it.row,
-                          it.p_min + token);
+                     it.p_min + token);
         }
     }
 }
@@ -652,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                                   : i >= B_ITEMFREE && i < B_DRAIN                  ? kItemReaders
                                                                                     : 1);
         sh.abort = 0;
-        for (int i = 0; i <= kTaintWords; ++i) sh.tainted[i] = 0;
+        sh.tainted_count = 0;
         fence_mbar_init();
     }
     if (warp == kWarpMma) {
@@ -674,9 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
     }
     __syncthreads();
     if (warp == kWarpMma) tmem_dealloc(sh.tmem, 512);
-    uint32_t any = 0;
-    for (int i = 0; i <= kTaintWords; ++i) any |= sh.tainted[i];
-    if (any != 0) redo_tainted(p, sh, warp);  // after every store of the first pass
+    if (sh.tainted_count != 0) redo_tainted(p, sh, warp);  // after every store of the first pass
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -738,8 +803,8 @@ cudaError_t launch_window_attention_tc(const WindowAttentionArgs &a, cudaStream_
         return cudaErrorNotSupported;
     // each request rounds up to whole items at most once
     const int64_t items = ((int64_t)a.cache.total_tokens / (2 * p.tq) + a.cache.batch) * a.num_kv_heads;
-    const int64_t sms = device_sm_count();
-    return launch_serial(attention_tc_kernel, dim3((unsigned)(items < sms ? items : sms)), kThreads, SM_DYN, stream, p);
+    if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    return launch_serial(attention_tc_kernel, dim3((unsigned)items), kThreads, SM_DYN, stream, p);
 }
 
 }  // namespace kda
