@@ -9,7 +9,7 @@
 // ca and cb: with half-split pairs the pieces are the two halves of four pairs (channel i and
 // i + rotary_dim / 2), with interleaved pairs they are neighbours; either way both channels of a
 // pair are in one lane, and the channels that do not rotate fall to the lanes past rotary_dim / 8.
-// Measured (28,000 tokens, 96 + 8 + 8 heads, bf16 into the cache, 1.74 GB): 284 us, 6.12 TB/s, 0.90
+// Measured (30,195 tokens, 96 + 8 + 8 heads, bf16 into the cache, 1.74 GB): 284 us, 6.12 TB/s, 0.90
 // of the measured copy bandwidth; with 256-thread blocks 321 us, four rows a group 307, the rows in
 // two batches of four 344: the loads in flight set the pace.
 #include "kda_common.cuh"

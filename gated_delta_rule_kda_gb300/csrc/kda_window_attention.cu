@@ -8,6 +8,8 @@
 // scores and 4 x 8 outputs, so that each shared-memory read feeds two to four FMAs.  A key that a
 // row does not see takes no part: its score is replaced (never computed with), its probability of
 // zero skips the product with v, and keys past the end or without a page are loaded as zeros.
+// Measured: 3 requests of 40 to 300 tokens, window 257 + 3, 6 and 2 heads: 28 us (64-row items 35, without
+// clusters 38); 4 us of FMAs a key tile and CTA.
 // With few items a cluster of CTAs shares each one's key tiles, and joins the partial results
 // through distributed shared memory.
 #include <cfloat>
