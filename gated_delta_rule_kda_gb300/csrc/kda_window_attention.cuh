@@ -99,6 +99,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+    return n;
+}
 // The address of this CTA's shared address `addr` in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t remote(uint32_t addr, uint32_t rank) {
     uint32_t r;

@@ -13,7 +13,8 @@
 // spans only 128 / G tokens: the window's edges then cost few masked tiles.  Keys come in tiles of
 // 128, those of the sinks first.  The grid has a CTA an item; one an SM starts and, when done with its
 // item, takes over one that has not started (cluster launch control), so that SMs that are slower at the
-// moment take fewer.
+// moment take fewer.  With few items a cluster of up to eight CTAs shares the key tiles of one, and joins
+// the partial results through distributed shared memory (in an order that the sizes alone decide).
 //   warp 8      TMA: q of the next item, then k, v tiles page by page into a ring of five 32 KB
 //               stages (a page that does not exist is an out-of-range box, which reads as zeros)
 //   warps 9, 10 issue the MMAs of row tiles 0 and 1: s = q k^T into TMEM, o += p v with p read from
@@ -47,6 +48,7 @@ constexpr int kTile = 128;                    // rows of a row tile, keys of a k
 constexpr uint32_t kTileBytes = kTile * kD * 2;
 constexpr int kStages = 5;
 constexpr int kItems = 4;                     // work items announced ahead
+constexpr int kPitchO = kD + 4;               // floats of a row's partial result: o, m, l
 constexpr int kTainted = 200;                 // marked items a CTA keeps; it takes no more work near the end
 constexpr int kItemReaders = 11;              // warps that read them: softmax, MMA, values
 constexpr int kWarpTma = 8, kWarpMma = 9, kWarpScrub = 11;
@@ -97,9 +99,12 @@ struct Item {
     int32_t h, row;            // kv head, row of the table
     int32_t p_min, p_max;      // indices of its first and last token
     int32_t n;                 // key tiles; < 0: no more items
-    int32_t sink_tiles, skip;  // tile i starts at key 128 (i < sink_tiles ? i : i + skip)
+    int32_t from;              // the first of its tiles among those of the keys its tokens see
+    int32_t sink_tiles, skip;  // of those, tile i starts at key 128 (i < sink_tiles ? i : i + skip)
 
-    __device__ __forceinline__ int32_t key(int32_t i) const { return kTile * (i < sink_tiles ? i : i + skip); }
+    __device__ __forceinline__ int32_t key(int32_t i) const {
+        return kTile * (from + i < sink_tiles ? from + i : from + i + skip);
+    }
     __device__ __forceinline__ bool two(const Params &p) const { return tokens > p.tq; }  // a second row tile
     // Some row of the item must not see some key of the tile that starts at j0.
     __device__ __forceinline__ bool masked(int32_t j0, const Params &p) const {
@@ -188,6 +193,7 @@ __device__ __forceinline__ Item find_item(const Params &p, AttnWalk &walk, int64
     it.p_max = it.p_min + it.tokens - 1;
     const AttnKeys keys(it.p_min, it.p_max, p.a.window, p.a.sinks, kTile);
     it.n = keys.count();
+    it.from = 0;
     it.sink_tiles = keys.sink_tiles;
     it.skip = keys.low_tile - keys.sink_tiles;
     return it;
@@ -216,6 +222,7 @@ __device__ __forceinline__ bool taken_work(const uint4 *answer, uint32_t &w) {
     return ok != 0;
 }
 
+template <bool kSplit>
 __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
     const int lane = threadIdx.x & 31;
     const int32_t page = p.a.cache.page_size, pages = kTile / page;  // pages of a tile
@@ -227,6 +234,7 @@ __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
     bool asking = false;
     // The grid has a CTA an item: those that have not started are taken over, one at a time.
     const auto ask = [&] {
+        if (kSplit) return;
         const uint32_t marked = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(&sh.tainted_count), 0);
         asking = marked + 2 * kItems < kTainted;
         if (asking && lane == 0) {
@@ -292,10 +300,15 @@ __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
     };
     AttnWalk walk;
     AttnRequest req;
-    uint32_t w = blockIdx.x;
+    uint32_t w = kSplit ? blockIdx.x / cluster_size() : blockIdx.x;
     bool more = true;
     for (uint32_t k = 0; ok && more;) {
-        const Item it = find_item(p, walk, w, req);
+        Item it = find_item(p, walk, w, req);
+        if (kSplit && it.n > 0) {  // this CTA's share of the item's tiles
+            const int32_t rank = (int32_t)cluster_rank(), size = (int32_t)cluster_size(), n = it.n;
+            it.from = (int32_t)((int64_t)n * rank / size);
+            it.n = (int32_t)((int64_t)n * (rank + 1) / size) - it.from;
+        }
         if (it.n >= 0) {
             if (k >= kItems && !(ok = wait(sh, B_ITEMFREE + k % kItems, (k / kItems - 1) & 1, p))) break;
             if (lane == 0) {
@@ -523,6 +536,23 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
     return fmaxf(fmaxf(a, b), fmaxf(__uint_as_float(s[30]), __uint_as_float(s[31])));
 }
 
+// A split item's partial results of one row: o as it is, then m and l.
+__device__ __forceinline__ float *partial_row(unsigned char *sm, int r, int row) {
+    return reinterpret_cast<float *>(sm + SM_KV) + (kTile * r + row) * kPitchO;
+}
+__device__ __forceinline__ void keep_partial(uint32_t o_tmem, bool any, float m, float l, float *dst) {
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        float o[32];
+        if (any) tmem_ld32(o_tmem + 32 * c, o);
+#pragma unroll
+        for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<float4 *>(dst + 32 * c + k) =
+                any ? make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    *reinterpret_cast<float2 *>(dst + kD) = make_float2(m, l);
+}
+
 // Writes a row tile's outputs.  Four lanes (rows) exchange 16-byte chunks so that each store covers
 // 64 contiguous bytes of eight rows; a row a thread, the 32 lines of every store kept the load/store
 // unit busy for 4,000 cycles an item.
@@ -576,7 +606,8 @@ __device__ __forceinline__ void store_rows(const Params &p, uint32_t o_tmem, boo
     }
 }
 
-__device__ void softmax_warps(const Params &p, Shared &sh, int r) {
+template <bool kSplit>
+__device__ void softmax_warps(const Params &p, Shared &sh, unsigned char *sm, int r) {
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
     const int row = 32 * quarter + lane;  // of the row tile
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
@@ -688,8 +719,15 @@ __device__ void softmax_warps(const Params &p, Shared &sh, int r) {
 
         if (n > 0) {
             if (!wait(sh, B_O + r, o_phase, p)) return;
+            // the partial results will lie where the other row tile's values do
+            if (kSplit && it->two(p) && !wait(sh, B_O + 1 - r, o_phase, p)) return;
             o_phase ^= 1;
             fence_after_sync();
+        }
+        if (kSplit) {
+            keep_partial(o_tmem, n > 0, m, l, partial_row(sm, r, row));
+            if (lane == 0) queue.done(sh);
+            continue;
         }
         store_rows(p, o_tmem, n > 0, l, static_cast<__nv_bfloat16 *>(a.o) + ((int64_t)it->first * a.num_q_heads + it->h * p.G) * kD,
                    r * p.tq, it->tokens);
@@ -712,6 +750,53 @@ __device__ __noinline__ void redo_tainted(const Params &p, const Shared &sh, int
     }
 }
 
+// Joins a split item: its rows go round the cluster's warps, four channels a lane.
+__device__ __noinline__ void join_split(const Params &p, Shared &sh, unsigned char *sm, int warp) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t size = cluster_size(), rank = cluster_rank();
+    AttnWalk walk;
+    AttnRequest req;
+    const Item it = find_item(p, walk, blockIdx.x / size, req);
+    if (it.n < 0) return;  // the whole cluster
+    uint32_t failed = 0, tainted = 0;
+    if (lane < (int)size) {
+        failed = remote_u32(remote(smem_u32(&sh.abort), lane));
+        tainted = remote_u32(remote(smem_u32(&sh.tainted_count), lane));
+    }
+    if (__any_sync(0xffffffffu, failed != 0)) return;
+    tainted = __any_sync(0xffffffffu, tainted != 0);
+    for (int32_t row = rank * (kThreads / 32) + warp; row < it.tokens * p.G; row += size * (kThreads / 32)) {
+        const int32_t token = row / p.G, g = row - token * p.G;
+        const int64_t q_row = (int64_t)(it.first + token) * p.a.num_q_heads + it.h * p.G + g;
+        if (tainted) {
+            attn_row(p.a, q_row, it.h, it.row, it.p_min + token);
+            continue;
+        }
+        const int r = token >= p.tq ? 1 : 0;
+        const uint32_t mine = smem_u32(partial_row(sm, r, (token - r * p.tq) * p.G + g));
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < (int)size) ml = remote_float2(remote(mine + kD * 4, lane));
+        float top = ml.x;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2_approx((ml.x - top) * p.c);  // (a NaN sum stays one)
+        float sum = w * ml.y;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (uint32_t s = 0; s < size; ++s) {
+            const float ws = __shfl_sync(0xffffffffu, w, s);
+            const float4 x = remote_float4(remote(mine + 16 * lane, s));
+            acc = make_float4(fmaf(ws, x.x, acc.x), fmaf(ws, x.y, acc.y), fmaf(ws, x.z, acc.z), fmaf(ws, x.w, acc.w));
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        store4(static_cast<__nv_bfloat16 *>(p.a.o) + q_row * kD + 4 * lane,
+               make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    }
+}
+
+template <bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_constant__ Params p) {
     extern __shared__ unsigned char dyn[];
     __shared__ Shared sh;
@@ -737,16 +822,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
     fence_after_sync();
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-        softmax_warps(p, sh, warp >> 2);
+        softmax_warps<kSplit>(p, sh, sm, warp >> 2);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-        if (warp == kWarpTma) tma_warp(p, sh, sm);
+        if (warp == kWarpTma) tma_warp<kSplit>(p, sh, sm);
         else if (warp == kWarpScrub) scrub_warp(p, sh, sm);
         else if ((threadIdx.x & 31) == 0) mma_thread(p, sh, sm, warp - kWarpMma);
     }
     __syncthreads();
     if (warp == kWarpMma) tmem_dealloc(sh.tmem, 512);
-    if (sh.tainted_count != 0) redo_tainted(p, sh, warp);  // after every store of the first pass
+    if constexpr (kSplit) {
+        cluster_sync();
+        join_split(p, sh, sm, warp);
+        __syncwarp();
+        cluster_sync();  // no CTA leaves while another reads its partials
+    } else {
+        if (sh.tainted_count != 0) redo_tainted(p, sh, warp);  // after every store of the first pass
+    }
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -806,10 +898,20 @@ cudaError_t launch_window_attention_tc(const WindowAttentionArgs &a, cudaStream_
            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorNotSupported;
-    // each request rounds up to whole items at most once
-    const int64_t items = ((int64_t)a.cache.total_tokens / (2 * p.tq) + a.cache.batch) * a.num_kv_heads;
+    // sum of ceil(n_b / tokens) over the requests, at most
+    const int64_t tokens = 2 * p.tq;
+    const int64_t items = (a.cache.total_tokens + a.cache.batch * (tokens - 1)) / tokens * a.num_kv_heads;
     if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    return launch_serial(attention_tc_kernel, dim3((unsigned)items), kThreads, SM_DYN, stream, p);
+    // Few items: a cluster shares each one's key tiles, as long as all CTAs are resident at once (a
+    // cluster of 4 or 8 does not fill every group of SMs) and keep two tiles or more.
+    const int64_t reach = (int64_t)a.window + tokens - 1 + a.sinks;
+    const int64_t held = (int64_t)a.cache.table_width * a.cache.page_size;
+    const int64_t tiles = ((reach < held ? reach : held) + kTile - 1) / kTile;
+    const int64_t sms = device_sm_count();
+    int splits = 1;
+    while (splits < 8 && items * splits * 2 <= sms - (splits == 1 ? 0 : sms / 5) && tiles >= 4 * splits) splits *= 2;
+    if (splits == 1) return launch_serial(attention_tc_kernel<false>, dim3((unsigned)items), kThreads, SM_DYN, stream, p);
+    return launch_clusters(attention_tc_kernel<true>, dim3((unsigned)(items * splits)), splits, kThreads, SM_DYN, stream, p);
 }
 
 }  // namespace kda
