@@ -268,10 +268,12 @@ cudaError_t launch_window_attention(const WindowAttentionArgs &a, cudaStream_t s
     // positive scale leaves alone; any other scale (and fp32) runs on the FMA units.
     const bool tensor = a.dtype == KDA_BF16 && a.scale > 0.f && a.scale <= FLT_MAX;
     if (!tensor) return launch_window_attention_rows(a, stream);
-    // Up to 64 rows a request and kv head fit the split kernel (which wants them in one grid of
-    // at most 65535 requests); more make a 128-row tile worth its while.
+    // Up to 32 rows a request and kv head go to the split kernel (which wants them in one grid of at
+    // most 65535 requests); more make a 128-row tile worth its while.  Measured at 8 kv heads, 8 query
+    // heads each, split / tensor-core kernel: 4 tokens (32 rows), 64 requests at window 1024: 72 / 87 us,
+    // 4 requests over 60,000 keys: 160 / 343 us; 8 tokens (64 rows): 129 / 87 and 335 / 344 us.
     const int64_t rows = (int64_t)a.max_tokens * (a.num_q_heads / a.num_kv_heads);
-    return rows <= 64 && a.cache.batch <= 65535 ? launch_window_attention_split(a, stream)
+    return rows <= kSplitRows && a.cache.batch <= 65535 ? launch_window_attention_split(a, stream)
                                                 : launch_window_attention_tc(a, stream);
 }
 

@@ -212,6 +212,7 @@ __device__ __noinline__ inline void attn_row(const WindowAttentionArgs &a, int64
 
 cudaError_t launch_window_attention_rows(const WindowAttentionArgs &a, cudaStream_t stream);
 cudaError_t launch_window_attention_tc(const WindowAttentionArgs &a, cudaStream_t stream);
+constexpr int kSplitRows = 32;  // most rows of a request and kv head that the split kernel takes
 cudaError_t launch_window_attention_split(const WindowAttentionArgs &a, cudaStream_t stream);
 
 // A tensor map over kv_pool as rows of 128 channels, 64 channels x box_rows a box, 128-byte swizzle.

@@ -7,10 +7,10 @@
 //   M = max m_i;  o = (sum_i 2^(c (m_i - M)) o_i) / (sum_i 2^(c (m_i - M)) l_i)
 // in one launch, with no workspace, in an order that the sizes alone decide.
 //
-// A row is a (token, query head of the group) pair; max_tokens G <= 64 of them, in 1, 2 or 4 blocks
+// A row is a (token, query head of the group) pair; max_tokens G <= 32 of them, in one or two blocks
 // of 16.  A producer warp fetches k and v by TMA, page by page, into a ring of 32 KB stages; of the
 // four others, warp w takes row block w % kBlocks and every key group w / kBlocks of a tile, in steps
-// of 16 keys on the warp-wide tensor instruction (m16n8k16): with at most 64 rows the 128-row MMA would
+// of 16 keys on the warp-wide tensor instruction (m16n8k16): with at most 32 rows the 128-row MMA would
 // idle, and the fragments of the 16-row one stay in registers from scores to outputs.  The running
 // maximum moves lazily, as in the prefill kernel.  Scores, m, l and o are fp32; p is rounded to bf16
 // for its product (at most 2^-8 of each weight).
@@ -407,7 +407,7 @@ cudaError_t launch_window_attention_split(const WindowAttentionArgs &a, cudaStre
     int splits = 1;
     while (splits < kMaxSplits && ctas * splits <= device_sm_count() && tiles >= 4 * splits) splits *= 2;
     const int64_t rows = (int64_t)a.max_tokens * p.G;
-    return rows <= 16 ? launch<1>(p, splits, stream) : rows <= 32 ? launch<2>(p, splits, stream) : launch<4>(p, splits, stream);
+    return rows <= 16 ? launch<1>(p, splits, stream) : launch<kSplitRows / 16>(p, splits, stream);
 }
 
 }  // namespace kda

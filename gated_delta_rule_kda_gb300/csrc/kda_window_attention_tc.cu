@@ -29,7 +29,7 @@
 // a key tile and row tile, 512 cycles each at its full rate).
 // Measured: 2 x 16,384 tokens behind cached ones, window 4096 + 16, 32 query and 8 kv heads: 1.42 ms,
 // 1378 TFLOP/s (0.74 of a large bf16 GEMM's rate); 8192 tokens, window 1024 + 4, 96 and 8 heads: 0.45 to
-// 0.56 ms, 0.86 to 0.69 PFLOP/s: of its ten key tiles an item four are on an edge, which costs a softmax
+// 0.575 ms, 0.86 to 0.68 PFLOP/s: of its ten key tiles an item four are on an edge, which costs a softmax
 // warp about 1,700 cycles more.  Scores read from TMEM twice instead of held: 3.17 ms on the first; four
 // stages instead of five: 5 % slower; work in fixed turns: 1.44 ms and up to 0.60.
 #include <cuda.h>

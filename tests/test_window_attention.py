@@ -272,6 +272,28 @@ def test_decode_of_ragged_lengths_over_many_splits(kda):
             check(call(kda, q, c, new, window, sinks), q, c, new, window, sinks)
 
 
+@pytest.mark.parametrize("new,group", [([40], 4), ([9, 33, 0], 5), ([70], 1), ([2], 33)])
+@pytest.mark.parametrize("window,sinks", [(None, 0), (1500, 70)])
+@pytest.mark.parametrize("bad", [False, True])
+def test_short_steps_behind_long_rows(kda, new, group, window, sinks, bad):
+    """Few rows over many keys: CTAs share an item's keys and join their results.  With `bad`, a value of the
+    first request's first token is NaN: its other tokens see it too, the other requests do not."""
+    c = build_cache([n + 3000 + 100 * i for i, n in enumerate(new)], 32, 2, BF16, seed=47)
+    q = queries(sum(new), 2 * group, BF16, 47)
+    clean = {**c, "pool": c["pool"].clone()}
+    if bad:
+        j = 3000
+        c["pool"][int(c["table"][int(c["slot"][0]), j // 32]), 1, 0, j % 32, 7] = float("nan")
+    o = call(kda, q, c, new, window, sinks)
+    assert torch.equal(torch.isnan(o), torch.isnan(call(kda, q, c, new, window, sinks)))
+    if bad:
+        seen = torch.zeros_like(o, dtype=torch.bool)
+        seen[: new[0], :group, 7] = True
+        assert torch.equal(torch.isnan(o), seen)
+        o = torch.where(seen, call(kda, q, clean, new, window, sinks), o)
+    check(o, q, clean, new, window, sinks)
+
+
 def test_large_scores(kda):
     """Scores of some hundreds, growing and falling along the row: the running maximum keeps every
     exponential in range.  q and k are scaled so that products are exact in bf16."""
