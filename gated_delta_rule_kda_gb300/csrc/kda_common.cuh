@@ -52,13 +52,17 @@ inline int device_sm_count() {
 // everything before it is complete.  Takes one to two microseconds off a chain of short kernels.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// A kernel whose dynamic shared memory may, with what it declares itself, pass the default 48 KB is given
+// `most` (the largest size that any of its calls needs) once per call: the setting is the process's, so
+// one that followed the call's own size could be lowered by another thread between setting and launch.
+template <typename... Params>
+cudaError_t allow_smem(void (*kernel)(Params...), size_t most) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+}
+
 template <typename... Params, typename... Args>
 cudaError_t launch_serial(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
                           const Args &...args) {
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -285,6 +285,18 @@ __global__ void __launch_bounds__(kReleaseThreads) pages_release_kernel(const Pa
     for (int64_t j = from + threadIdx.x; j < to; j += kReleaseThreads) row[j] = -1;
 }
 
+// Shared memory of a plan: a bit a page, and for a fork a bit a row.  Above 32 KB (with the static
+// arrays still well inside the default 48) the kernel gets the most that the calls accept, 160 KB.
+constexpr size_t kPlanSmem = ((1 << 20) + (1 << 18)) / 8;
+template <typename Args>
+cudaError_t launch_plan(void (*kernel)(Args), size_t smem, cudaStream_t stream, const Args &a) {
+    if (smem > 32 * 1024) {
+        const cudaError_t e = allow_smem(kernel, kPlanSmem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_serial(kernel, dim3(1), kPlanThreads, smem, stream, a);
+}
+
 unsigned copy_grid(int64_t units) {
     const int64_t most = (int64_t)device_sm_count() * 64;
     return (unsigned)(units < 1 ? 1 : units < most ? units : most);
@@ -302,7 +314,7 @@ cudaError_t launch_pages_copy(const PageMoves &m, cudaStream_t stream) {
 cudaError_t launch_pages_fork(const PageForkArgs &a, cudaStream_t stream) {
     if (a.moves.n == 0) return cudaSuccess;
     const size_t smem = 4 * (((size_t)a.moves.num_pages + 31) / 32 + ((size_t)a.table_rows + 31) / 32);
-    const cudaError_t e = launch_serial(pages_fork_plan_kernel, dim3(1), kPlanThreads, smem, stream, a);
+    const cudaError_t e = launch_plan(pages_fork_plan_kernel, smem, stream, a);
     return e == cudaSuccess ? launch_pages_copy(a.moves, stream) : e;
 }
 
@@ -313,7 +325,7 @@ cudaError_t launch_pages_release(const PageReleaseArgs &a, cudaStream_t stream) 
 
 cudaError_t launch_pages_compact(const PageCompactArgs &a, cudaStream_t stream) {
     const size_t smem = 4 * (((size_t)a.moves.num_pages + 31) / 32);
-    const cudaError_t e = launch_serial(pages_compact_plan_kernel, dim3(1), kPlanThreads, smem, stream, a);
+    const cudaError_t e = launch_plan(pages_compact_plan_kernel, smem, stream, a);
     if (e != cudaSuccess) return e;
     // at most min(L, P - L) <= P / 2 pages move
     const unsigned grid = copy_grid(copy_units(a.moves, (a.moves.num_pages + 1) / 2));

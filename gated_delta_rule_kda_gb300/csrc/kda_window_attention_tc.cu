@@ -910,7 +910,11 @@ cudaError_t launch_window_attention_tc(const WindowAttentionArgs &a, cudaStream_
     const int64_t sms = device_sm_count();
     int splits = 1;
     while (splits < 8 && items * splits * 2 <= sms - (splits == 1 ? 0 : sms / 5) && tiles >= 4 * splits) splits *= 2;
-    if (splits == 1) return launch_serial(attention_tc_kernel<false>, dim3((unsigned)items), kThreads, SM_DYN, stream, p);
+    if (splits == 1) {
+        const cudaError_t e = allow_smem(attention_tc_kernel<false>, SM_DYN);
+        return e == cudaSuccess ? launch_serial(attention_tc_kernel<false>, dim3((unsigned)items), kThreads, SM_DYN, stream, p)
+                                : e;
+    }
     return launch_clusters(attention_tc_kernel<true>, dim3((unsigned)(items * splits)), splits, kThreads, SM_DYN, stream, p);
 }
 

@@ -1,4 +1,8 @@
 """Copy, fork, release and compaction of cache pages: whole numbers and bytes, all exact."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -180,3 +184,31 @@ def test_fork_then_attention_sees_the_same_row(kda):
     kda.kda_pages_compact(c["pool"][None], c["table"])
     assert torch.equal(ask(parent), want)
     assert kda.kda_get_device_status()[0] == 0
+
+
+BOUNDARY = """
+import torch
+from gated_delta_rule_kda_gb300 import kda
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+# the fork's plan holds a bit a page and a bit a row, the compaction's a bit a page, both 128 bytes beside them
+for P, R in ((392128, 33), (392160, 33), (392161, 33), (393152, 33), (393153, 33)):
+    pool = torch.zeros((1, P, 4), dtype=torch.int32, device="cuda")
+    pool[0, 7], table, kv_len = 9, torch.full((R, 1), -1, dtype=torch.int32, device="cuda"), i32([0] * R)
+    table[2, 0], kv_len[2] = 7, 5
+    kda.kda_pages_fork(pool, table, kv_len, i32([2]), i32([4]), 16)
+    assert table[4, 0].item() == 0 and kv_len[4].item() == 5 and bool((pool[0, 0] == 9).all()), P
+for P in (392192, 392193, 393216, 393217):
+    pool = torch.zeros((1, P, 4), dtype=torch.int32, device="cuda")
+    pool[0, P - 1] = 9
+    table, live = kda.kda_pages_compact(pool, i32([[P - 1]]))
+    assert live.item() == 1 and table.item() == 0 and bool((pool[0, 0] == 9).all()), P
+assert kda.kda_get_device_status()[0] == 0
+"""
+
+
+def test_plans_around_the_default_shared_memory_limit(kda):
+    """Pools whose bitmap and the plan's few static bytes lie below, at and above 48 KB together, in a process
+    that has made no larger call before."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", BOUNDARY], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
