@@ -206,9 +206,12 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_plan_kernel(const Pag
             if ((uint32_t)c >= (uint32_t)R || c == p) continue;
             int32_t *to = a.page_table + (int64_t)c * M;
             const bool given = a.src[f] != kRefused;
-            const int32_t fresh = a.dst[f], at = fresh >= 0 ? a.kv_len[c] / a.page_size : -1;
+            const int32_t fresh = a.dst[f], length = a.kv_len[c];
+            const int32_t at = fresh >= 0 ? length / a.page_size : -1;
+            // what the parent has mapped past its tokens stays its own: both rows would append there
+            const int32_t shared = given ? length / a.page_size + (length % a.page_size != 0) : 0;
             for (int32_t j = tid & 31; j < M; j += 32)
-                to[j] = !given ? -1 : j == at ? fresh : a.page_table[(int64_t)p * M + j];
+                to[j] = j >= shared ? -1 : j == at ? fresh : a.page_table[(int64_t)p * M + j];
         }
         __syncthreads();
     }

@@ -730,7 +730,8 @@ def _pages_workspace(workspace, P, rows, device):
 
 def kda_pages_fork(pool, page_table, kv_len, parent, child, page_size, *, workspace=None, stream=None):
     """Rows child[i] become branches of rows parent[i], in place in page_table and kv_len: whole
-    pages shared, a part-filled last page copied to a fresh one in every layer of pool."""
+    pages shared, a part-filled last page copied to a fresh one in every layer of pool, no entry
+    past the parent's tokens."""
     F = parent.numel()
     R, M = page_table.shape
     if child.numel() != F or kv_len.numel() != R:

@@ -703,8 +703,10 @@ size_t kda_pages_workspace_size(int32_t num_pages, int32_t table_rows);
 /*
  * kda_pages_fork - row child[i] becomes a branch of row parent[i]: the same
  * length, sharing its whole pages, with a page of its own in place of a
- * part-filled last one (copied in every layer).  A page is free when no row of
- * the table names it; what a child row named before is released by the call.
+ * part-filled last one (copied in every layer).  Entries past the parent's
+ * tokens (pages reserved ahead, or left when its kv_len was lowered) are not
+ * shared: they are -1 in the child.  A page is free when no row of the table
+ * names it; what a child row named before is released by the call.
  * Fresh pages are the lowest free ones, in the order of i.
  *
  *   num_forks   F in [0, R];  parent, child [F] int32; no row is a child twice,

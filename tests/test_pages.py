@@ -212,3 +212,56 @@ def test_plans_around_the_default_shared_memory_limit(kda):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", BOUNDARY], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("length,shared", [(32, 2), (20, 1), (0, 0), (1, 0), (64, 4), (63, 3)])
+def test_fork_takes_no_page_past_the_parent_s_tokens(kda, length, shared):
+    """A parent with pages mapped past its tokens (reserved ahead, or left when its length was lowered): the child
+    shares those that are full and has a page of its own for a part-filled one; the rest stays the parent's."""
+    page, names = 16, [6, 1, 8, 3]
+    table = np.array([names, [-1] * 4, [2, 9, 9, -1]], np.int32)
+    pool = torch.arange(10 * 64, device="cuda", dtype=torch.int32).view(1, 10, 64)
+    want_row, want = [-1] * 4, pool.clone()
+    want_row[:shared] = names[:shared]
+    if length % page:
+        want_row[shared] = 0  # the lowest page that no row names
+        want[:, 0] = pool[:, names[shared]]
+    dt, dn = i32(table), i32([length, 7, 20])
+    kda.kda_pages_fork(pool, dt, dn, i32([0]), i32([1]), page)
+    assert dt.tolist() == [names, want_row, table[2].tolist()] and dn.tolist() == [length, length, 20]
+    assert torch.equal(pool, want)
+    assert kda.kda_get_device_status()[0] == 0
+
+
+@pytest.mark.parametrize("length", [32, 20])
+def test_branches_of_a_row_with_pages_ahead_append_apart(kda, length):
+    """Both rows grow across the page edge: each finds its own keys and values, and a branch that has not been given
+    a page yet is refused instead of writing the parent's."""
+    page, steps = 16, 20
+    g = torch.Generator(device="cuda")
+    g.manual_seed(length)
+    pool = torch.randn((1, 12, 2, 1, page, 128), generator=g, device="cuda")
+    table, kv_len = i32([[3, 4, 5, 6], [-1] * 4]), i32([length, 0])
+    kda.kda_pages_fork(pool, table, kv_len, i32([0]), i32([1]), page)
+    x = torch.randn((2, steps, 2, 1, 128), generator=g, device="cuda")  # row, step, key / value
+
+    def append(t, rows):
+        n = len(rows)
+        kda.kda_qk_norm_rope_append(x[rows, t, 0], x[rows, t, 0], x[rows, t, 1], None, None, pool[0], table, i32(rows),
+                                    i32(list(range(n + 1))), kv_len, norm=False)
+
+    spare = iter([10, 11])
+    for t in range(steps):
+        j = length + t
+        kv_len[:] = j + 1
+        if table[1, j // page].item() < 0:
+            before = pool.clone()
+            append(t, [1])
+            assert kda.kda_get_device_status()[0] == 6 and torch.equal(pool, before)
+            table[1, j // page] = next(spare)
+        append(t, [0, 1])
+    assert kda.kda_get_device_status()[0] == 0
+    for r in range(2):
+        for t in range(steps):
+            j = length + t
+            assert torch.equal(pool[0, table[r, j // page].item(), :, :, j % page], x[r, t])
