@@ -8,6 +8,7 @@ there is no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -208,6 +209,30 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+# What a call allocates belongs to the stream that it launches on: a block of the current stream's would
+# be handed out again at once when the caller drops it (a workspace: when the call returns), while the
+# other stream's kernels still use it.
+def _on(stream):
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _kept(t: torch.Tensor, stream) -> torch.Tensor:
+    """t, allocated for `stream`, not handed out again before what the caller's stream does with it is done."""
+    if stream is not None and t.is_cuda:
+        current = torch.cuda.current_stream(t.device)
+        if current != stream:
+            t.record_stream(current)
+    return t
+
+
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    return _kept(t, stream)
+
+
 def _check(fn: str, rc: int):
     if rc != KDA_OK:
         raise KdaError(fn, rc)
@@ -231,12 +256,12 @@ def kda_prefill(q, k, v, log_alpha, beta, cu_seqlens, S0=None, scale=DEFAULT_SCA
     N = cu_seqlens.shape[0] - 1
     out_dtype = out_dtype or q.dtype
     if o is None:
-        o = torch.empty((T, H, HEAD_DIM), dtype=out_dtype, device=q.device)
+        o = _empty((T, H, HEAD_DIM), out_dtype, q.device, stream)
     if S_final is None and want_state:
-        S_final = torch.empty((N, H, HEAD_DIM, HEAD_DIM), dtype=torch.float32, device=q.device)
+        S_final = _empty((N, H, HEAD_DIM, HEAD_DIM), torch.float32, q.device, stream)
     need = kda_prefill_workspace_size(N, T, H, q.dtype)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, torch.uint8, q.device, stream)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = getattr(_lib, _entry)(_dt(q), _dtype_code(o.dtype), N, T, H, _p(q), _p(k), _p(v),
                           _p(log_alpha), _p(beta), _p(S0), _p(cu_seqlens), float(scale), _p(o),
@@ -260,13 +285,14 @@ def checkpoint_offsets(cu_seqlens, every: int) -> torch.Tensor:
     return torch.cat([torch.zeros(1, dtype=torch.int64), counts.cumsum(0)]).to(torch.int32)
 
 
-def _checkpoint_args(cu_seqlens, H, every, ckpt_base, ckpt_states, device):
+def _checkpoint_args(cu_seqlens, H, every, ckpt_base, ckpt_states, device, stream):
+    with _on(stream):  # the offsets are read, and uploaded, in the order of the call's stream
+        base = checkpoint_offsets(cu_seqlens, every).to(device) if ckpt_base is None else ckpt_base
+        total = int(base[-1]) if ckpt_states is None else 0
     if ckpt_base is None:
-        ckpt_base = checkpoint_offsets(cu_seqlens, every).to(device)
+        ckpt_base = _kept(base, stream)
     if ckpt_states is None:
-        total = int(ckpt_base[-1])
-        ckpt_states = torch.empty((total, H, HEAD_DIM, HEAD_DIM), dtype=torch.float32,
-                                  device=device)
+        ckpt_states = _empty((total, H, HEAD_DIM, HEAD_DIM), torch.float32, device, stream)
     return ckpt_base, ckpt_states
 
 
@@ -281,15 +307,15 @@ def kda_prefill_with_checkpoints(q, k, v, log_alpha, beta, cu_seqlens, every, S0
     N = cu_seqlens.shape[0] - 1
     out_dtype = out_dtype or q.dtype
     if o is None:
-        o = torch.empty((T, H, HEAD_DIM), dtype=out_dtype, device=q.device)
+        o = _empty((T, H, HEAD_DIM), out_dtype, q.device, stream)
     if S_final is None and want_state:
-        S_final = torch.empty((N, H, HEAD_DIM, HEAD_DIM), dtype=torch.float32, device=q.device)
+        S_final = _empty((N, H, HEAD_DIM, HEAD_DIM), torch.float32, q.device, stream)
     if every:
         ckpt_base, ckpt_states = _checkpoint_args(cu_seqlens, H, every, ckpt_base, ckpt_states,
-                                                  q.device)
+                                                  q.device, stream)
     need = kda_prefill_workspace_size(N, T, H, q.dtype)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, torch.uint8, q.device, stream)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     rc = getattr(_lib, _entry)(
         _dt(q), _dtype_code(o.dtype), N, T, H, _p(q), _p(k), _p(v), _p(log_alpha), _p(beta),
@@ -317,7 +343,7 @@ def kda_decode_step(q, k, v, log_alpha, beta, S_inout, scale=DEFAULT_SCALE, *, o
     B, H, _ = q.shape
     out_dtype = out_dtype or q.dtype
     if o is None:
-        o = torch.empty((B, H, HEAD_DIM), dtype=out_dtype, device=q.device)
+        o = _empty((B, H, HEAD_DIM), out_dtype, q.device, stream)
     rc = getattr(_lib, _entry)(_dt(q), _dtype_code(o.dtype), B, H, _p(q), _p(k), _p(v),
                                _p(log_alpha), _p(beta), _p(S_inout), float(scale), _p(o),
                                _stream(stream))
@@ -338,11 +364,11 @@ def kda_frontend(qp, kp, vp, conv_w, z, A, b, beta_logit, cu_seqlens, l2_eps=1e-
     T, H, _ = qp.shape
     N = cu_seqlens.shape[0] - 1
     dev = qp.device
-    q_hat = torch.empty((T, H, HEAD_DIM), dtype=out_dtype, device=dev)
-    k_hat = torch.empty_like(q_hat)
-    v_out = torch.empty_like(q_hat)
-    log_alpha = torch.empty((T, H, HEAD_DIM), dtype=torch.float32, device=dev)
-    beta = torch.empty((T, H), dtype=torch.float32, device=dev)
+    q_hat = _empty((T, H, HEAD_DIM), out_dtype, dev, stream)
+    k_hat = _empty(q_hat.shape, out_dtype, dev, stream)
+    v_out = _empty(q_hat.shape, out_dtype, dev, stream)
+    log_alpha = _empty((T, H, HEAD_DIM), torch.float32, dev, stream)
+    beta = _empty((T, H), torch.float32, dev, stream)
     rc = getattr(_lib, _entry)(N, T, H, _p(qp), _p(kp), _p(vp), _p(conv_w), _p(z), _p(A), _p(b),
                            _p(beta_logit), _p(cu_seqlens), float(l2_eps),
                            _dtype_code(out_dtype), _p(q_hat), _p(k_hat), _p(v_out),
@@ -361,7 +387,7 @@ def kda_frontend_unbounded_decay(qp, kp, vp, conv_w, z, A, b, beta_logit, cu_seq
 def kda_output_gate(o_tilde, g, eps=1e-6, *, out_dtype=torch.bfloat16, out=None, stream=None):
     rows = o_tilde.numel() // HEAD_DIM
     if out is None:
-        out = torch.empty(o_tilde.shape, dtype=out_dtype, device=o_tilde.device)
+        out = _empty(o_tilde.shape, out_dtype, o_tilde.device, stream)
     rc = _lib.kda_output_gate(rows, _dt(o_tilde), _p(o_tilde), _p(g), float(eps),
                               _dtype_code(out.dtype), _p(out), _stream(stream))
     _check("kda_output_gate", rc)
@@ -380,12 +406,12 @@ def kda_layer_core(qp, kp, vp, conv_w, z, A, b, beta_logit, g, cu_seqlens, S0=No
     T, H, _ = qp.shape
     N = cu_seqlens.shape[0] - 1
     if o is None:
-        o = torch.empty((T, H, HEAD_DIM), dtype=out_dtype, device=qp.device)
+        o = _empty((T, H, HEAD_DIM), out_dtype, qp.device, stream)
     if S_final is None and want_state:
-        S_final = torch.empty((N, H, HEAD_DIM, HEAD_DIM), dtype=torch.float32, device=qp.device)
+        S_final = _empty((N, H, HEAD_DIM, HEAD_DIM), torch.float32, qp.device, stream)
     need = kda_layer_core_workspace_size(N, T, H)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=qp.device)
+        workspace = _empty(max(need, 16), torch.uint8, qp.device, stream)
     wbytes = workspace.numel() * workspace.element_size()
     rc = getattr(_lib, _entry)(N, T, H, _p(qp), _p(kp), _p(vp), _p(conv_w), _p(z), _p(A), _p(b),
                              _p(beta_logit), _p(g), _p(cu_seqlens), _p(S0), float(scale),
@@ -427,9 +453,9 @@ def kda_layer_core_fused(qp, kp, vp, conv_w, z, A, b, beta_logit, g, cu_seqlens,
     T, H, _ = qp.shape
     N = cu_seqlens.shape[0] - 1
     if o is None:
-        o = torch.empty((T, H, HEAD_DIM), dtype=out_dtype, device=qp.device)
+        o = _empty((T, H, HEAD_DIM), out_dtype, qp.device, stream)
     if S_final is None and want_state:
-        S_final = torch.empty((N, H, HEAD_DIM, HEAD_DIM), dtype=torch.float32, device=qp.device)
+        S_final = _empty((N, H, HEAD_DIM, HEAD_DIM), torch.float32, qp.device, stream)
     rc = getattr(_lib, _entry)(N, T, H, _p(qp), _p(kp), _p(vp), _p(conv_w), _p(z), _p(A),
                                _p(b), _p(beta_logit), _p(g), _p(cu_seqlens), _p(S0),
                                float(scale), float(l2_eps), float(rms_eps),
@@ -459,11 +485,11 @@ def kda_layer_core_fused_with_checkpoints(qp, kp, vp, conv_w, z, A, b, beta_logi
     T, H, _ = qp.shape
     N = cu_seqlens.shape[0] - 1
     if o is None:
-        o = torch.empty((T, H, HEAD_DIM), dtype=out_dtype, device=qp.device)
+        o = _empty((T, H, HEAD_DIM), out_dtype, qp.device, stream)
     if S_final is None and want_state:
-        S_final = torch.empty((N, H, HEAD_DIM, HEAD_DIM), dtype=torch.float32, device=qp.device)
+        S_final = _empty((N, H, HEAD_DIM, HEAD_DIM), torch.float32, qp.device, stream)
     ckpt_base, ckpt_states = _checkpoint_args(cu_seqlens, H, every, ckpt_base, ckpt_states,
-                                              qp.device)
+                                              qp.device, stream)
     rc = _lib.kda_layer_core_fused_with_checkpoints(
         N, T, H, _p(qp), _p(kp), _p(vp), _p(conv_w), _p(z), _p(A), _p(b), _p(beta_logit), _p(g),
         _p(cu_seqlens), _p(S0), float(scale), float(l2_eps), float(rms_eps),
@@ -485,7 +511,7 @@ def kda_decode_layer(qp, kp, vp, conv_w, z, A, b, beta_logit, g, slot, S_pool, c
     B, H, _ = qp.shape
     P = S_pool.shape[0]
     if o is None:
-        o = torch.empty((B, H, HEAD_DIM), dtype=out_dtype, device=qp.device)
+        o = _empty((B, H, HEAD_DIM), out_dtype, qp.device, stream)
     rc = _lib.kda_decode_layer(B, H, P, _p(qp), _p(kp), _p(vp), _p(conv_w), _p(z), _p(A), _p(b),
                                _p(beta_logit), _p(g), _p(slot), _p(S_pool), _p(conv_pool),
                                float(scale), float(l2_eps), float(rms_eps), _dtype_code(o.dtype),
@@ -505,7 +531,7 @@ def kda_decode_tokens(q, k, v, log_alpha, beta, cu_tokens, slot, S_pool, write_b
     P = S_pool.shape[0]
     out_dtype = out_dtype or q.dtype
     if o is None:
-        o = torch.empty((T, H, HEAD_DIM), dtype=out_dtype, device=q.device)
+        o = _empty((T, H, HEAD_DIM), out_dtype, q.device, stream)
     rc = _lib.kda_decode_tokens(_dt(q), _dtype_code(o.dtype), B, H, P, T, _p(cu_tokens),
                                 _p(slot), _p(q), _p(k), _p(v), _p(log_alpha), _p(beta),
                                 _p(S_pool), int(bool(write_back)), _p(S_final), float(scale),
@@ -526,7 +552,7 @@ def kda_decode_layer_tokens(qp, kp, vp, conv_w, z, A, b, beta_logit, g, cu_token
     B = slot.shape[0]
     P = S_pool.shape[0]
     if o is None:
-        o = torch.empty((T, H, HEAD_DIM), dtype=out_dtype, device=qp.device)
+        o = _empty((T, H, HEAD_DIM), out_dtype, qp.device, stream)
     rc = _lib.kda_decode_layer_tokens(B, H, P, T, _p(cu_tokens), _p(slot), _p(qp), _p(kp), _p(vp),
                                       _p(conv_w), _p(z), _p(A), _p(b), _p(beta_logit), _p(g),
                                       _p(S_pool), _p(conv_pool), int(bool(write_back)),
@@ -630,9 +656,9 @@ def kda_qk_norm_rope(q, k, rope, positions, q_weight=None, k_weight=None, eps=1e
     Returns (q_out, k_out)."""
     out_dtype = q_out.dtype if q_out is not None else out_dtype or q.dtype
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        q_out = _empty(q.shape, out_dtype, q.device, stream)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=out_dtype, device=k.device)
+        k_out = _empty(k.shape, out_dtype, k.device, stream)
     T = q.shape[0]
     if k.shape[0] != T or q_out.shape != q.shape or k_out.shape != k.shape or k_out.dtype != out_dtype \
             or k.dtype != q.dtype:
@@ -655,7 +681,7 @@ def kda_qk_norm_rope_append(q, k, v, rope, positions, kv_pool, page_table, slot,
     slot [B], cu_tokens [B+1].  Outputs have the pool's type.  Returns q_out."""
     P, pool_heads, page = _pool_shape(kv_pool)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=kv_pool.dtype, device=q.device)
+        q_out = _empty(q.shape, kv_pool.dtype, q.device, stream)
     T, k_shape, dtype = q.shape[0], k.shape, q.dtype
     if k_shape[0] != T or v.shape != k_shape or k_shape[1] != pool_heads or q_out.shape != q.shape \
             or q_out.dtype is not kv_pool.dtype or k.dtype is not dtype or v.dtype is not dtype:
@@ -682,7 +708,7 @@ def kda_window_attention(q, kv_pool, page_table, slot, cu_tokens, kv_len, window
     if kv_pool.dtype is not q.dtype:
         raise TypeError("q and kv_pool must have one type")
     if o is None:
-        o = torch.empty_like(q)
+        o = _empty(q.shape, q.dtype, q.device, stream)
     elif o.shape != q.shape or o.dtype is not q.dtype:
         raise ValueError("o must have q's shape and type")
     if d != HEAD_DIM:
@@ -720,10 +746,10 @@ def kda_pages_workspace_size(num_pages: int, table_rows: int) -> int:
     return int(_lib.kda_pages_workspace_size(num_pages, table_rows))
 
 
-def _pages_workspace(workspace, P, rows, device):
+def _pages_workspace(workspace, P, rows, device, stream):
     if workspace is None:
         n = kda_pages_workspace_size(P, rows)
-        workspace = torch.empty(n, dtype=torch.uint8, device=device)
+        workspace = _empty(n, torch.uint8, device, stream)
         return workspace, n
     return workspace, workspace.numel() * workspace.element_size()
 
@@ -737,7 +763,7 @@ def kda_pages_fork(pool, page_table, kv_len, parent, child, page_size, *, worksp
     if child.numel() != F or kv_len.numel() != R:
         raise ValueError("parent and child must have one length, kv_len one entry per table row")
     L, P, nbytes = _layers(pool)
-    workspace, wbytes = _pages_workspace(workspace, P, R, pool.device)
+    workspace, wbytes = _pages_workspace(workspace, P, R, pool.device, stream)
     pa, ch, pt, kl = _ptrs(_I32, parent, child, page_table, kv_len)
     _check("kda_pages_fork", _lib.kda_pages_fork(L, P, nbytes, page_size, R, M, F, pa, ch, pt, kl, _ptr(pool),
                                                  _ptr(workspace), wbytes, _raw_stream(stream, pool)))
@@ -764,8 +790,8 @@ def kda_pages_compact(pool, page_table, *, table_out=None, num_live=None, worksp
     if table_out.shape != page_table.shape:
         raise ValueError("table_out must have page_table's shape")
     if num_live is None:
-        num_live = torch.empty(1, dtype=_I32, device=pool.device)
-    workspace, wbytes = _pages_workspace(workspace, P, R, pool.device)
+        num_live = _empty(1, _I32, pool.device, stream)
+    workspace, wbytes = _pages_workspace(workspace, P, R, pool.device, stream)
     tin, tout, live = _ptrs(_I32, page_table, table_out, num_live)
     _check("kda_pages_compact", _lib.kda_pages_compact(L, P, nbytes, R, M, tin, tout, live, _ptr(pool),
                                                        _ptr(workspace), wbytes, _raw_stream(stream, pool)))
