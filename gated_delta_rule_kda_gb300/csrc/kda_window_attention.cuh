@@ -72,15 +72,17 @@ struct AttnWalk {
 };
 
 // Keys that the tokens p in [p_min, p_max] of a row of `len` tokens see: [0, sink_end) and
-// [low, end), in tiles of `tile` keys: tiles [0, sink_tiles) and [low_tile, end_tile).
+// [low, end), in tiles of `tile` keys: tiles [0, sink_tiles) and [low_tile, end_tile).  A row may be
+// 2^31 - 1 tokens long, so ends are rounded up to tiles in unsigned numbers.
 struct AttnKeys {
     int32_t sink_tiles, low_tile, end_tile;
     __device__ __forceinline__ AttnKeys(int32_t p_min, int32_t p_max, int32_t window, int32_t sinks,
                                         int32_t tile) {
         const int32_t end = max(p_max + 1, 0);
         const int32_t low = p_min < window ? 0 : p_min - window + 1;
-        end_tile = (end + tile - 1) / tile;
-        sink_tiles = (min(sinks, end) + tile - 1) / tile;
+        const auto tiles = [tile](int32_t n) { return (int32_t)(((uint32_t)n + tile - 1) / tile); };
+        end_tile = tiles(end);
+        sink_tiles = tiles(min(sinks, end));
         low_tile = min(max(low / tile, sink_tiles), max(end_tile, sink_tiles));
         end_tile = max(end_tile, low_tile);
     }

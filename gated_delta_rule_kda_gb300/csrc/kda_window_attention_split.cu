@@ -92,7 +92,7 @@ __device__ __forceinline__ void arrive(uint64_t *bar) {
 
 // Whether some row of a request (tokens p0 .. last) must not see some of the keys [j, j + n).
 __device__ __forceinline__ bool some_hidden(const WindowAttentionArgs &a, int32_t j, int32_t n, int32_t p0, int32_t last) {
-    return j + n - 1 > p0 || (last - j >= a.window && j + n > a.sinks);
+    return j + (n - 1) > p0 || (last - j >= a.window && j + (n - 1) >= a.sinks);
 }
 
 __device__ __forceinline__ void tma_load_box(uint32_t dst, const void *tmap, int y, uint64_t *bar) {
@@ -117,8 +117,9 @@ __device__ void produce(const Params &p, Shared &sh, unsigned char *sm, const At
         const int32_t n = i - from, s = n % kStages, j0 = keys.tile(i) * kTile;
         const bool edge = some_hidden(a, j0, kTile, p0, last);
         // lane b: box b of the tile
-        const int32_t shift = edge ? 4 : min(page_shift, 6), j = j0 + (lane << shift);
+        const int32_t shift = edge ? 4 : min(page_shift, 6);
         const bool mine = lane << shift < kTile;
+        const int32_t j = mine ? j0 + (lane << shift) : j0;
         int32_t id = -1;
         if (mine && (!edge || (j <= last && (p0 - j - 16 < a.window - 1 || j < a.sinks))))
             id = attn_page(a.cache, req.row, last, j >> page_shift);

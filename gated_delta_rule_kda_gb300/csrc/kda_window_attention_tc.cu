@@ -111,7 +111,7 @@ struct Item {
         return masked(j0, p_min, p_max, p);
     }
     static __device__ __forceinline__ bool masked(int32_t j0, int32_t lo, int32_t hi, const Params &p) {
-        return j0 + kTile - 1 > lo || (hi - j0 >= p.a.window && j0 + kTile > p.a.sinks);
+        return j0 + (kTile - 1) > lo || (hi - j0 >= p.a.window && j0 + (kTile - 1) >= p.a.sinks);
     }
 };
 

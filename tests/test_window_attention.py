@@ -312,3 +312,27 @@ def check_large(o, q, c, new):
     ref, a = attention64(q, c, new, 600, 3)
     err = np.abs(to64(o) - ref)
     assert (err <= 2.0 ** -8 * (a + np.abs(ref)) + 2.0 ** -8 * a).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("new", [1, 3, 70])
+@pytest.mark.parametrize("page,behind", [(64, 64), (16, 16), (16, 100)])
+def test_rows_up_to_the_last_index_that_is_accepted(kda, page, behind, new, dtype):
+    """A row that ends within 128 tokens of 2^31, with pages for its first tokens and for those near its end: the answer
+    of a short row that holds the same keys at the same places."""
+    far, near, window, sinks = 2 ** 31 - behind, 1024 - behind, 90, 5
+    small = build_cache([near], page, 2, dtype, seed=53)
+    q = queries(new, 6, dtype, 53)
+    width = (2 ** 31 - 1) // page
+    row = small["table"][small["slot"][0].item()]
+    table = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    table[0, 0] = row[0]
+    last = -(-near // page)
+    first = (near - new - window) // page
+    shift = (2 ** 31 - 1024) // page  # the end of the one row on the other's
+    table[0, first + shift: last + shift] = row[first:last]
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c = dict(pool=small["pool"], table=table, slot=zero, kv_len=zero + far)
+    o = call(kda, q, c, [new], window, sinks)
+    assert kda.kda_get_device_status()[0] == 0
+    check(o, q, small, [new], window, sinks)
