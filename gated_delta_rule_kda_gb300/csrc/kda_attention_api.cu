@@ -1,10 +1,17 @@
 // C ABI of the paged-cache operators (norm + rotation + append, sliding-window attention, page
 // management): argument validation on the host, then kernel launches.  Nothing here allocates.
+#include <atomic>
+
 #include "kda_common.cuh"
 
 using namespace kda;
 
 namespace {
+
+#ifdef KDA_DEBUG
+// Armed by kda_debug_inject_attention_timeout, consumed by the next kda_window_attention.
+std::atomic<int> g_withhold_attention{0};
+#endif
 
 constexpr int64_t kInt32Max = 0x7fffffffLL;
 
@@ -137,7 +144,19 @@ kda_status kda_window_attention(kda_dtype dtype, int32_t batch, int32_t total_to
         return KDA_ERR_UNSUPPORTED;
     WindowAttentionArgs a{dtype, max_tokens, num_q_heads, num_kv_heads, window, sinks, q, kv_pool,
                           scale, o, c, device_status()};
+#ifdef KDA_DEBUG
+    a.withhold = g_withhold_attention.exchange(0);
+#endif
     return from_cuda(launch_window_attention(a, static_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_debug_inject_attention_timeout(void) {
+#ifdef KDA_DEBUG
+    g_withhold_attention.store(1);
+    return KDA_OK;
+#else
+    return KDA_ERR_UNSUPPORTED;
+#endif
 }
 
 kda_status kda_pages_copy(int32_t num_layers, int32_t num_pages, int64_t page_bytes, int32_t n,

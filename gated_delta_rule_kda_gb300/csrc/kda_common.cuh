@@ -287,6 +287,9 @@ struct WindowAttentionArgs {
     void *o;  // [T][Hq][128]
     CacheArgs cache;
     DeviceStatus status;
+#ifdef KDA_DEBUG
+    int32_t withhold;  // test-only: the load warps fetch nothing, and waits give up after 1 ms
+#endif
 };
 
 // Moves of pages: pages dst[i] := pages src[i] of each layer, i < *count (or n when null).

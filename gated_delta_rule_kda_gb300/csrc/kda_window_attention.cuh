@@ -5,6 +5,7 @@
 #include <cuda.h>
 
 #include "kda_common.cuh"
+#include "tc_primitives.cuh"
 
 namespace kda {
 
@@ -129,6 +130,50 @@ __device__ __forceinline__ uint32_t remote_u32(uint32_t addr) {
     uint32_t x;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
     return x;
+}
+
+constexpr uint64_t kAttnWaitNs = 2000000000ull;  // longest wait
+__device__ __forceinline__ uint64_t attn_wait_ns(const WindowAttentionArgs &a) {
+#ifdef KDA_DEBUG
+    if (a.withhold) return 1000000ull;
+#endif
+    return kAttnWaitNs;
+}
+__device__ __forceinline__ bool attn_withhold(const WindowAttentionArgs &a) {
+#ifdef KDA_DEBUG
+    return a.withhold != 0;
+#else
+    return false;
+#endif
+}
+// Waits that run out.  `abort` is the CTA's word: set by the first to give up, seen by the other waits.
+__device__ __forceinline__ bool attn_given_up(const uint32_t *abort) {
+    return *reinterpret_cast<const volatile uint32_t *>(abort) != 0;
+}
+__device__ __forceinline__ void attn_give_up(uint32_t *abort, const WindowAttentionArgs &a, uint32_t what) {
+    atomicExch(abort, 1u);
+    record_status(a.status, KDA_ERR_DEVICE_TIMEOUT, what);
+}
+// A whole warp waits for a phase, for attn_wait_ns() at most or until another has given up.  Every lane gets the
+// same answer: what follows are full-mask exchanges and warp-wide instructions, which lanes that went
+// different ways could never meet in again.
+__device__ __forceinline__ bool attn_wait_warp(uint64_t *bar, uint32_t parity, uint32_t *abort,
+                                               const WindowAttentionArgs &a, uint32_t what) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    bool done = tc::mbar_try_wait(bar, parity);
+    if (__all_sync(kAll, done)) return true;
+    const uint64_t t0 = tc::global_timer_ns();
+    while (true) {
+        for (int i = 0; i < 4; ++i) {
+            done = done || tc::mbar_try_wait(bar, parity);
+            if (__all_sync(kAll, done)) return true;
+        }
+        if (__any_sync(kAll, attn_given_up(abort))) return false;
+        if (__any_sync(kAll, tc::global_timer_ns() - t0 > attn_wait_ns(a))) {
+            if ((threadIdx.x & 31) == 0) attn_give_up(abort, a, what);
+            return false;
+        }
+    }
 }
 
 // A launch of clusters of `size` CTAs along x (above 8: the non-portable size), which may come up early

@@ -34,7 +34,6 @@ constexpr uint32_t kStageBytes = kTile * 512;  // boxes of rows, each [k, v][hal
 constexpr int kStages = 3;
 constexpr int kMaxSplits = 16;
 constexpr int kPitch = kD + 4;                // partial outputs: fragment stores hit distinct banks
-constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr size_t kSmem = kStages * kStageBytes + 1024;  // the start is rounded up to 1024 bytes
 
 struct Params {
@@ -54,18 +53,7 @@ struct Shared {
 };
 
 __device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity, const Params &p, uint32_t what) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (true) {
-        for (int i = 0; i < 4; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        if (*reinterpret_cast<volatile uint32_t *>(&sh.abort)) return false;
-        if (global_timer_ns() - t0 > kWaitNs) {
-            atomicExch(&sh.abort, 1u);
-            record_status(p.a.status, KDA_ERR_DEVICE_TIMEOUT, what);
-            return false;
-        }
-    }
+    return attn_wait_warp(bar, parity, &sh.abort, p.a, what);
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
@@ -142,7 +130,7 @@ __device__ void produce(const Params &p, Shared &sh, unsigned char *sm, const At
     }
     if (!ok && lane == 0)  // gave up: the copies in flight still land before the CTA leaves
         for (int32_t k = max(from, i - kStages); k < i; ++k)
-            mbar_wait_bounded(&sh.full[(k - from) % kStages], ((k - from) / kStages) & 1, kWaitNs);
+            mbar_wait_bounded(&sh.full[(k - from) % kStages], ((k - from) / kStages) & 1, kAttnWaitNs);
 }
 
 template <int kBlocks>
@@ -178,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_split_kernel(const __gr
     const int32_t from = (int32_t)((int64_t)tiles * rank / splits), to = (int32_t)((int64_t)tiles * (rank + 1) / splits);
 
     if (warp == kWarps) {
-        produce(p, sh, sm, req, keys, h, from, to);
+        if (!attn_withhold(a)) produce(p, sh, sm, req, keys, h, from, to);
     } else {
         const int block = warp % kBlocks, group = warp / kBlocks;
         // this thread's two rows: 16 block + lane / 4 (+ 8)

@@ -52,7 +52,6 @@ constexpr int kPitchO = kD + 4;               // floats of a row's partial resul
 constexpr int kTainted = 200;                 // marked items a CTA keeps; it takes no more work near the end
 constexpr int kItemReaders = 11;              // warps that read them: softmax, MMA, values
 constexpr int kWarpTma = 8, kWarpMma = 9, kWarpScrub = 11;
-constexpr uint64_t kWaitNs = 2000000000ull;
 // 384 threads start with 168 registers; the softmax warps take 208, the others keep 88:
 // 256 * 208 + 128 * 88 = 384 * 168
 constexpr int kRegsSoftmax = 208, kRegsOther = 88;
@@ -128,20 +127,23 @@ struct Shared {
     uint32_t abort;
 };
 
-// Waits for a phase, giving up after kWaitNs or when another warp has given up.
-__device__ __forceinline__ bool wait(Shared &sh, int bar, uint32_t parity, const Params &p) {
+// One thread waits for a phase, giving up after attn_wait_ns() or when another warp has given up.
+__device__ __forceinline__ bool wait_one(Shared &sh, int bar, uint32_t parity, const Params &p) {
     if (mbar_try_wait(sh.bar + bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     while (true) {
         for (int i = 0; i < 4; ++i)
             if (mbar_try_wait(sh.bar + bar, parity)) return true;
-        if (*reinterpret_cast<volatile uint32_t *>(&sh.abort)) return false;
-        if (global_timer_ns() - t0 > kWaitNs) {
-            atomicExch(&sh.abort, 1u);
-            record_status(p.a.status, KDA_ERR_DEVICE_TIMEOUT, (uint32_t)(64 + bar));
+        if (attn_given_up(&sh.abort)) return false;
+        if (global_timer_ns() - t0 > attn_wait_ns(p.a)) {
+            attn_give_up(&sh.abort, p.a, (uint32_t)(64 + bar));
             return false;
         }
     }
+}
+// A warp does, all lanes to one verdict.
+__device__ __forceinline__ bool wait(Shared &sh, int bar, uint32_t parity, const Params &p) {
+    return attn_wait_warp(sh.bar + bar, parity, &sh.abort, p.a, (uint32_t)(64 + bar));
 }
 
 // The ring of k, v stages: tile loads in order, stage n % kStages, phase n / kStages.  A load
@@ -161,10 +163,13 @@ struct Ring {
 // The items in turn, for the warps that read them.
 struct Items {
     uint32_t k = 0;
-    // The next item, in its place until done(); null after the last one or when a wait gave up.
+    // The next item, in its place until done(); null after the last one or when a wait gave up.  A whole
+    // warp calls it, or (kOne) one thread for its warp.
+    template <bool kOne = false>
     __device__ __forceinline__ const Item *next(Shared &sh, const Params &p) {
         const uint32_t slot = k % kItems;
-        if (!wait(sh, B_ITEM + slot, k / kItems & 1, p)) return nullptr;
+        const bool there = kOne ? wait_one(sh, B_ITEM + slot, k / kItems & 1, p) : wait(sh, B_ITEM + slot, k / kItems & 1, p);
+        if (!there) return nullptr;
         ++k;
         return sh.items[slot].n >= 0 ? &sh.items[slot] : nullptr;
     }
@@ -318,6 +323,10 @@ __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
             }
             ++k;
         }
+        if (attn_withhold(p.a)) {
+            ok = false;
+            break;
+        }
         if (it.n <= 0) ask();
         else if (!(ok = load_item(it))) break;
         if (asking) {
@@ -337,11 +346,11 @@ __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
         }
     }
     if (!ok && lane == 0) {  // gave up: the copies in flight still land before the CTA leaves
-        if (items > 0) mbar_wait_bounded(sh.bar + B_QFULL, (items - 1) & 1, kWaitNs);
-        mbar_wait_bounded(sh.bar + B_NEXT, asked & 1, kWaitNs);
+        if (items > 0) mbar_wait_bounded(sh.bar + B_QFULL, (items - 1) & 1, kAttnWaitNs);
+        mbar_wait_bounded(sh.bar + B_NEXT, asked & 1, kAttnWaitNs);
         for (int s = 0; s < kStages; ++s) {
-            mbar_wait_bounded(sh.bar + B_KVFULL + s, ~(uses[0] >> s) & 1, kWaitNs);
-            mbar_wait_bounded(sh.bar + B_RAW + s, ~(uses[1] >> s) & 1, kWaitNs);
+            mbar_wait_bounded(sh.bar + B_KVFULL + s, ~(uses[0] >> s) & 1, kAttnWaitNs);
+            mbar_wait_bounded(sh.bar + B_RAW + s, ~(uses[1] >> s) & 1, kAttnWaitNs);
         }
     }
 }
@@ -390,20 +399,20 @@ __device__ void mma_thread(const Params &p, Shared &sh, unsigned char *sm, int r
     const auto full = [&](int stage) {
         const uint32_t phase = full_phase >> stage & 1;
         full_phase ^= 1u << stage;
-        return wait(sh, B_KVFULL + stage, phase, p);
+        return wait_one(sh, B_KVFULL + stage, phase, p);
     };
     uint32_t turns = 0;
-    const auto turn = [&] { return wait(sh, B_TURN + r, (turns++ + 1 + r) & 1, p); };  // row tile 0 begins
+    const auto turn = [&] { return wait_one(sh, B_TURN + r, (turns++ + 1 + r) & 1, p); };  // row tile 0 begins
     Items queue;
     while (ok) {
-        const Item *at = queue.next(sh, p);
+        const Item *at = queue.next<true>(sh, p);
         if (at == nullptr) break;
         const Item it = *at;
         queue.done(sh);
         const int32_t n = it.n;
         const bool two = it.two(p), mine = r == 0 || two;
         if (n == 0) continue;
-        if (!(ok = wait(sh, B_QFULL, items & 1, p) && full(ring.stage))) break;
+        if (!(ok = wait_one(sh, B_QFULL, items & 1, p) && full(ring.stage))) break;
         ++items;
         fence_after_sync();
         if (mine) {
@@ -421,7 +430,7 @@ __device__ void mma_thread(const Params &p, Shared &sh, unsigned char *sm, int r
             const int k = ring.stage;
             const bool more = i + 1 < n;
             if (it.masked(it.key(i), p)) {
-                ok = wait(sh, B_CLEAN + v, clean_phase >> v & 1, p);
+                ok = wait_one(sh, B_CLEAN + v, clean_phase >> v & 1, p);
                 clean_phase ^= 1u << v;
             } else {
                 ok = full(v);
@@ -429,10 +438,10 @@ __device__ void mma_thread(const Params &p, Shared &sh, unsigned char *sm, int r
             if (!ok || (more && !(ok = full(k)))) break;
             if (mine) {
                 if (two && !(ok = turn())) break;
-                if (!(ok = wait(sh, B_P + 2 * r, p_phase, p))) break;
+                if (!(ok = wait_one(sh, B_P + 2 * r, p_phase, p))) break;
                 fence_after_sync();
                 mma_values(tmem, v_desc + v * kTileStep, r, 0, i == 0);
-                if (!(ok = wait(sh, B_P + 2 * r + 1, p_phase, p))) break;
+                if (!(ok = wait_one(sh, B_P + 2 * r + 1, p_phase, p))) break;
                 p_phase ^= 1;
                 fence_after_sync();
                 mma_values(tmem, v_desc + v * kTileStep, r, 1, false);
@@ -454,7 +463,7 @@ __device__ void mma_thread(const Params &p, Shared &sh, unsigned char *sm, int r
     }
     if (!ok) {  // gave up: the MMAs in flight finish before TMEM is freed
         mma_commit(sh.bar + B_DRAIN + r);
-        mbar_wait_bounded(sh.bar + B_DRAIN + r, 0, kWaitNs);
+        mbar_wait_bounded(sh.bar + B_DRAIN + r, 0, kAttnWaitNs);
     }
 }
 

@@ -69,6 +69,7 @@ EXPORTED = (
     "kda_check_prefill_inputs",
     "kda_get_device_status",
     "kda_debug_inject_handoff_timeout",
+    "kda_debug_inject_attention_timeout",
 )
 
 # Capacity of the fixed scratch array behind kda_layer_core_noalloc (include/kda.h).
@@ -169,6 +170,8 @@ def _load() -> ctypes.CDLL:
     lib.kda_get_device_status.restype = ctypes.c_int
     lib.kda_debug_inject_handoff_timeout.argtypes = []
     lib.kda_debug_inject_handoff_timeout.restype = ctypes.c_int
+    lib.kda_debug_inject_attention_timeout.argtypes = []
+    lib.kda_debug_inject_attention_timeout.restype = ctypes.c_int
     return lib
 
 

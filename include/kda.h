@@ -804,6 +804,18 @@ kda_status kda_get_device_status(void *stream, uint32_t *detail);
  */
 kda_status kda_debug_inject_handoff_timeout(void);
 
+/*
+ * kda_debug_inject_attention_timeout - the same for kda_window_attention: a
+ * library built with KDA_DEBUG arms the process's NEXT call of it.  In a bf16
+ * launch (scale > 0) the warps that fetch queries, keys and values fetch nothing,
+ * so that no copy or product is in flight, and every wait gives up after 1 ms:
+ * the launch leaves without writing o, and kda_get_device_status reports
+ * KDA_ERR_DEVICE_TIMEOUT (detail: 97 from the kernel for short steps, 64 and
+ * above from the other).  The fp32 kernel has no such waits and runs as usual.
+ * The normal library arms nothing and returns KDA_ERR_UNSUPPORTED.
+ */
+kda_status kda_debug_inject_attention_timeout(void);
+
 #ifdef __cplusplus
 }
 #endif

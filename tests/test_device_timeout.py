@@ -78,3 +78,45 @@ def test_debug_library_reports_a_wait_that_runs_out(kda):
                                       f(inp.beta), inp.cu_seqlens.cpu().numpy())
     assert_close(to64(o), ref_o, TOL_BF16, "o after the timed-out launch")
     assert_close(to64(Sf), ref_S, TOL_BF16, "S_final after the timed-out launch")
+
+
+def test_normal_library_refuses_the_attention_injection(kda):
+    assert kda.library().kda_debug_inject_attention_timeout() == UNSUPPORTED
+
+
+# (tokens of each request, tokens before them, window, details): one token a row and a few (the kernel for short
+# steps, a row over one CTA and over several), a prefill, and a short step behind a long row (CTAs that share an item)
+ATTENTION = [([1], [100], 60, [97]), ([2, 1], [3000, 500], 2 ** 31 - 1, [97]), ([300, 20], [50, 0], 50, range(64, 128)),
+             ([40], [3000], 2 ** 31 - 1, range(64, 128))]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,old,window,details", ATTENTION)
+def test_debug_library_reports_attention_waits_that_run_out(kda, new, old, window, details):
+    """The load warps fetch nothing, so every other warp's wait runs out: the launch leaves with the status, o as it
+    was, and the next call is right."""
+    from gated_delta_rule_kda_gb300 import build
+    from tests._cache import build_cache, cu_of, queries
+    c = build_cache([a + b for a, b in zip(new, old)], 32, 2, torch.bfloat16, seed=59)
+    q, cu = queries(sum(new), 8, torch.bfloat16, 59), cu_of(new)
+    want = kda.kda_window_attention(q, c["pool"], c["table"], c["slot"], cu, c["kv_len"], window, 4, max_tokens=max(new))
+    assert kda.kda_get_device_status()[0] == 0
+    lib = ctypes.CDLL(build.build(debug=True))
+    lib.kda_window_attention.argtypes = kda.library().kda_window_attention.argtypes
+    lib.kda_get_device_status.argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_uint32)]
+    lib.kda_debug_inject_attention_timeout.argtypes = []
+    stream, detail = torch.cuda.current_stream().cuda_stream, ctypes.c_uint32(0)
+    o = torch.full_like(q, -7.0)
+
+    def attend():
+        R, M = c["table"].shape
+        P, _, Hkv, page, _ = c["pool"].shape
+        assert lib.kda_window_attention(0, len(new), sum(new), max(new), 8, Hkv, P, page, R, M, window, 4, q.data_ptr(),
+                                        c["pool"].data_ptr(), c["table"].data_ptr(), c["slot"].data_ptr(), cu.data_ptr(),
+                                        c["kv_len"].data_ptr(), 128 ** -0.5, o.data_ptr(), stream) == 0
+        return lib.kda_get_device_status(stream, ctypes.byref(detail))
+
+    assert lib.kda_debug_inject_attention_timeout() == 0
+    assert attend() == TIMEOUT and detail.value in details
+    assert bool((o == -7.0).all())
+    assert attend() == 0 and torch.equal(o, want)
