@@ -100,7 +100,6 @@ __device__ void produce(const Params &p, Shared &sh, unsigned char *sm, const At
     const WindowAttentionArgs &a = p.a;
     const int32_t page_shift = p.page_shift, p0 = req.len - req.n, last = req.len - 1;
     int32_t i = from;
-    bool ok = true;
     for (; i < to; ++i) {
         const int32_t n = i - from, s = n % kStages, j0 = keys.tile(i) * kTile;
         const bool edge = some_hidden(a, j0, kTile, p0, last);
@@ -112,7 +111,7 @@ __device__ void produce(const Params &p, Shared &sh, unsigned char *sm, const At
         if (mine && (!edge || (j <= last && (p0 - j - 16 < a.window - 1 || j < a.sinks))))
             id = attn_page(a.cache, req.row, last, j >> page_shift);
         const uint32_t exist = __ballot_sync(0xffffffffu, id >= 0);
-        if (n >= kStages && !(ok = wait(sh, &sh.empty[s], (n / kStages - 1) & 1, p, 96))) break;
+        if (n >= kStages && !wait(sh, &sh.empty[s], (n / kStages - 1) & 1, p, 96)) break;
         if (lane == 0) {
             // a bit for 16 keys
             const uint32_t bits = shift == 4   ? exist
@@ -128,7 +127,8 @@ __device__ void produce(const Params &p, Shared &sh, unsigned char *sm, const At
             tma_load_box(smem_u32(sm + s * kStageBytes + (lane << (shift + 9))), edge ? &p.tm_edge : &p.tm_kv, y, &sh.full[s]);
         }
     }
-    if (!ok && lane == 0)  // gave up: the copies in flight still land before the CTA leaves
+    // Whichever warp gives up, the copies in flight land before the CTA leaves.
+    if (lane == 0)
         for (int32_t k = max(from, i - kStages); k < i; ++k)
             mbar_wait_bounded(&sh.full[(k - from) % kStages], ((k - from) / kStages) & 1, kAttnWaitNs);
 }

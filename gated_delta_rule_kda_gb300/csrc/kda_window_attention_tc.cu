@@ -235,8 +235,8 @@ __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
     Ring ring;
     uint32_t loads = 0, items = 0, tiles = 0, uses[2] = {0, 0};  // bit s: parity of the uses of KVFULL, RAW + s
     bool ok = true;
-    uint32_t asked = 0;  // requests for more work
-    bool asking = false;
+    uint32_t asked = 0;  // requests for more work that were answered
+    bool asking = false;  // one is under way
     // The grid has a CTA an item: those that have not started are taken over, one at a time.
     const auto ask = [&] {
         if (kSplit) return;
@@ -332,6 +332,7 @@ __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
         if (asking) {
             if (!(ok = wait(sh, B_NEXT, asked & 1, p))) break;
             ++asked;
+            asking = false;
             more = taken_work(&sh.next, w);
             __syncwarp();
         } else {
@@ -345,9 +346,10 @@ __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
             }
         }
     }
-    if (!ok && lane == 0) {  // gave up: the copies in flight still land before the CTA leaves
+    // Whichever warp gives up, the copies in flight land before the CTA leaves (they have, if none did).
+    if (lane == 0) {
         if (items > 0) mbar_wait_bounded(sh.bar + B_QFULL, (items - 1) & 1, kAttnWaitNs);
-        mbar_wait_bounded(sh.bar + B_NEXT, asked & 1, kAttnWaitNs);
+        if (asking) mbar_wait_bounded(sh.bar + B_NEXT, asked & 1, kAttnWaitNs);
         for (int s = 0; s < kStages; ++s) {
             mbar_wait_bounded(sh.bar + B_KVFULL + s, ~(uses[0] >> s) & 1, kAttnWaitNs);
             mbar_wait_bounded(sh.bar + B_RAW + s, ~(uses[1] >> s) & 1, kAttnWaitNs);
@@ -461,10 +463,9 @@ __device__ void mma_thread(const Params &p, Shared &sh, unsigned char *sm, int r
             }
         }
     }
-    if (!ok) {  // gave up: the MMAs in flight finish before TMEM is freed
-        mma_commit(sh.bar + B_DRAIN + r);
-        mbar_wait_bounded(sh.bar + B_DRAIN + r, 0, kAttnWaitNs);
-    }
+    // Whichever warp gives up, the MMAs in flight finish before TMEM is freed.
+    mma_commit(sh.bar + B_DRAIN + r);
+    mbar_wait_bounded(sh.bar + B_DRAIN + r, 0, kAttnWaitNs);
 }
 
 // ---------------------------------------------------------------------------

@@ -10,6 +10,7 @@ copy or tensor-core product in flight.  Nothing faults, traps or hangs: the test
 reported status, then that the next prefill through the same library is correct.
 """
 import ctypes
+import time
 
 import numpy as np
 import pytest
@@ -95,6 +96,17 @@ ATTENTION = [([1], [100], 60, [97]), ([2, 1], [3000, 500], 2 ** 31 - 1, [97]), (
 def test_debug_library_reports_attention_waits_that_run_out(kda, new, old, window, details):
     """The load warps fetch nothing, so every other warp's wait runs out: the launch leaves with the status, o as it
     was, and the next call is right."""
+    _attention_gives_up(kda, new, old, window, details)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,old,window,details", ATTENTION)
+def test_attention_that_gives_up_waits_only_for_what_is_in_flight(kda, new, old, window, details):
+    """With every wait limited to 1 ms the launch is over in far less than the 2 s of one unlimited wait."""
+    assert _attention_gives_up(kda, new, old, window, details) < 0.5
+
+
+def _attention_gives_up(kda, new, old, window, details):
     from gated_delta_rule_kda_gb300 import build
     from tests._cache import build_cache, cu_of, queries
     c = build_cache([a + b for a, b in zip(new, old)], 32, 2, torch.bfloat16, seed=59)
@@ -117,6 +129,9 @@ def test_debug_library_reports_attention_waits_that_run_out(kda, new, old, windo
         return lib.kda_get_device_status(stream, ctypes.byref(detail))
 
     assert lib.kda_debug_inject_attention_timeout() == 0
+    t0 = time.perf_counter()
     assert attend() == TIMEOUT and detail.value in details
+    taken = time.perf_counter() - t0
     assert bool((o == -7.0).all())
     assert attend() == 0 and torch.equal(o, want)
+    return taken
