@@ -19,7 +19,8 @@ PAGE, WINDOW, SINKS = 16, 64, 4
 def run(prompt: int = 150, steps: int = 24, kda_heads: int = 4, q_heads: int = 8, kv_heads: int = 2,
         seed: int = 0, device: str = "cuda"):
     """Outputs of the attention layer and of the KDA layer, [branches, steps, heads, 128] each, the
-    prompt's attention output, and how many pages are live at the end."""
+    prompt's attention output, how many pages are live at the end, and the last token's attention
+    output once more, from the cache as it was brought together."""
     total, branches, rows = prompt + steps, 2, 4
     i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=device)
 
@@ -41,11 +42,11 @@ def run(prompt: int = 150, steps: int = 24, kda_heads: int = 4, q_heads: int = 8
     kv_len = torch.zeros(rows, dtype=torch.int32, device=device)
 
     def attend(t0, n, slots, pos):
-        """The attention layer over tokens [t0, t0 + n), the same for each request in `slots`."""
+        """The attention layer over tokens [t0, t0 + n), the same for each request in `slots`: its output and queries."""
         idx = torch.arange(t0, t0 + n, device=device).repeat(len(slots))
         cu, slot = i32([n * i for i in range(len(slots) + 1)]), i32(slots)
         qn = kda.kda_qk_norm_rope_append(q[idx], k[idx], v[idx], rope, pos, pool[0], table, slot, cu, kv_len, wq, wk)
-        return kda.kda_window_attention(qn, pool[0], table, slot, cu, kv_len, WINDOW, SINKS, max_tokens=n)
+        return kda.kda_window_attention(qn, pool[0], table, slot, cu, kv_len, WINDOW, SINKS, max_tokens=n), qn
 
     # prefill into row 2, whose pages are scattered over the pool
     row, child = 2, 0
@@ -53,7 +54,7 @@ def run(prompt: int = 150, steps: int = 24, kda_heads: int = 4, q_heads: int = 8
     table[row, :used] = torch.randperm(pages, generator=torch.Generator().manual_seed(seed))[:used].to(device, torch.int32)
     kv_len[row] = prompt
     table[row, -(-prompt // PAGE):] = -1  # pages come with the tokens
-    prompt_out = attend(0, prompt, [row], torch.arange(prompt, dtype=torch.int32, device=device))
+    prompt_out, _ = attend(0, prompt, [row], torch.arange(prompt, dtype=torch.int32, device=device))
     cu = i32([0, prompt])
     part = lambda t: t[:prompt].contiguous()
     _, S = kda.kda_layer_core_fused(part(lin.qp), part(lin.kp), part(lin.vp), lin.conv_w, part(lin.z), lin.A, lin.b,
@@ -75,7 +76,7 @@ def run(prompt: int = 150, steps: int = 24, kda_heads: int = 4, q_heads: int = 8
             free = sorted(set(range(pages)) - set(table.flatten().tolist()))[:branches]
             table[slots, t // PAGE] = i32(free)
         kv_len[slots] = t + 1
-        o = attend(t, 1, slots, i32([t] * branches))
+        o, qn = attend(t, 1, slots, i32([t] * branches))
         att.append(o)
         pick = lambda x: x[t:t + 1].expand(branches, *x.shape[1:]).contiguous()
         lin_out.append(kda.kda_decode_layer(pick(lin.qp), pick(lin.kp), pick(lin.vp), lin.conv_w, pick(lin.z), lin.A,
@@ -85,8 +86,7 @@ def run(prompt: int = 150, steps: int = 24, kda_heads: int = 4, q_heads: int = 8
 
     kda.kda_pages_release(table, kv_len, i32([child]), PAGE)
     _, live = kda.kda_pages_compact(pool, table)
-    again = kda.kda_window_attention(torch.zeros_like(q[:1].contiguous()), pool[0], table, i32([row]), i32([0, 1]),
-                                     kv_len, WINDOW, SINKS, max_tokens=1)
+    again = kda.kda_window_attention(qn[:1], pool[0], table, i32([row]), i32([0, 1]), kv_len, WINDOW, SINKS, max_tokens=1)
     status, detail = kda.kda_get_device_status()
     if status != 0:
         raise RuntimeError(f"device status {status} (detail {detail})")

@@ -38,3 +38,34 @@ def test_hybrid_example_against_64_bits():
     # k and q may round to the neighbouring bf16 where fp32 and 64 bits fall either side of a tie: one
     # ulp (2^-8) of one of 128 products, some 2^-8 |q_i k_i| scale < 2^-9 of a score unit
     assert (np.abs(got - ref) <= 2.0 ** -8 * (a + np.abs(ref)) + 2.0 ** -8 * a).all()
+
+
+def test_hybrid_example_answers_alike_after_release_and_compaction():
+    """The last token asked once more, of the row that is left in the compacted cache: the same keys and values in other
+    pages.  Window and sinks are two key tiles, which one CTA takes whatever the batch, so the bits are the same."""
+    from gated_delta_rule_kda_gb300 import build
+    build.build()
+    from gated_delta_rule_kda_gb300 import hybrid_example as ex
+    att, _, _, _, again = ex.run(150, 24)
+    assert att.float().abs().max() > 0.1
+    assert torch.equal(again[0], att[0, -1])
+
+
+@pytest.mark.parametrize("prompt", [150, 64])
+def test_hybrid_example_recurrent_layer_against_the_oracle(prompt):
+    """The KDA layer's prefill, its states handed to the pools and to the branch, and the decode of both branches: one
+    run of the oracle over prompt and steps, at the layer's tolerance."""
+    import oracle
+    from gated_delta_rule_kda_gb300 import build, synthetic
+    from tests._parity import assert_gated_close
+    build.build()
+    from gated_delta_rule_kda_gb300 import hybrid_example as ex
+    steps, heads = 24, 4
+    _, lin, _, _, _ = ex.run(prompt, steps)
+    inp = synthetic.layer_inputs([prompt + steps], heads, seed=0, s0_std=0.1, device="cuda")
+    conv_w = to64(inp.conv_w).reshape(3, heads * 128, 4)
+    f = to64
+    o, _ = oracle.kda_layer_core(f(inp.qp), f(inp.kp), f(inp.vp), conv_w, f(inp.z), f(inp.A), f(inp.b),
+                                 f(inp.beta_logit), f(inp.g), inp.cu_seqlens.cpu().numpy(), f(inp.S0))
+    for branch in range(2):
+        assert_gated_close(to64(lin[branch]), o[prompt:], False, f"branch {branch}")
