@@ -61,7 +61,7 @@ def run(prompt: int = 150, steps: int = 24, kda_heads: int = 4, q_heads: int = 8
                                     part(lin.beta_logit), part(lin.g), cu, lin.S0)
     S_pool[row] = S[0]
     for s, x in enumerate((lin.qp, lin.kp, lin.vp)):
-        for tap in range(3):
+        for tap in range(min(3, prompt)):  # (zeros before the first token)
             conv_pool[row, s, tap] = x[prompt - 1 - tap]
 
     # the branch: shared whole pages, a page of its own for the part-filled one, its own state rows

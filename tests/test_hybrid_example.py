@@ -69,3 +69,9 @@ def test_hybrid_example_recurrent_layer_against_the_oracle(prompt):
                                  f(inp.beta_logit), f(inp.g), inp.cu_seqlens.cpu().numpy(), f(inp.S0))
     for branch in range(2):
         assert_gated_close(to64(lin[branch]), o[prompt:], False, f"branch {branch}")
+
+
+@pytest.mark.parametrize("prompt", [1, 2])
+def test_hybrid_example_with_a_prompt_shorter_than_the_convolution(prompt):
+    """The convolution state of a prompt of fewer than three tokens has zeros for those before its first."""
+    test_hybrid_example_recurrent_layer_against_the_oracle(prompt)
