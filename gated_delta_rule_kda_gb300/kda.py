@@ -583,45 +583,60 @@ _F32, _I32 = torch.float32, torch.int32
 _ELEM = {torch.bfloat16: KDA_BF16, torch.float32: KDA_FP32}
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    if t is None:
-        return None
-    if not t.is_contiguous():
-        raise ValueError("tensors must be contiguous")
+def _refuse(t: torch.Tensor, dtype, dev: int):
+    """Says why a tensor cannot be handed to a call on GPU dev."""
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"expected {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError("tensors must be on one GPU")
+    raise ValueError("tensors must be contiguous")
+
+
+def _ptr(t: torch.Tensor, dev: int):
+    if not t.is_contiguous() or t.get_device() != dev:
+        _refuse(t, None, dev)
     return t.data_ptr()
 
 
-def _ptrs(dtype: torch.dtype, *tensors):
-    """Pointers of dense tensors of one type (None for None)."""
+def _ptrs(dev: int, dtype: torch.dtype, *tensors):
+    """Pointers of dense tensors of one type on GPU dev (None for None)."""
+    out = []
     for t in tensors:
-        if t is not None:
-            if t.dtype is not dtype:
-                raise TypeError(f"expected {dtype}, got {t.dtype}")
-            if not t.is_contiguous():
-                raise ValueError("tensors must be contiguous")
-    return [None if t is None else t.data_ptr() for t in tensors]
+        if t is None:
+            out.append(None)
+            continue
+        if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
+            _refuse(t, dtype, dev)
+        out.append(t.data_ptr())
+    return out
 
 
-def _raw_stream(stream, t: torch.Tensor):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else None
+def _launch(stream, dev: int):
+    """The raw stream of a call on tensors of GPU dev.  It must be the current one: the library launches
+    there, and its kernels would take a host or another GPU's address for one of that GPU's."""
+    if dev < 0:
+        raise ValueError("tensors must be on a GPU")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError("tensors must be on the current GPU")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _elem(t: torch.Tensor) -> int:
-    code = _ELEM.get(t.dtype)
+def _elem(dtype: torch.dtype) -> int:
+    code = _ELEM.get(dtype)
     if code is None:
-        raise TypeError(f"unsupported dtype {t.dtype}")
+        raise TypeError(f"unsupported dtype {dtype}")
     return code
 
 
-def _heads(t: torch.Tensor):
-    """(heads, elements from token to token) of [T, heads, 128] whose heads lie side by side."""
+def _heads(t: torch.Tensor, dev: int):
+    """(tokens, heads, elements from token to token) of [T, heads, 128] whose heads lie side by side."""
     T, H, d = t.shape
     s0, s1, s2 = t.stride()
     if d != HEAD_DIM or s2 != 1 or (s1 != HEAD_DIM and H > 1):
         raise ValueError("the heads of a token must lie side by side, 128 channels each")
-    return H, s0 if T > 1 else H * HEAD_DIM
+    if t.get_device() != dev:
+        _refuse(t, None, dev)
+    return T, H, s0 if T > 1 else H * HEAD_DIM
 
 
 def _pool_shape(kv_pool):
@@ -632,7 +647,7 @@ def _pool_shape(kv_pool):
     return shape[0], shape[2], shape[3]
 
 
-def _rope_args(rope, positions, T):
+def _rope_args(rope, positions, T, dev):
     if rope is None:
         return None, 0, 0, None
     if positions.numel() != T:
@@ -640,16 +655,16 @@ def _rope_args(rope, positions, T):
     P, half, _ = rope.shape
     if rope.dtype is not _F32 or positions.dtype is not _I32:
         raise TypeError("the rotation table must be float32, positions int32")
-    return _ptr(rope), P, 2 * half, _ptr(positions)
+    return _ptr(rope, dev), P, 2 * half, _ptr(positions, dev)
 
 
-def _cache_args(page_table, slot, cu_tokens, kv_len):
+def _cache_args(dev, page_table, slot, cu_tokens, kv_len):
     """(requests, rows, width, pointers of the table, slots, offsets and lengths)."""
     R, M = page_table.shape
     B = slot.numel()
     if cu_tokens.numel() != B + 1 or kv_len.numel() != R:
         raise ValueError("cu_tokens must have one entry more than slot, kv_len one per table row")
-    return B, R, M, _ptrs(_I32, page_table, slot, cu_tokens, kv_len)
+    return B, R, M, _ptrs(dev, _I32, page_table, slot, cu_tokens, kv_len)
 
 
 def kda_qk_norm_rope(q, k, rope, positions, q_weight=None, k_weight=None, eps=1e-6, *, norm=True,
@@ -657,21 +672,21 @@ def kda_qk_norm_rope(q, k, rope, positions, q_weight=None, k_weight=None, eps=1e
     """q [T, Hq, 128] and k [T, Hkv, 128] (heads dense, any token stride) normed per head and
     rotated by rope_table(...) at positions [T] int32 (rope None: no rotation).
     Returns (q_out, k_out)."""
-    out_dtype = q_out.dtype if q_out is not None else out_dtype or q.dtype
+    dtype, dev = q.dtype, q.get_device()
+    out_dtype = q_out.dtype if q_out is not None else out_dtype or dtype
     if q_out is None:
         q_out = _empty(q.shape, out_dtype, q.device, stream)
     if k_out is None:
         k_out = _empty(k.shape, out_dtype, k.device, stream)
-    T = q.shape[0]
-    if k.shape[0] != T or q_out.shape != q.shape or k_out.shape != k.shape or k_out.dtype != out_dtype \
-            or k.dtype != q.dtype:
+    if k.shape[0] != q.shape[0] or q_out.shape != q.shape or k_out.shape != k.shape or k_out.dtype is not out_dtype \
+            or k.dtype is not dtype:
         raise ValueError("q, k and their outputs must agree in tokens, heads and type")
-    (Hq, qs), (Hkv, ks) = _heads(q), _heads(k)
-    table, P, R, pos = _rope_args(rope, positions, T)
-    wq, wk = _ptrs(_F32, q_weight, k_weight)
-    rc = _lib.kda_qk_norm_rope(_elem(q), _elem(q_out), T, Hq, Hkv, q.data_ptr(), qs, k.data_ptr(), ks,
-                               wq, wk, eps, norm, table, P, R, interleaved, pos, _ptr(q_out),
-                               _ptr(k_out), _raw_stream(stream, q))
+    (T, Hq, qs), (_, Hkv, ks) = _heads(q, dev), _heads(k, dev)
+    table, P, R, pos = _rope_args(rope, positions, T, dev)
+    wq, wk = _ptrs(dev, _F32, q_weight, k_weight)
+    rc = _lib.kda_qk_norm_rope(_elem(dtype), _elem(out_dtype), T, Hq, Hkv, q.data_ptr(), qs, k.data_ptr(), ks,
+                               wq, wk, eps, norm, table, P, R, interleaved, pos, _ptr(q_out, dev),
+                               _ptr(k_out, dev), _launch(stream, dev))
     _check("kda_qk_norm_rope", rc)
     return q_out, k_out
 
@@ -682,21 +697,21 @@ def kda_qk_norm_rope_append(q, k, v, rope, positions, kv_pool, page_table, slot,
     """kda_qk_norm_rope with k (normed and rotated) and v written to the cache pages of the tokens:
     kv_pool [P, 2, Hkv, page_size, 128], page_table [R, M], kv_len [R] (these tokens counted),
     slot [B], cu_tokens [B+1].  Outputs have the pool's type.  Returns q_out."""
+    dtype, out_dtype, dev = q.dtype, kv_pool.dtype, q.get_device()
     P, pool_heads, page = _pool_shape(kv_pool)
     if q_out is None:
-        q_out = _empty(q.shape, kv_pool.dtype, q.device, stream)
-    T, k_shape, dtype = q.shape[0], k.shape, q.dtype
-    if k_shape[0] != T or v.shape != k_shape or k_shape[1] != pool_heads or q_out.shape != q.shape \
-            or q_out.dtype is not kv_pool.dtype or k.dtype is not dtype or v.dtype is not dtype:
+        q_out = _empty(q.shape, out_dtype, q.device, stream)
+    (T, Hq, qs), (Tk, Hkv, ks), (Tv, Hv, vs) = _heads(q, dev), _heads(k, dev), _heads(v, dev)
+    if Tk != T or Tv != T or Hkv != pool_heads or Hv != Hkv or q_out.shape != q.shape \
+            or q_out.dtype is not out_dtype or k.dtype is not dtype or v.dtype is not dtype:
         raise ValueError("q, k, v, q_out and kv_pool must agree in tokens, heads and type")
-    (Hq, qs), (Hkv, ks), (_, vs) = _heads(q), _heads(k), _heads(v)
-    table, npos, R, pos = _rope_args(rope, positions, T)
-    B, rows, width, (pt, sl, cu, kl) = _cache_args(page_table, slot, cu_tokens, kv_len)
-    wq, wk = _ptrs(_F32, q_weight, k_weight)
+    table, npos, R, pos = _rope_args(rope, positions, T, dev)
+    B, rows, width, (pt, sl, cu, kl) = _cache_args(dev, page_table, slot, cu_tokens, kv_len)
+    wq, wk = _ptrs(dev, _F32, q_weight, k_weight)
     rc = _lib.kda_qk_norm_rope_append(
-        _elem(q), _elem(q_out), B, T, Hq, Hkv, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+        _elem(dtype), _elem(out_dtype), B, T, Hq, Hkv, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
         wq, wk, eps, norm, table, npos, R, interleaved, pos, P, page, rows, width, pt, sl, cu, kl,
-        _ptr(kv_pool), _ptr(q_out), _raw_stream(stream, q))
+        _ptr(kv_pool, dev), _ptr(q_out, dev), _launch(stream, dev))
     _check("kda_qk_norm_rope_append", rc)
     return q_out
 
@@ -706,21 +721,22 @@ def kda_window_attention(q, kv_pool, page_table, slot, cu_tokens, kv_len, window
     """Attention of q [T, Hq, 128] over the requests' rows of the cache, with a sliding window and
     the first `sinks` tokens always visible (window None: plain causal).  max_tokens: no request
     brings more (default: T); small values let the call split long rows.  Returns o."""
-    T, Hq, d = q.shape
+    shape, dtype, dev = q.shape, q.dtype, q.get_device()
+    T, Hq, d = shape
     P, Hkv, page = _pool_shape(kv_pool)
-    if kv_pool.dtype is not q.dtype:
+    if kv_pool.dtype is not dtype:
         raise TypeError("q and kv_pool must have one type")
     if o is None:
-        o = _empty(q.shape, q.dtype, q.device, stream)
-    elif o.shape != q.shape or o.dtype is not q.dtype:
+        o = _empty(shape, dtype, q.device, stream)
+    elif o.shape != shape or o.dtype is not dtype:
         raise ValueError("o must have q's shape and type")
     if d != HEAD_DIM:
         raise ValueError("q must be [tokens, heads, 128]")
-    B, rows, width, (pt, sl, cu, kl) = _cache_args(page_table, slot, cu_tokens, kv_len)
+    B, rows, width, (pt, sl, cu, kl) = _cache_args(dev, page_table, slot, cu_tokens, kv_len)
     rc = _lib.kda_window_attention(
-        _elem(q), B, T, max(T, 1) if max_tokens is None else max_tokens, Hq, Hkv, P, page, rows, width,
-        0x7fffffff if window is None else window, sinks, _ptr(q), _ptr(kv_pool), pt, sl, cu, kl, scale,
-        _ptr(o), _raw_stream(stream, q))
+        _elem(dtype), B, T, max(T, 1) if max_tokens is None else max_tokens, Hq, Hkv, P, page, rows, width,
+        0x7fffffff if window is None else window, sinks, _ptr(q, dev), _ptr(kv_pool, dev), pt, sl, cu, kl, scale,
+        _ptr(o, dev), _launch(stream, dev))
     _check("kda_window_attention", rc)
     return o
 
@@ -741,8 +757,9 @@ def kda_pages_copy(pool, src, dst, *, stream=None):
     if dst.numel() != n:
         raise ValueError("src and dst must have one length")
     L, P, nbytes = _layers(pool)
-    s, d = _ptrs(_I32, src, dst)
-    _check("kda_pages_copy", _lib.kda_pages_copy(L, P, nbytes, n, s, d, _ptr(pool), _raw_stream(stream, pool)))
+    dev = pool.get_device()
+    s, d = _ptrs(dev, _I32, src, dst)
+    _check("kda_pages_copy", _lib.kda_pages_copy(L, P, nbytes, n, s, d, _ptr(pool, dev), _launch(stream, dev)))
 
 
 def kda_pages_workspace_size(num_pages: int, table_rows: int) -> int:
@@ -767,9 +784,10 @@ def kda_pages_fork(pool, page_table, kv_len, parent, child, page_size, *, worksp
         raise ValueError("parent and child must have one length, kv_len one entry per table row")
     L, P, nbytes = _layers(pool)
     workspace, wbytes = _pages_workspace(workspace, P, R, pool.device, stream)
-    pa, ch, pt, kl = _ptrs(_I32, parent, child, page_table, kv_len)
-    _check("kda_pages_fork", _lib.kda_pages_fork(L, P, nbytes, page_size, R, M, F, pa, ch, pt, kl, _ptr(pool),
-                                                 _ptr(workspace), wbytes, _raw_stream(stream, pool)))
+    dev = pool.get_device()
+    pa, ch, pt, kl = _ptrs(dev, _I32, parent, child, page_table, kv_len)
+    _check("kda_pages_fork", _lib.kda_pages_fork(L, P, nbytes, page_size, R, M, F, pa, ch, pt, kl, _ptr(pool, dev),
+                                                 _ptr(workspace, dev), wbytes, _launch(stream, dev)))
 
 
 def kda_pages_release(page_table, kv_len, rows, page_size, window=0, sinks=0, *, stream=None):
@@ -778,9 +796,10 @@ def kda_pages_release(page_table, kv_len, rows, page_size, window=0, sinks=0, *,
     R, M = page_table.shape
     if kv_len.numel() != R:
         raise ValueError("kv_len must have one entry per table row")
-    r, pt, kl = _ptrs(_I32, rows, page_table, kv_len)
+    dev = page_table.get_device()
+    r, pt, kl = _ptrs(dev, _I32, rows, page_table, kv_len)
     _check("kda_pages_release", _lib.kda_pages_release(R, M, page_size, rows.numel(), r, window, sinks, pt, kl,
-                                                       _raw_stream(stream, page_table)))
+                                                       _launch(stream, dev)))
 
 
 def kda_pages_compact(pool, page_table, *, table_out=None, num_live=None, workspace=None, stream=None):
@@ -795,9 +814,10 @@ def kda_pages_compact(pool, page_table, *, table_out=None, num_live=None, worksp
     if num_live is None:
         num_live = _empty(1, _I32, pool.device, stream)
     workspace, wbytes = _pages_workspace(workspace, P, R, pool.device, stream)
-    tin, tout, live = _ptrs(_I32, page_table, table_out, num_live)
-    _check("kda_pages_compact", _lib.kda_pages_compact(L, P, nbytes, R, M, tin, tout, live, _ptr(pool),
-                                                       _ptr(workspace), wbytes, _raw_stream(stream, pool)))
+    dev = pool.get_device()
+    tin, tout, live = _ptrs(dev, _I32, page_table, table_out, num_live)
+    _check("kda_pages_compact", _lib.kda_pages_compact(L, P, nbytes, R, M, tin, tout, live, _ptr(pool, dev),
+                                                       _ptr(workspace, dev), wbytes, _launch(stream, dev)))
     return table_out, num_live
 
 

@@ -169,3 +169,62 @@ def test_binding_refuses_what_it_cannot_marshal(kda):
         kda.kda_pages_copy(torch.zeros((1, 4, 8)), i32(2), i32(3))
     with pytest.raises(ValueError):
         kda.kda_pages_copy(torch.zeros((4, 8)), i32(2), i32(2))
+
+
+def _binding_arguments():
+    """Arguments that every paged-cache call of the binding takes, on the CPU."""
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    return dict(q=torch.zeros((2, 4, 128)), k=torch.zeros((2, 2, 128)), v=torch.zeros((2, 2, 128)),
+                rope=torch.zeros((9, 8, 2)), positions=i32(2), pool=torch.zeros((3, 2, 2, 16, 128)), table=i32(2, 3),
+                slot=i32(1), cu=i32(2), kv_len=i32(2), wq=torch.zeros(128), wk=torch.zeros(128), rows=i32(1),
+                workspace=torch.zeros(1 << 12, dtype=torch.uint8), live=i32(1), window=16, sinks=1, most=2, page=16)
+
+
+def _binding_calls(kda, a):
+    cache = (a["pool"], a["table"], a["slot"], a["cu"], a["kv_len"])
+    return {
+        "rope": lambda: kda.kda_qk_norm_rope(a["q"], a["k"], a["rope"], a["positions"], a["wq"], a["wk"]),
+        "append": lambda: kda.kda_qk_norm_rope_append(a["q"], a["k"], a["v"], a["rope"], a["positions"], *cache, a["wq"],
+                                                      a["wk"]),
+        "attention": lambda: kda.kda_window_attention(a["q"], *cache, a["window"], a["sinks"], max_tokens=a["most"]),
+        "copy": lambda: kda.kda_pages_copy(a["pool"][None], a["rows"], a["rows"]),
+        "fork": lambda: kda.kda_pages_fork(a["pool"][None], a["table"], a["kv_len"], a["rows"], a["rows"], a["page"],
+                                           workspace=a["workspace"]),
+        "release": lambda: kda.kda_pages_release(a["table"], a["kv_len"], a["rows"], a["page"], a["window"], a["sinks"]),
+        "compact": lambda: kda.kda_pages_compact(a["pool"][None], a["table"], num_live=a["live"],
+                                                 workspace=a["workspace"]),
+    }
+
+
+class _NoLaunch:
+    """In place of the library: takes down what a call would have launched."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, entry):
+        return lambda *a: self.calls.append((entry, a)) or 0
+
+
+@pytest.mark.parametrize("name", ["rope", "append", "attention", "copy", "fork", "release", "compact"])
+def test_binding_refuses_tensors_that_are_not_on_the_gpu(kda, name, monkeypatch):
+    """Host addresses never reach a kernel."""
+    lib = _NoLaunch()
+    monkeypatch.setattr(kda, "_lib", lib)
+    with pytest.raises(ValueError, match="GPU"):
+        _binding_calls(kda, _binding_arguments())[name]()
+    assert not lib.calls
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name,arg", [("rope", "rope"), ("rope", "positions"), ("rope", "wk"), ("append", "v"),
+                                      ("append", "slot"), ("append", "cu"), ("attention", "table"),
+                                      ("attention", "kv_len"), ("copy", "rows"), ("fork", "kv_len"),
+                                      ("fork", "workspace"), ("release", "rows"), ("compact", "live")])
+def test_binding_refuses_one_tensor_left_on_the_host(kda, name, arg, monkeypatch):
+    a = {x: t.cuda() if isinstance(t, torch.Tensor) and x != arg else t for x, t in _binding_arguments().items()}
+    lib = _NoLaunch()
+    monkeypatch.setattr(kda, "_lib", lib)
+    with pytest.raises(ValueError, match="GPU"):
+        _binding_calls(kda, a)[name]()
+    assert not lib.calls

@@ -90,6 +90,7 @@ def test_what_a_call_allocates_belongs_to_its_stream(kda, name, monkeypatch):
     calls = _calls(kda)  # before torch.empty is watched
     assert set(calls) == set(ALLOCATING)
     monkeypatch.setattr(kda, "_lib", Lib())
+    monkeypatch.setattr(kda, "_launch", lambda s, dev: s.cuda_stream)  # (it refuses CPU tensors)
     monkeypatch.setattr(torch.cuda, "stream", switch)
     monkeypatch.setattr(torch, "empty", record(torch.empty))
     monkeypatch.setattr(torch, "empty_like", record(torch.empty_like))
