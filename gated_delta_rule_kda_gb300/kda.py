@@ -652,10 +652,19 @@ def _rope_args(rope, positions, T, dev):
         return None, 0, 0, None
     if positions.numel() != T:
         raise ValueError("positions must have one entry per token")
-    P, half, _ = rope.shape
+    shape = rope.shape
+    if len(shape) != 3 or shape[2] != 2:
+        raise ValueError("the rotation table must be [positions, rotary_dim / 2, 2]")
     if rope.dtype is not _F32 or positions.dtype is not _I32:
         raise TypeError("the rotation table must be float32, positions int32")
-    return _ptr(rope, dev), P, 2 * half, _ptr(positions, dev)
+    return _ptr(rope, dev), shape[0], 2 * shape[1], _ptr(positions, dev)
+
+
+def _weights(dev, *weights):
+    for w in weights:
+        if w is not None and w.numel() != HEAD_DIM:
+            raise ValueError("a weight must be [128]")
+    return _ptrs(dev, _F32, *weights)
 
 
 def _cache_args(dev, page_table, slot, cu_tokens, kv_len):
@@ -683,7 +692,7 @@ def kda_qk_norm_rope(q, k, rope, positions, q_weight=None, k_weight=None, eps=1e
         raise ValueError("q, k and their outputs must agree in tokens, heads and type")
     (T, Hq, qs), (_, Hkv, ks) = _heads(q, dev), _heads(k, dev)
     table, P, R, pos = _rope_args(rope, positions, T, dev)
-    wq, wk = _ptrs(dev, _F32, q_weight, k_weight)
+    wq, wk = _weights(dev, q_weight, k_weight)
     rc = _lib.kda_qk_norm_rope(_elem(dtype), _elem(out_dtype), T, Hq, Hkv, q.data_ptr(), qs, k.data_ptr(), ks,
                                wq, wk, eps, norm, table, P, R, interleaved, pos, _ptr(q_out, dev),
                                _ptr(k_out, dev), _launch(stream, dev))
@@ -707,7 +716,7 @@ def kda_qk_norm_rope_append(q, k, v, rope, positions, kv_pool, page_table, slot,
         raise ValueError("q, k, v, q_out and kv_pool must agree in tokens, heads and type")
     table, npos, R, pos = _rope_args(rope, positions, T, dev)
     B, rows, width, (pt, sl, cu, kl) = _cache_args(dev, page_table, slot, cu_tokens, kv_len)
-    wq, wk = _ptrs(dev, _F32, q_weight, k_weight)
+    wq, wk = _weights(dev, q_weight, k_weight)
     rc = _lib.kda_qk_norm_rope_append(
         _elem(dtype), _elem(out_dtype), B, T, Hq, Hkv, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
         wq, wk, eps, norm, table, npos, R, interleaved, pos, P, page, rows, width, pt, sl, cu, kl,

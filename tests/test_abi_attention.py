@@ -228,3 +228,21 @@ def test_binding_refuses_one_tensor_left_on_the_host(kda, name, arg, monkeypatch
     with pytest.raises(ValueError, match="GPU"):
         _binding_calls(kda, a)[name]()
     assert not lib.calls
+
+
+@pytest.mark.parametrize("name,change", [
+    ("rope", dict(wq=torch.zeros(127))), ("rope", dict(wk=torch.zeros(1))), ("append", dict(wq=torch.zeros(64))),
+    ("append", dict(wk=torch.zeros(0))), ("rope", dict(rope=torch.zeros((9, 8, 1)))),
+    ("append", dict(rope=torch.zeros((9, 16, 1)))), ("rope", dict(rope=torch.zeros((9, 4, 4)))),
+    ("append", dict(rope=torch.zeros((9, 16))))])
+def test_binding_refuses_weights_and_tables_of_another_shape(kda, name, change, monkeypatch):
+    """The C call cannot see that a weight is not [128] or a table not [positions, rotary_dim / 2, 2]: the kernel would
+    read past their ends."""
+    lib = _NoLaunch()
+    monkeypatch.setattr(kda, "_lib", lib)
+    monkeypatch.setattr(kda, "_launch", lambda stream, dev: None)  # (it refuses CPU tensors)
+    with pytest.raises(ValueError):
+        _binding_calls(kda, {**_binding_arguments(), **change})[name]()
+    assert not lib.calls
+    _binding_calls(kda, _binding_arguments())[name]()
+    assert len(lib.calls) == 1
