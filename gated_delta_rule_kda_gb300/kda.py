@@ -628,6 +628,12 @@ def _elem(dtype: torch.dtype) -> int:
     return code
 
 
+def _count(n: int) -> int:
+    """n as the int32 that means the same, where more than 2^31 - 1 means no more than that and any negative
+    number is refused (ctypes would keep the low 32 bits)."""
+    return -1 if n < 0 else n if n <= 0x7fffffff else 0x7fffffff
+
+
 def _heads(t: torch.Tensor, dev: int):
     """(tokens, heads, elements from token to token) of [T, heads, 128] whose heads lie side by side."""
     T, H, d = t.shape
@@ -743,8 +749,8 @@ def kda_window_attention(q, kv_pool, page_table, slot, cu_tokens, kv_len, window
         raise ValueError("q must be [tokens, heads, 128]")
     B, rows, width, (pt, sl, cu, kl) = _cache_args(dev, page_table, slot, cu_tokens, kv_len)
     rc = _lib.kda_window_attention(
-        _elem(dtype), B, T, max(T, 1) if max_tokens is None else max_tokens, Hq, Hkv, P, page, rows, width,
-        0x7fffffff if window is None else window, sinks, _ptr(q, dev), _ptr(kv_pool, dev), pt, sl, cu, kl, scale,
+        _elem(dtype), B, T, max(T, 1) if max_tokens is None else _count(max_tokens), Hq, Hkv, P, page, rows, width,
+        0x7fffffff if window is None else _count(window), _count(sinks), _ptr(q, dev), _ptr(kv_pool, dev), pt, sl, cu, kl, scale,
         _ptr(o, dev), _launch(stream, dev))
     _check("kda_window_attention", rc)
     return o
@@ -756,6 +762,8 @@ def _layers(pool):
     if len(shape) < 3:
         raise ValueError("pool must be [layers, pages, ...]")
     L, P = shape[0], shape[1]
+    if L > 0x7fffffff or P > 0x7fffffff:
+        raise ValueError("a pool has at most 2^31 - 1 layers and pages")
     return L, P, pool.numel() // max(1, L * P) * pool.element_size()
 
 
@@ -795,7 +803,7 @@ def kda_pages_fork(pool, page_table, kv_len, parent, child, page_size, *, worksp
     workspace, wbytes = _pages_workspace(workspace, P, R, pool.device, stream)
     dev = pool.get_device()
     pa, ch, pt, kl = _ptrs(dev, _I32, parent, child, page_table, kv_len)
-    _check("kda_pages_fork", _lib.kda_pages_fork(L, P, nbytes, page_size, R, M, F, pa, ch, pt, kl, _ptr(pool, dev),
+    _check("kda_pages_fork", _lib.kda_pages_fork(L, P, nbytes, _count(page_size), R, M, F, pa, ch, pt, kl, _ptr(pool, dev),
                                                  _ptr(workspace, dev), wbytes, _launch(stream, dev)))
 
 
@@ -807,7 +815,8 @@ def kda_pages_release(page_table, kv_len, rows, page_size, window=0, sinks=0, *,
         raise ValueError("kv_len must have one entry per table row")
     dev = page_table.get_device()
     r, pt, kl = _ptrs(dev, _I32, rows, page_table, kv_len)
-    _check("kda_pages_release", _lib.kda_pages_release(R, M, page_size, rows.numel(), r, window, sinks, pt, kl,
+    _check("kda_pages_release", _lib.kda_pages_release(R, M, _count(page_size), rows.numel(), r, _count(window),
+                                                       _count(sinks), pt, kl,
                                                        _launch(stream, dev)))
 
 

@@ -246,3 +246,37 @@ def test_binding_refuses_weights_and_tables_of_another_shape(kda, name, change, 
     assert not lib.calls
     _binding_calls(kda, _binding_arguments())[name]()
     assert len(lib.calls) == 1
+
+
+@pytest.mark.parametrize("big", [2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 40])
+def test_binding_does_not_wrap_large_counts(kda, big, monkeypatch):
+    """A window, sink count or token bound past 2^31 - 1 means no more than that; a page size is refused by the call
+    itself (which sees one that no cache has)."""
+    lib = _NoLaunch()
+    monkeypatch.setattr(kda, "_lib", lib)
+    monkeypatch.setattr(kda, "_launch", lambda stream, dev: None)  # (it refuses CPU tensors)
+    most = 2 ** 31 - 1
+    calls = _binding_calls(kda, {**_binding_arguments(), "window": big, "sinks": big, "most": big, "page": big})
+    for name in ("attention", "release", "fork"):
+        calls[name]()
+    (_, attention), (_, release), (_, fork) = lib.calls
+    assert attention[3] == most and attention[10:12] == (most, most)
+    assert release[2] == most and release[5:7] == (most, most)
+    assert fork[3] == most
+    calls = _binding_calls(kda, {**_binding_arguments(), "window": -big, "sinks": -big, "most": -big})
+    for name in ("attention", "release"):
+        calls[name]()
+    (_, attention), (_, release) = lib.calls[3:]
+    assert attention[3] < 0 and attention[10] < 0 and attention[11] < 0 and release[5] < 0 and release[6] < 0
+
+
+def test_binding_refuses_more_pages_than_the_call_can_count(kda, monkeypatch):
+    """[1, 2^32 + 8, 16] bytes: the page count would wrap to 8."""
+    lib = _NoLaunch()
+    monkeypatch.setattr(kda, "_lib", lib)
+    monkeypatch.setattr(kda, "_launch", lambda stream, dev: None)
+    pool = torch.zeros(16, dtype=torch.uint8).expand(1, 2 ** 32 + 8, 16)
+    one = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="pages"):
+        kda.kda_pages_copy(pool, one, one)
+    assert not lib.calls
