@@ -11,7 +11,8 @@
 // pair are in one lane, and the channels that do not rotate fall to the lanes past rotary_dim / 8.
 // Measured (30,195 tokens, 96 + 8 + 8 heads, bf16 into the cache, 1.74 GB): 284 us, 6.12 TB/s, 0.90
 // of the measured copy bandwidth; with 256-thread blocks 321 us, four rows a group 307, the rows in
-// two batches of four 344: the loads in flight set the pace.
+// two batches of four 344: the loads in flight set the pace.  (Eight blocks an SM leave 64 registers: the
+// instantiations that append spill 36 to 56 bytes.)
 #include "kda_common.cuh"
 
 namespace kda {

@@ -223,7 +223,9 @@ __device__ __forceinline__ uint32_t low_bits(int32_t n) {
 }
 
 // One row (query q_row of [T][Hq], index pos) from its visible keys alone, fp32 throughout; a warp a
-// row, four channels a lane.  Runs only where a masked tile held a non-finite value.
+// row, four channels a lane.  Runs only where a masked tile held a non-finite value.  A key at a time, each
+// waiting for the one before: 0.6 to 0.9 us a visible key (two tokens over 131,072 keys with a NaN in one kv
+// head 114 ms, against 0.12 without), so it must stay as rare as that.
 __device__ __noinline__ inline void attn_row(const WindowAttentionArgs &a, int64_t q_row, int32_t h,
                                              int32_t table_row, int32_t pos) {
     const int lane = threadIdx.x & 31;

@@ -15,8 +15,8 @@
 // maximum moves lazily, as in the prefill kernel.  Scores, m, l and o are fp32; p is rounded to bf16
 // for its product (at most 2^-8 of each weight).
 // Measured: one token for each of 256 requests (rows of 1 to 8192, window 1024 + 4, 96 and 8 heads) 178 us,
-// 5.87 TB/s of seen keys and values (0.87 of the measured copy bandwidth); two tokens for each of 4 requests
-// over 65,536 to 131,072 (64 and 8 heads) 239 us, 6.31 TB/s; one token of one request 9.8 us.  A copy for
+// 5.9 TB/s of seen keys and values (0.87 of the measured copy bandwidth); two tokens for each of 4 requests
+// over 65,536 to 131,072 (64 and 8 heads) 237 us, 6.35 TB/s; one token of one request 9.5 us.  A copy for
 // each half of a box's channels and for k and v apart: 196 and 294 us (the producer's loop sets the pace);
 // whole pages on the edges: 184; L2 prefetches four tiles ahead: 224.
 #include "kda_window_attention.cuh"

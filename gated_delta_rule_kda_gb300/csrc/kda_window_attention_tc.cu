@@ -27,11 +27,14 @@
 //               rows are at the end computed again one by one, each from its visible keys alone.
 // TMEM: s0, s1, o0, o1 of 128 columns each.  Bound: the tensor core (two 128 x 128 x 128 products
 // a key tile and row tile, 512 cycles each at its full rate).
-// Measured: 2 x 16,384 tokens behind cached ones, window 4096 + 16, 32 query and 8 kv heads: 1.42 ms,
-// 1378 TFLOP/s (0.74 of a large bf16 GEMM's rate); 8192 tokens, window 1024 + 4, 96 and 8 heads: 0.45 to
-// 0.575 ms, 0.86 to 0.68 PFLOP/s: of its ten key tiles an item four are on an edge, which costs a softmax
+// Measured: 2 x 16,384 tokens behind cached ones, window 4096 + 16, 32 query and 8 kv heads: 1.49 ms,
+// 1310 TFLOP/s (0.70 of a large bf16 GEMM's rate; 1.42 in bursts of a few launches, before the power limit
+// tells); 8192 tokens, window 1024 + 4, 96 and 8 heads: 0.52 to 0.575 ms from run to run, for no cause that was
+// found (0.45 at best), 0.74 to 0.68 PFLOP/s: of its ten key tiles an item four are on an edge, which costs a softmax
 // warp about 1,700 cycles more.  Scores read from TMEM twice instead of held: 3.17 ms on the first; four
-// stages instead of five: 5 % slower; work in fixed turns: 1.44 ms and up to 0.60.
+// stages instead of five: 5 % slower; work in fixed turns: 1.44 ms (where these were 1.42) and up to 0.60.
+// Two issuing warps over two row tiles, and a maximum that moves only past 2^8, are published methods for
+// attention on this chip.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -667,9 +667,15 @@ kda_status kda_qk_norm_rope_append(kda_dtype in_dtype, kda_dtype out_dtype, int3
  *               statistics and sums in fp32, probabilities rounded to bf16 for
  *               the second product.  KDA_FP32: fp32 throughout
  *   max_tokens  >= 1: no request brings more (one that does is refused)
- *   q, o        [T][Hq][128], 16-byte aligned; NULL when T = 0
+ *   q, o        [T][Hq][128], 16-byte aligned; NULL when T = 0.  o is not q
  * The same call gives the same bits again (the split of a long row over CTAs, and with it
  * the order of its sums, goes by the sizes of the call).
+ * An infinity or NaN among the values (bf16) of a key that some tokens of a
+ * request's step see and others do not makes the call slow, not wrong: the rows
+ * next to it are computed one by one, each by a warp at 0.6 to 0.9 us a key
+ * (two tokens behind 131,072: 114 ms instead of 0.12; a prefill of 8192 under a
+ * window of 1024: 8.3 ms instead of 0.54).  A value that all tokens of the step
+ * see, or none, costs nothing; a step of one token a request never meets it.
  * Errors: KDA_ERR_INVALID_ARGUMENT (null/misaligned pointers, sizes below 1,
  * T < 0, sinks < 0, Hq not a multiple of Hkv, dtype), KDA_ERR_UNSUPPORTED
  * (page_size, Hq / Hkv above 128, Hkv above 65535, T * Hq, M page_size or
