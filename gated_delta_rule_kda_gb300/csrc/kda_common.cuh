@@ -292,6 +292,47 @@ struct WindowAttentionArgs {
 #endif
 };
 
+// Attention of requests whose rows share their first tokens: group g holds requests
+// [cu_groups[g], cu_groups[g+1]), whose keys below prefix_len[g] are read through the first one's row.
+struct PrefixAttentionArgs {
+    kda_dtype dtype;
+    int32_t max_tokens, num_q_heads, num_kv_heads, num_groups;
+    const void *q, *kv_pool;  // [T][Hq][128], [P][2][Hkv][page_size][128]
+    const int32_t *cu_groups, *prefix_len;  // [Ng+1], [Ng]
+    float scale;
+    void *o;  // [T][Hq][128]
+    CacheArgs cache;
+    void *workspace;
+    DeviceStatus status;
+#ifdef KDA_DEBUG
+    int32_t withhold;  // test-only: the load warps fetch nothing, and waits give up after 1 ms
+#endif
+};
+
+// The best continuations of a batch of beams.
+struct BeamSelectArgs {
+    kda_dtype dtype;
+    int32_t batch, beams, vocab, choices;
+    const void *logits;  // row (b, k) starts row_stride (b beams + k) elements on
+    int64_t row_stride;
+    const float *scores;   // [B][K]
+    const uint8_t *ended;  // [B][K] or null
+    int32_t end_token;     // -1: none
+    int32_t *parent, *token;  // [B][N]
+    float *score;             // [B][N]
+    uint8_t *ended_out;       // [B][N] or null
+    void *workspace;
+};
+
+// Beams take over their parents' rows: slot [B][K] in place, moves in src, dst [B K].
+struct BeamPlanArgs {
+    int32_t batch, beams, num_rows;
+    const int32_t *parent;  // [B][K]
+    int32_t *slot;          // [B][K]
+    int32_t *src, *dst;     // [B K]
+    DeviceStatus status;
+};
+
 // Moves of pages: pages dst[i] := pages src[i] of each layer, i < *count (or n when null).
 struct PageMoves {
     int32_t num_layers, num_pages, n;
@@ -306,6 +347,7 @@ struct PageForkArgs {
     int32_t *page_table, *kv_len;
     int32_t *free_list, *src, *dst;  // [F] each, in the workspace
     DeviceStatus status;
+    BeamPlanArgs beams;  // beam reordering: what gives parent and child (its dst and src)
 };
 struct PageReleaseArgs {
     int32_t table_rows, table_width, page_size, n, window, sinks;
@@ -328,6 +370,13 @@ cudaError_t launch_qk_norm_rope(const NormRopeArgs &a, cudaStream_t stream);
 cudaError_t launch_window_attention(const WindowAttentionArgs &a, cudaStream_t stream);
 cudaError_t launch_pages_copy(const PageMoves &a, cudaStream_t stream);
 cudaError_t launch_pages_fork(const PageForkArgs &a, cudaStream_t stream);
+cudaError_t launch_prefix_attention(const PrefixAttentionArgs &a, cudaStream_t stream);
+size_t prefix_attention_workspace(kda_dtype dtype, int32_t batch, int32_t total_tokens, int32_t num_groups,
+                                  int32_t num_q_heads, int32_t num_kv_heads);
+cudaError_t launch_beam_select(const BeamSelectArgs &a, cudaStream_t stream);
+size_t beam_select_workspace(int32_t batch, int32_t beams, int32_t vocab, int32_t choices);
+cudaError_t launch_beam_slots(const BeamPlanArgs &a, cudaStream_t stream);
+cudaError_t launch_beam_reorder(const PageForkArgs &a, cudaStream_t stream);
 cudaError_t launch_pages_release(const PageReleaseArgs &a, cudaStream_t stream);
 cudaError_t launch_pages_compact(const PageCompactArgs &a, cudaStream_t stream);
 cudaError_t launch_check_prefill(const CheckArgs &a, cudaStream_t stream);

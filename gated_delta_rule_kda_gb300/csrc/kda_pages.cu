@@ -136,6 +136,91 @@ __device__ __forceinline__ void mark_live(uint32_t *live, const uint32_t *skip, 
     }
 }
 
+// ---------------------------------------------------------------------------
+// Beams
+// ---------------------------------------------------------------------------
+// The rows that beams take (kda_beam_reorder), by one CTA; a warp a prompt, lanes l and l + 32 its beams.
+// `seen`, `twice`: a bit a row each, zeroed; lists: 64 rows a warp.
+__device__ __forceinline__ void beam_plan(const BeamPlanArgs &a, uint32_t *seen, uint32_t *twice, int32_t *lists) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int32_t K = a.beams, n = a.batch * K;
+    for (int32_t i = threadIdx.x; i < n; i += kPlanThreads) {
+        const int32_t r = a.slot[i];
+        if ((uint32_t)r >= (uint32_t)a.num_rows) continue;
+        if (atomicOr(seen + (r >> 5), 1u << (r & 31)) >> (r & 31) & 1u) atomicOr(twice + (r >> 5), 1u << (r & 31));
+    }
+    __syncthreads();
+    int32_t *list = lists + warp * KDA_MAX_BEAMS;
+    for (int32_t b = warp; b < a.batch; b += kPlanThreads / 32) {
+        const int32_t at = b * K;
+        int32_t parent[2], row[2];
+        bool good = true;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int32_t i = lane + 32 * u;
+            parent[u] = -1;
+            row[u] = -1;
+            if (i >= K) continue;
+            parent[u] = a.parent[at + i];
+            if ((uint32_t)parent[u] >= (uint32_t)K) parent[u] = -1;
+            row[u] = a.slot[at + i];
+            good &= (uint32_t)row[u] < (uint32_t)a.num_rows && !(twice[row[u] >> 5] >> (row[u] & 31) & 1u);
+        }
+        if (!__all_sync(kAll, good)) {
+            if (lane == 0) record_status(a.status, KDA_ERR_DEVICE_CHECK, (uint32_t)b);
+            for (int32_t i = lane; i < K; i += 32) a.src[at + i] = a.dst[at + i] = -1;
+            continue;
+        }
+        // of the beams that name a parent the first is its heir
+        bool heir[2] = {parent[0] >= 0, parent[1] >= 0};
+        uint64_t named = 0;  // bit k: beam k has a child
+        for (int32_t j = 0; j < K; ++j) {
+            const int32_t pj = __shfl_sync(kAll, j < 32 ? parent[0] : parent[1], j & 31);
+            if (pj < 0) continue;
+            named |= 1ull << pj;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) heir[u] &= !(j < lane + 32 * u && pj == parent[u]);
+        }
+        const uint64_t heirs = (uint64_t)__ballot_sync(kAll, heir[1]) << 32 | __ballot_sync(kAll, heir[0]);
+        // the rows of beams without a child, in order
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int32_t i = lane + 32 * u;
+            if (i < K && !(named >> i & 1)) list[__popcll(~named & ((1ull << i) - 1))] = row[u];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int32_t i = lane + 32 * u;
+            const int32_t p = max(parent[u], 0);
+            const int32_t low = __shfl_sync(kAll, row[0], p & 31), high = __shfl_sync(kAll, row[1], p & 31);
+            const int32_t held = parent[u] < 0 ? -1 : p < 32 ? low : high;
+            if (i < K) {  // (as many others as rows without a child: each parent has one heir)
+                const int32_t taken = heir[u] ? held : list[__popcll(~heirs & ((1ull << i) - 1))];
+                a.slot[at + i] = taken;
+                a.src[at + i] = heir[u] ? -1 : held;
+                a.dst[at + i] = heir[u] ? -1 : taken;
+            }
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+}
+
+// The plan alone (no cache).
+__global__ void __launch_bounds__(kPlanThreads) beam_plan_kernel(const BeamPlanArgs a) {
+    extern __shared__ uint32_t smem[];
+    __shared__ int32_t lists[kPlanThreads / 32 * KDA_MAX_BEAMS];
+    const int32_t words = (a.num_rows + 31) / 32;
+    for (int32_t i = threadIdx.x; i < 2 * words; i += kPlanThreads) smem[i] = 0;
+    grid_wait();
+    __syncthreads();
+    beam_plan(a, smem, smem + words, lists);
+}
+
+// kBeams: parent and child are the src and dst of a.beams, which are worked out first.
+template <bool kBeams>
 __global__ void __launch_bounds__(kPlanThreads) pages_fork_plan_kernel(const PageForkArgs a) {
     extern __shared__ uint32_t smem[];
     __shared__ int32_t warp_sums[32];
@@ -144,9 +229,16 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_plan_kernel(const Pag
     uint32_t *live = smem, *is_child = smem + words;
     const int tid = threadIdx.x;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the copies come up meanwhile
-    for (int32_t i = tid; i < words + row_words; i += kPlanThreads) smem[i] = 0;
+    const int32_t zeroed = kBeams ? max(words + row_words, 2 * row_words) : words + row_words;
+    for (int32_t i = tid; i < zeroed; i += kPlanThreads) smem[i] = 0;
     grid_wait();
     __syncthreads();
+    if constexpr (kBeams) {  // the beams' two bits a row lie where the pages' will
+        __shared__ int32_t lists[kPlanThreads / 32 * KDA_MAX_BEAMS];
+        beam_plan(a.beams, smem, smem + row_words, lists);
+        for (int32_t i = tid; i < zeroed; i += kPlanThreads) smem[i] = 0;
+        __syncthreads();
+    }
     for (int32_t i = tid; i < F; i += kPlanThreads) {
         const int32_t c = a.child[i];
         if ((uint32_t)c < (uint32_t)R && c != a.parent[i]) atomicOr(is_child + (c >> 5), 1u << (c & 31));
@@ -196,7 +288,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_plan_kernel(const Pag
             const int32_t fresh = half ? a.free_list[k] : -1;
             a.src[i] = !ok ? kRefused : half ? old : -1;
             a.dst[i] = fresh;
-            if (!ok) record_status(a.status, KDA_ERR_DEVICE_CHECK, (uint32_t)i);
+            if (!ok && !(kBeams && parent < 0)) record_status(a.status, KDA_ERR_DEVICE_CHECK, (uint32_t)i);
             if ((uint32_t)child < (uint32_t)R && child != parent) a.kv_len[child] = ok ? length : 0;
         }
         __syncthreads();
@@ -317,7 +409,19 @@ cudaError_t launch_pages_copy(const PageMoves &m, cudaStream_t stream) {
 cudaError_t launch_pages_fork(const PageForkArgs &a, cudaStream_t stream) {
     if (a.moves.n == 0) return cudaSuccess;
     const size_t smem = 4 * (((size_t)a.moves.num_pages + 31) / 32 + ((size_t)a.table_rows + 31) / 32);
-    const cudaError_t e = launch_plan(pages_fork_plan_kernel, smem, stream, a);
+    const cudaError_t e = launch_plan(pages_fork_plan_kernel<false>, smem, stream, a);
+    return e == cudaSuccess ? launch_pages_copy(a.moves, stream) : e;
+}
+
+cudaError_t launch_beam_slots(const BeamPlanArgs &a, cudaStream_t stream) {
+    const size_t smem = 8 * (((size_t)a.num_rows + 31) / 32);
+    return launch_plan(beam_plan_kernel, smem, stream, a);
+}
+
+cudaError_t launch_beam_reorder(const PageForkArgs &a, cudaStream_t stream) {
+    const size_t words = ((size_t)a.moves.num_pages + 31) / 32, row_words = ((size_t)a.table_rows + 31) / 32;
+    const size_t smem = 4 * (row_words + (words > row_words ? words : row_words));
+    const cudaError_t e = launch_plan(pages_fork_plan_kernel<true>, smem, stream, a);
     return e == cudaSuccess ? launch_pages_copy(a.moves, stream) : e;
 }
 

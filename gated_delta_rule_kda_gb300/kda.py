@@ -66,6 +66,12 @@ EXPORTED = (
     "kda_pages_fork",
     "kda_pages_release",
     "kda_pages_compact",
+    "kda_prefix_attention_workspace_size",
+    "kda_prefix_attention",
+    "kda_beam_select_workspace_size",
+    "kda_beam_select",
+    "kda_beam_reorder_workspace_size",
+    "kda_beam_reorder",
     "kda_check_prefill_inputs",
     "kda_get_device_status",
     "kda_debug_inject_handoff_timeout",
@@ -164,6 +170,18 @@ def _load() -> ctypes.CDLL:
     lib.kda_pages_release.restype = ctypes.c_int
     lib.kda_pages_compact.argtypes = [I32, I32, I64, I32, I32, P, P, P, P, P, SZ, P]
     lib.kda_pages_compact.restype = ctypes.c_int
+    lib.kda_prefix_attention_workspace_size.argtypes = [ctypes.c_int] + [I32] * 5
+    lib.kda_prefix_attention_workspace_size.restype = SZ
+    lib.kda_prefix_attention.argtypes = [ctypes.c_int] + [I32] * 10 + [P] * 8 + [F, P, P, SZ, P]
+    lib.kda_prefix_attention.restype = ctypes.c_int
+    lib.kda_beam_select_workspace_size.argtypes = [I32] * 4
+    lib.kda_beam_select_workspace_size.restype = SZ
+    lib.kda_beam_select.argtypes = [ctypes.c_int, I32, I32, I32, I32, P, I64, P, P, I32, P, P, P, P, P, SZ, P]
+    lib.kda_beam_select.restype = ctypes.c_int
+    lib.kda_beam_reorder_workspace_size.argtypes = [I32, I32]
+    lib.kda_beam_reorder_workspace_size.restype = SZ
+    lib.kda_beam_reorder.argtypes = [I32, I32, I32, P, P, P, P, I32, I32, I64, I32, I32, P, P, P, P, SZ, P]
+    lib.kda_beam_reorder.restype = ctypes.c_int
     lib.kda_check_prefill_inputs.argtypes = [I32, I32, I32, P, I32, P, P]
     lib.kda_check_prefill_inputs.restype = ctypes.c_int
     lib.kda_get_device_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
@@ -837,6 +855,149 @@ def kda_pages_compact(pool, page_table, *, table_out=None, num_live=None, worksp
     _check("kda_pages_compact", _lib.kda_pages_compact(L, P, nbytes, R, M, tin, tout, live, _ptr(pool, dev),
                                                        _ptr(workspace, dev), wbytes, _launch(stream, dev)))
     return table_out, num_live
+
+
+def _workspace(workspace, size, sizes, device, stream):
+    """A workspace and its bytes: the caller's, or one of what `size` says for these sizes."""
+    if workspace is None:
+        n = size(*sizes)
+        workspace = _empty(max(n, 16), torch.uint8, device, stream)
+        return workspace, n
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def kda_prefix_attention_workspace_size(dtype: torch.dtype, requests: int, tokens: int, groups: int, q_heads: int,
+                                        kv_heads: int) -> int:
+    return int(_lib.kda_prefix_attention_workspace_size(_elem(dtype), requests, tokens, groups, q_heads, kv_heads))
+
+
+def kda_prefix_attention(q, kv_pool, page_table, slot, cu_tokens, kv_len, cu_groups, prefix_len, scale=DEFAULT_SCALE, *,
+                         max_tokens=None, o=None, workspace=None, stream=None):
+    """Causal attention of q [T, Hq, 128] over the requests' rows of the cache, where the rows of group g's requests
+    [cu_groups[g], cu_groups[g+1]) share their first prefix_len[g] tokens: those are read once for the group, through
+    its first request's row.  cu_groups [Ng+1] and prefix_len [Ng] int32 on the device; the other arguments as
+    kda_window_attention's.  Returns o."""
+    shape, dtype, dev = q.shape, q.dtype, q.get_device()
+    T, Hq, d = shape
+    P, Hkv, page = _pool_shape(kv_pool)
+    if kv_pool.dtype is not dtype:
+        raise TypeError("q and kv_pool must have one type")
+    if o is None:
+        o = _empty(shape, dtype, q.device, stream)
+    elif o.shape != shape or o.dtype is not dtype:
+        raise ValueError("o must have q's shape and type")
+    if d != HEAD_DIM:
+        raise ValueError("q must be [tokens, heads, 128]")
+    B, rows, width, (pt, sl, cu, kl) = _cache_args(dev, page_table, slot, cu_tokens, kv_len)
+    Ng = prefix_len.numel()
+    if cu_groups.numel() != Ng + 1:
+        raise ValueError("cu_groups must have one entry more than prefix_len")
+    cg, pl = _ptrs(dev, _I32, cu_groups, prefix_len)
+    code = _elem(dtype)
+    workspace, wbytes = _workspace(workspace, _lib.kda_prefix_attention_workspace_size, (code, B, T, Ng, Hq, Hkv),
+                                   q.device, stream)
+    rc = _lib.kda_prefix_attention(code, B, T, max(T, 1) if max_tokens is None else _count(max_tokens), Hq, Hkv, P, page,
+                                   rows, width, Ng, _ptr(q, dev), _ptr(kv_pool, dev), pt, sl, cu, kl, cg, pl, scale,
+                                   _ptr(o, dev), _ptr(workspace, dev), wbytes, _launch(stream, dev))
+    _check("kda_prefix_attention", rc)
+    return o
+
+
+MAX_BEAMS = 64  # KDA_MAX_BEAMS in include/kda.h
+
+
+def _flags(t: torch.Tensor, shape, dev: int):
+    """The pointer of bytes (bool or uint8) of this shape."""
+    if t.dtype not in (torch.bool, torch.uint8):
+        raise TypeError(f"expected bool or uint8, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"expected {tuple(shape)}, got {tuple(t.shape)}")
+    return _ptr(t, dev)
+
+
+def kda_beam_select_workspace_size(prompts: int, beams: int, vocab: int, choices: int) -> int:
+    return int(_lib.kda_beam_select_workspace_size(prompts, beams, vocab, choices))
+
+
+def kda_beam_select(logits, scores, choices=None, *, ended=None, end_token=-1, parent=None, token=None, score=None,
+                    ended_out=None, workspace=None, stream=None):
+    """The `choices` best continuations (default: as many as beams) of each prompt's beams: logits [B, K, V] (dense in
+    the vocabulary, any stride from row to row: a slice of a padded output is fine), scores [B, K] fp32 the beams'
+    totals so far (-inf: no such beam), ended [B, K] bool the beams that continue as they are, with end_token.
+    Returns (parent, token [B, N] int32, score [B, N] fp32, ended_out [B, N] bool), best first."""
+    dev = logits.get_device()
+    B, K, V = logits.shape
+    N = K if choices is None else choices
+    if not 1 <= N <= MAX_BEAMS:  # (no outputs of that size are made for the call to refuse)
+        raise KdaError("kda_beam_select", 1 if N < 1 else 2)
+    sb, sk, sv = logits.stride()
+    if (sv != 1 and V > 1) or (B > 1 and sb != K * sk):
+        raise ValueError("the rows of logits must be dense and evenly spaced")
+    stride = sk if K > 1 else sb if B > 1 else V
+    shape = torch.Size((B, N))
+    if scores.shape != logits.shape[:2]:
+        raise ValueError("scores must be [prompts, beams]")
+    if parent is None:
+        parent = _empty(shape, _I32, logits.device, stream)
+    if token is None:
+        token = _empty(shape, _I32, logits.device, stream)
+    if score is None:
+        score = _empty(shape, _F32, logits.device, stream)
+    if ended_out is None:
+        ended_out = _empty(shape, torch.bool, logits.device, stream)
+    if parent.shape != shape or token.shape != shape or score.shape != shape:
+        raise ValueError("parent, token and score must be [prompts, choices]")
+    code = _elem(logits.dtype)
+    pa, to = _ptrs(dev, _I32, parent, token)
+    sc, so = _ptrs(dev, _F32, scores, score)
+    en = None if ended is None else _flags(ended, logits.shape[:2], dev)
+    eo = _flags(ended_out, shape, dev)
+    workspace, wbytes = _workspace(workspace, _lib.kda_beam_select_workspace_size, (B, K, V, N), logits.device, stream)
+    rc = _lib.kda_beam_select(code, B, K, V, N, logits.data_ptr(), stride, sc, en,
+                              max(-2, min(end_token, 0x7fffffff)), pa, to, so, eo,
+                              _ptr(workspace, dev), wbytes, _launch(stream, dev))
+    _check("kda_beam_select", rc)
+    return parent, token, score, ended_out
+
+
+def kda_beam_reorder_workspace_size(num_pages: int, num_rows: int) -> int:
+    return int(_lib.kda_beam_reorder_workspace_size(num_pages, num_rows))
+
+
+def kda_beam_reorder(parent, slot, pool=None, page_table=None, kv_len=None, page_size=0, *, num_rows=None, src=None,
+                     dst=None, workspace=None, stream=None):
+    """New beams [B, K] take over the rows of their parents (parent [B, K] int32: beams of their prompt): slot [B, K]
+    int32, in place.  A parent's first child keeps its row; the others take the rows of beams without a child, as
+    branches in the cache (pool [layers, pages, ...], page_table [R, M], kv_len [R]; None: no cache, and num_rows
+    says how many rows there are).  Returns (src, dst) [B K] int32, the rows that kda_pages_copy copies in the pools
+    of recurrent and convolution states."""
+    dev = slot.get_device()
+    shape = slot.shape
+    if len(shape) != 2 or parent.shape != shape:
+        raise ValueError("parent and slot must be [prompts, beams]")
+    B, K = shape
+    n = B * K
+    if src is None:
+        src = _empty(n, _I32, slot.device, stream)
+    if dst is None:
+        dst = _empty(n, _I32, slot.device, stream)
+    if src.numel() != n or dst.numel() != n:
+        raise ValueError("src and dst must have an entry for each beam")
+    pa, sl, s, d = _ptrs(dev, _I32, parent, slot, src, dst)
+    if page_table is None:
+        if pool is not None or kv_len is not None or num_rows is None:
+            raise ValueError("without a table there is no pool and no kv_len, and num_rows must be given")
+        cache, rest = (_count(num_rows),), (0, 0, 0, 0, 0, None, None, None, None, 0)
+    else:
+        R, M = page_table.shape
+        if kv_len.numel() != R or num_rows not in (None, R):
+            raise ValueError("kv_len must have one entry per table row, of which there are num_rows")
+        L, P, nbytes = _layers(pool)
+        workspace, wbytes = _workspace(workspace, _lib.kda_beam_reorder_workspace_size, (P, R), pool.device, stream)
+        pt, kl = _ptrs(dev, _I32, page_table, kv_len)
+        cache, rest = (R,), (L, P, nbytes, _count(page_size), M, pt, kl, _ptr(pool, dev), _ptr(workspace, dev), wbytes)
+    _check("kda_beam_reorder", _lib.kda_beam_reorder(B, K, *cache, pa, sl, s, d, *rest, _launch(stream, dev)))
+    return src, dst
 
 
 def kda_check_prefill_inputs(cu_seqlens, log_alpha=None, total_tokens=None, num_heads=1,

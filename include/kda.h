@@ -756,6 +756,159 @@ kda_status kda_pages_compact(int32_t num_layers, int32_t num_pages, int64_t page
                              int32_t *table_out, int32_t *num_live, void *pool, void *workspace,
                              size_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Branches of a request: beams, samples, drafts
+ *
+ * kda_pages_fork leaves rows that share the whole pages of their first tokens.
+ * The calls below decode such rows: attention that reads the shared keys once
+ * for all of them, the choice of the best continuations over the vocabulary,
+ * and the exchange of cache rows and states that follows from it.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Bytes of workspace for kda_prefix_attention.
+ */
+size_t kda_prefix_attention_workspace_size(kda_dtype dtype, int32_t batch, int32_t total_tokens,
+                                           int32_t num_groups, int32_t num_q_heads,
+                                           int32_t num_kv_heads);
+
+/*
+ * kda_prefix_attention - causal attention of the step's tokens over their rows
+ * of the cache, for groups of requests whose rows share their first tokens:
+ *
+ *   o = sum_j softmax_j(scale q . k_j) v_j  over 0 <= j <= p with the page of j
+ *       mapped; key j < prefix_len[g] is read through the row of the group's
+ *       first request, key j >= prefix_len[g] through the request's own
+ * Where the rows of a group hold the same tokens below prefix_len[g] (as
+ * kda_pages_fork leaves them) this is what kda_window_attention computes with
+ * window = INT32_MAX; the shared keys are read once for the whole group, and
+ * the rows of all its requests fill the tensor-core tiles together.  A token
+ * that sees no key gives 0.  Nothing outside a token's visible keys reaches it,
+ * whatever is stored there (NaN and infinities included).
+ *
+ *   dtype       of q, kv_pool and o.  KDA_BF16: tensor cores; scores, softmax
+ *               statistics and sums in fp32, probabilities rounded to bf16 for
+ *               the second product.  KDA_FP32: fp32 throughout
+ *   max_tokens  >= 1: no request brings more (one that does is refused)
+ *   cu_groups   [Ng+1] int32 (device): group g holds requests [cu_groups[g],
+ *               cu_groups[g+1]), 0 = cu_groups[0] <= ... <= cu_groups[Ng] = B
+ *   prefix_len  [Ng] int32 (device), any length >= 0 (whole pages or not), no
+ *               longer than what the group's requests held before the step:
+ *               prefix_len[g] <= kv_len[row] - n_b
+ *   q, o        [T][Hq][128], 16-byte aligned; NULL when T = 0.  o is not q
+ *   workspace   kda_prefix_attention_workspace_size() bytes, 16-byte aligned;
+ *               not shared by calls that overlap on the GPU
+ *   (cache arguments as above)
+ * Any number of tokens a request is right; the call is built for a few (single
+ * tokens, the verify of a draft): requests that bring hundreds fill the tiles
+ * alone, and kda_window_attention is then the faster call.
+ * The same call gives the same bits again.
+ * Errors: KDA_ERR_INVALID_ARGUMENT (null/misaligned pointers, sizes below 1,
+ * T < 0, Hq not a multiple of Hkv, dtype), KDA_ERR_WORKSPACE,
+ * KDA_ERR_UNSUPPORTED (as kda_window_attention; more than 2^20 requests or
+ * groups), KDA_ERR_CUDA.  A request whose slot, kv_len or token range is out of
+ * range, that no group holds, or whose group's prefix_len is longer than
+ * kv_len[row] - n_b or whose group's first slot is out of range, is refused by
+ * the kernel (its rows of o stay as they are; KDA_ERR_DEVICE_CHECK with
+ * detail = b).
+ */
+kda_status kda_prefix_attention(kda_dtype dtype, int32_t batch, int32_t total_tokens,
+                                int32_t max_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t num_pages, int32_t page_size, int32_t table_rows,
+                                int32_t table_width, int32_t num_groups, const void *q,
+                                const void *kv_pool, const int32_t *page_table,
+                                const int32_t *slot, const int32_t *cu_tokens,
+                                const int32_t *kv_len, const int32_t *cu_groups,
+                                const int32_t *prefix_len, float scale, void *o, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/* Most beams of a prompt, and most continuations chosen for one. */
+#define KDA_MAX_BEAMS 64
+
+/* Bytes of workspace for kda_beam_select. */
+size_t kda_beam_select_workspace_size(int32_t batch, int32_t beams, int32_t vocab, int32_t choices);
+
+/*
+ * kda_beam_select - the best continuations of each prompt's beams.
+ *
+ * For prompt b, beam k and token v the continuation's total is
+ *   scores[b][k] + x[v] - log sum_u e^x[u],   x = the logits of row (b, k)
+ * and the N = choices best of the K V continuations are given in falling order:
+ * of equal totals that of the lower beam, in a beam that of the higher logit,
+ * then the lower token.  A beam that has ended has one continuation, its own:
+ * (k, end_token) with total scores[b][k]; its logits are not read.  A total of
+ * -inf is never chosen; where fewer than N are left the rest is parent = -1,
+ * token = -1, score = -inf, ended_out = 0.
+ * Exponentials and partial sums are fp32; log-sum-exp and totals are formed and
+ * compared in 64 bits, and rounded to fp32 once.  A NaN among logits or scores
+ * counts as -inf, a logit of +inf as the largest fp32 number.
+ *
+ *   dtype       of the logits
+ *   batch       B >= 1 prompts; beams K and choices N in [1, KDA_MAX_BEAMS]
+ *   vocab       V >= 1
+ *   logits      row (b, k) of V logits starts row_stride (b K + k) elements on:
+ *               a slice of a padded output is fine; aligned to its element
+ *   scores      [B][K] fp32, the beams' totals so far (-inf: no such beam)
+ *   ended       [B][K] bytes, not 0 for a beam that has ended; NULL: none has
+ *   end_token   the token that ends a beam, in [0, V); -1: none (ended NULL)
+ *   parent      [B][N] int32: the beam k;  token [B][N] int32: v
+ *   score       [B][N] fp32: the total
+ *   ended_out   [B][N] bytes or NULL: 1 where the parent had ended or the token
+ *               is end_token
+ *   workspace   kda_beam_select_workspace_size() bytes, 16-byte aligned; not
+ *               shared by calls that overlap on the GPU
+ * The outputs overlap no input.
+ * Errors: KDA_ERR_INVALID_ARGUMENT (null/misaligned pointers, sizes, dtype, a
+ * row_stride below V, end_token), KDA_ERR_WORKSPACE, KDA_ERR_UNSUPPORTED (more
+ * than KDA_MAX_BEAMS beams or choices, V above 2^21, B K above 2^20),
+ * KDA_ERR_CUDA.
+ */
+kda_status kda_beam_select(kda_dtype dtype, int32_t batch, int32_t beams, int32_t vocab,
+                           int32_t choices, const void *logits, int64_t row_stride,
+                           const float *scores, const uint8_t *ended, int32_t end_token,
+                           int32_t *parent, int32_t *token, float *score, uint8_t *ended_out,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace for kda_beam_reorder with a cache. */
+size_t kda_beam_reorder_workspace_size(int32_t num_pages, int32_t num_rows);
+
+/*
+ * kda_beam_reorder - beams take over their parents' rows (of the cache's table,
+ * and of the pools of recurrent and convolution states, which one slot names).
+ *
+ * Of the new beams of prompt b that name parent k, the first keeps row
+ * slot[b][k]; the others take, in order, the rows of beams that no new beam
+ * names, in order.  slot is rewritten; for each of the others src[b K + i] =
+ * the parent's row and dst[b K + i] = its own, for the first ones -1, -1.  A
+ * beam whose parent is outside [0, K) has no tokens: it takes a row as the
+ * others do, with src = -1.  With kda_pages_copy over the state pools, given
+ * src and dst, every beam then has its parent's state, and only second children
+ * have moved any.
+ * With a cache (page_table not NULL) the rows dst become branches of src as by
+ * kda_pages_fork, in one call: whole pages shared, a part-filled last one
+ * copied to the lowest free page in every layer, the pages that only the row's
+ * former beam named released, rows without tokens emptied.
+ *
+ *   batch, beams  B >= 1; K in [1, KDA_MAX_BEAMS];  B K <= num_rows
+ *   num_rows    rows of the table and of the state pools
+ *   parent      [B][K] int32
+ *   slot        [B][K] int32, all different, in [0, num_rows); in and out
+ *   src, dst    [B K] int32 out
+ *   (cache arguments as kda_pages_fork; not read when page_table is NULL)
+ * A prompt with a slot out of range, or that another beam of the call has too,
+ * is refused by the kernel (its slots stay, src and dst are -1;
+ * KDA_ERR_DEVICE_CHECK with detail = b).  A branch whose parent row's kv_len is
+ * out of range, or for which no page is left, is refused as by kda_pages_fork
+ * (its row is left empty; detail = b K + i).
+ * Errors: KDA_ERR_INVALID_ARGUMENT, KDA_ERR_WORKSPACE, KDA_ERR_UNSUPPORTED
+ * (K above KDA_MAX_BEAMS, num_rows above 2^18, others as kda_pages_fork).
+ */
+kda_status kda_beam_reorder(int32_t batch, int32_t beams, int32_t num_rows, const int32_t *parent,
+                            int32_t *slot, int32_t *src, int32_t *dst, int32_t num_layers,
+                            int32_t num_pages, int64_t page_bytes, int32_t page_size,
+                            int32_t table_width, int32_t *page_table, int32_t *kv_len, void *pool,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
 /*
  * kda_check_prefill_inputs - the contents checks the host cannot make before a
  * prefill: cu_seqlens starts at 0, never decreases and ends at total_tokens;

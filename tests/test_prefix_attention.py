@@ -1,0 +1,338 @@
+"""Attention over a shared prefix against a 64-bit plain implementation.
+
+Tolerances, elementwise, as for the windowed attention.  bf16: a probability rounded to bf16 is off by
+at most 2^-8 of itself and so is the rounded output; the fp32 parts (128-term scores, exponentials,
+sums, the join of the parts) stay below 2^-12 of it.  With a = sum_j softmax_j |v_j| that is
+|o - ref| <= 2^-8 (a + |ref|) + 2^-12 a.  fp32: max-abs over rms 1e-5, the bound of every fp32 path here.
+"""
+import numpy as np
+import pytest
+import torch
+
+from tests._branches import build_branches, prefix64
+from tests._cache import cu_of, queries
+from tests._parity import TOL_FP32, assert_close, to64
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def kda():
+    from gated_delta_rule_kda_gb300 import build
+    build.build()
+    from gated_delta_rule_kda_gb300 import kda as mod
+    return mod
+
+
+def call(kda, q, c, new, **kw):
+    kw.setdefault("max_tokens", max(list(new) + [1]))
+    o = kda.kda_prefix_attention(q, c["pool"], c["table"], c["slot"], cu_of(new), c["kv_len"], c["cu_groups"],
+                                 c["prefix_len"], **kw)
+    torch.cuda.synchronize()
+    return o
+
+
+def check(o, q, c, new, scale=128 ** -0.5):
+    ref, a = prefix64(q, c, new, scale)
+    o64 = to64(o)
+    if o.dtype == FP32:
+        return assert_close(o64, ref, TOL_FP32, "o")
+    assert np.isfinite(o64).all()
+    over = np.abs(o64 - ref) - (2.0 ** -8 * (a + np.abs(ref)) + 2.0 ** -12 * a)
+    assert over.max(initial=-1.0) <= 1e-30, f"{over.max():.3e} over the bound at {np.unravel_index(over.argmax(), over.shape)}"
+
+
+# (prefix of each group, [own tokens of each branch] of each group, tokens of the step of each branch, kv heads, group, page)
+SHAPES = [
+    ([0], [[1]], [1], 1, 1, 16),                                             # one token that sees itself
+    ([1], [[1]], [1], 1, 1, 16),
+    ([64], [[1, 1]], [1, 1], 2, 4, 64),                                      # a tile, and nothing of its own before
+    ([500], [[1, 9, 30]], [1, 1, 1], 2, 12, 64),                             # beams, a prefix that ends inside a page
+    ([127, 128, 129, 0], [[3], [1, 2], [4, 4, 4], [5, 70]], [1] * 8, 1, 8, 32),   # tile edges, a group without a prefix
+    ([1000, 37], [[20, 300], [5]], [2, 3, 5], 2, 3, 16),                     # drafts
+    ([300], [[6] * 33], [1] * 33, 1, 16, 128),                               # 528 rows: more than two row tiles
+    ([700, 1300], [[4] * 20, [130] * 3], [1] * 23, 1, 6, 64),
+    ([77], [[40, 2, 9], []], [0, 2, 7], 1, 5, 16),                           # a request without tokens, a group without requests
+    ([260], [[400]], [300], 1, 2, 32),                                           # many tokens of one request
+    ([90], [[70, 90]], [64, 33], 2, 4, 16),
+    ([150], [[20] * 3], [9, 1, 20], 1, 33, 64),                              # odd heads a kv head
+    ([140], [[9, 3]], [2, 1], 1, 128, 32),                                   # one kv head of 128 query heads
+    ([5000], [[3, 70]], [1, 1], 1, 2, 128),                                  # one item over many CTAs
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_against_64_bits(kda, shape, dtype):
+    prefix, mine, new, heads, group, page = shape
+    c = build_branches(prefix + [0] * (len(mine) - len(prefix)), mine, page, heads, dtype, seed=len(new) * 31 + page)
+    q = queries(sum(new), heads * group, dtype, 3)
+    o = call(kda, q, c, new)
+    assert kda.kda_get_device_status()[0] == 0
+    check(o, q, c, new)
+
+
+def test_many_groups(kda):
+    """More groups than a CTA has threads, of all kinds of lengths, some without requests."""
+    rng = np.random.RandomState(5)
+    prefix = [int(rng.choice([0, 3, 16, 40, 129])) for _ in range(900)]
+    mine = [[int(rng.randint(1, 20)) for _ in range(rng.randint(0, 3))] for _ in prefix]
+    new = [1] * sum(len(m) for m in mine)
+    for dtype in (BF16, FP32):
+        c = build_branches(prefix, mine, 16, 1, dtype, seed=3)
+        q = queries(len(new), 2, dtype, 3)
+        o = call(kda, q, c, new)
+        assert kda.kda_get_device_status()[0] == 0
+        check(o, q, c, new)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_same_as_window_attention_without_a_window(kda, dtype):
+    """Rows that share their prefix: the two calls differ by roundings alone."""
+    new = [1, 2, 1, 4]
+    c = build_branches([333, 64], [[7, 40], [1, 90]], 32, 2, dtype, seed=7)
+    q = queries(sum(new), 16, dtype, 7)
+    o = call(kda, q, c, new)
+    w = kda.kda_window_attention(q, c["pool"], c["table"], c["slot"], cu_of(new), c["kv_len"], None, max_tokens=4)
+    ref, a = prefix64(q, c, new)
+    if dtype == FP32:
+        assert_close(to64(o), to64(w), 2 * TOL_FP32, "o")
+    else:
+        assert (np.abs(to64(o) - to64(w)) <= 2 * (2.0 ** -8 * (a + np.abs(ref)) + 2.0 ** -12 * a)).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_the_prefix_is_read_through_the_first_request_s_row(kda, dtype):
+    """What the other rows name below the prefix's length is not read: they may name nothing."""
+    new = [1, 1, 1]
+    c = build_branches([200], [[30, 5, 70]], 16, 2, dtype, seed=11)
+    q = queries(3, 8, dtype, 11)
+    want = call(kda, q, c, new)
+    slot = c["slot"].tolist()
+    c["table"][slot[1], : 200 // 16] = -1
+    c["table"][slot[2], : 200 // 16] = c["pool"].shape[0] + 5
+    assert torch.equal(call(kda, q, c, new), want)
+    check(want, q, c, new)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("new", [[1, 1], [3, 2], [40, 2]])
+def test_unmapped_pages_hold_no_keys(kda, new, dtype):
+    """Pages missing from the prefix and from a request's own keys; a request that has none left at all gives 0."""
+    c = build_branches([150, 90], [[60], [50]], 16, 2, dtype, seed=13)
+    slot = c["slot"].tolist()
+    c["table"][slot[0], 2] = -1
+    c["table"][slot[0], 150 // 16 + 1] = c["pool"].shape[0]
+    c["table"][slot[1], :] = -7
+    q = queries(sum(new), 6, dtype, 13)
+    o = call(kda, q, c, new)
+    assert kda.kda_get_device_status()[0] == 0
+    assert bool((o[new[0]:] == 0).all())
+    check(o, q, c, new)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf"), 3e38])
+@pytest.mark.parametrize("new", [[1, 1], [3, 5], [50, 2]])
+def test_what_no_token_sees_does_not_reach_the_output(kda, new, value, dtype):
+    """Behind the rows' last tokens, in pages that no row names, and in the pages of the prefix behind its end as the
+    other branches have them."""
+    page, lp, mine = 32, 149, [60, 71]
+    c = build_branches([lp], [mine], page, 2, dtype, seed=17)
+    slot, table = c["slot"].tolist(), c["table"].tolist()
+    named = {x for r in slot for x in table[r]} - {-1}
+    for p in range(c["pool"].shape[0]):
+        if p not in named:
+            c["pool"][p] = value
+    for r, n in zip(slot, mine):
+        if (lp + n) % page:
+            c["pool"][table[r][(lp + n) // page], :, :, (lp + n) % page:] = value
+    # the second branch's copy of the prefix's last part-filled page: its part below the prefix's end is not read
+    c["pool"][table[slot[1]][lp // page], :, :, : lp % page] = value
+    clean = {**c, "pool": torch.nan_to_num(c["pool"].float(), 0.0, 0.0, 0.0).to(dtype)}
+    q = queries(sum(new), 8, dtype, 17)
+    o = call(kda, q, c, new)
+    check(o, q, clean, new)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("n", [4, 30])
+def test_a_later_token_s_nan_stays_its_own(kda, n, value, dtype):
+    """A value of the step itself that is not finite: tokens before it and the other branch are untouched."""
+    new, lp, bad = [n, 2], 70, n // 2
+    c = build_branches([lp], [[20 + n, 9]], 16, 1, dtype, seed=19)
+    row = c["table"][c["slot"][0].item()].tolist()
+    j = lp + 20 + bad
+    clean = {**c, "pool": c["pool"].clone()}
+    c["pool"][row[j // 16], 1, :, j % 16, 3] = value
+    q = queries(sum(new), 4, dtype, 19)
+    o, ref = call(kda, q, c, new), call(kda, q, clean, new)
+    assert torch.isfinite(o[:bad]).all() and torch.isfinite(o[n:]).all()
+    assert not torch.isfinite(o[bad:n, :, 3]).any()
+    check(torch.cat([o[:bad], ref[bad:n], o[n:]]), q, clean, new)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("scale", [0.0, -0.2, 3.0, 1e-3])
+def test_scales(kda, scale, dtype):
+    new = [1, 2]
+    c = build_branches([100], [[20, 33]], 32, 1, dtype, seed=23)
+    q = queries(3, 4, dtype, 23)
+    check(call(kda, q, c, new, scale=scale), q, c, new, scale)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_scores_of_any_size(kda, dtype):
+    """Scores of the prefix far above and far below those of the own keys: the join keeps what counts.  fp32: a score
+    is a sum of 128 rounded products, off by up to d = 128 2^-24 scale sum_i |q_i k_i|, which moves a weight by
+    e^(2 d) and the output by (e^(2 d) - 1) (a + |ref|); with scores of some hundreds that is above the usual bound."""
+    new = [1, 1, 1]
+    for factor in (30.0, 0.01):
+        c = build_branches([300], [[9, 40, 100]], 32, 1, dtype, seed=29)
+        names = c["table"][c["slot"][0].item(), : 300 // 32].long()
+        c["pool"][names, 0] *= factor
+        q = queries(3, 8, dtype, 29) * 4
+        o = call(kda, q, c, new)
+        if dtype == BF16:
+            check(o, q, c, new)
+            continue
+        ref, a = prefix64(q, c, new)
+        keys = c["pool"][:, 0].double().abs().reshape(-1, 128)
+        d = 128 * 2.0 ** -24 * 128 ** -0.5 * (q.double().abs() @ keys.T).amax(-1).cpu().numpy()[..., None]
+        bound = np.expm1(2 * d) * (a + np.abs(ref)) + TOL_FP32 * np.sqrt((ref ** 2).mean())
+        assert (np.abs(to64(o) - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_refused_requests_leave_their_rows(kda, dtype):
+    """Slots, lengths, token ranges and prefixes out of range are refused one by one; the others are computed."""
+    new, lp = [1, 2, 1, 1], [100, 40]
+    c = build_branches(lp, [[20, 30], [9, 5]], 16, 1, dtype, seed=31)
+    q = queries(5, 4, dtype, 31)
+    good = call(kda, q, c, new)
+    check(good, q, c, new)
+    first = [0, 1, 3, 4, 5]
+
+    def run(refused, detail, max_tokens=2, **change):
+        o = torch.full_like(q, 7.0)
+        d = {**{k: v.clone() for k, v in c.items()}, **change}
+        call(kda, q, d, new, o=o, max_tokens=max_tokens)
+        assert kda.kda_get_device_status() == (6, detail)
+        for b in range(4):
+            part = slice(first[b], first[b + 1])
+            assert torch.equal(o[part], torch.full_like(o[part], 7.0) if b in refused else good[part]), b
+
+    def put(name, i, x):
+        t = c[name].clone()
+        t[i] = x
+        return {name: t}
+
+    rows = c["table"].shape[0]
+    run({1}, 1, **put("slot", 1, rows))
+    run({1}, 1, **put("slot", 1, -1))
+    run({3}, 3, **put("kv_len", c["slot"][3].item(), -1))
+    run({3}, 3, **put("kv_len", c["slot"][3].item(), c["table"].shape[1] * 16 + 1))
+    run({1}, 1, **put("kv_len", c["slot"][1].item(), 101))     # two tokens, one of them inside the prefix
+    run({1}, 1, max_tokens=1)
+    # a group without a row or with a prefix out of range: all its requests
+    for change in (put("slot", 2, rows), put("prefix_len", 1, -1), put("prefix_len", 1, c["table"].shape[1] * 16 + 1)):
+        d = {**{k: v.clone() for k, v in c.items()}, **change}
+        o = torch.full_like(q, 7.0)
+        call(kda, q, d, new, o=o)
+        status, detail = kda.kda_get_device_status()
+        assert status == 6 and detail in (2, 3)
+        assert torch.equal(o[:3], good[:3]) and bool((o[3:] == 7.0).all())
+
+
+def test_requests_outside_any_group_and_groups_that_overlap(kda):
+    new = [1] * 4
+    for dtype in (BF16, FP32):
+        c = build_branches([100, 40], [[20, 30], [9, 5]], 16, 1, dtype, seed=37)
+        q = queries(4, 4, dtype, 37)
+        good = call(kda, q, c, new)
+        i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+        for cu, done in [(i32(0, 2, 3), (0, 1, 2)), (i32(1, 2, 4), (2, 3)), (i32(0, 2, 9), (0, 1)), (i32(-3, 2, 4), (2, 3))]:
+            o = torch.full_like(q, 7.0)
+            call(kda, q, {**c, "cu_groups": cu}, new, o=o)
+            assert kda.kda_get_device_status()[0] == 6
+            for b in range(4):
+                if b in done:
+                    assert torch.equal(o[b], good[b])
+        # the same requests in five hundred groups: more work than the workspace holds is not begun
+        c = build_branches([40], [[3] * 100], 16, 1, dtype, seed=38)
+        q = queries(100, 16, dtype, 38)
+        o = torch.full_like(q, 7.0)
+        call(kda, q, {**c, "cu_groups": i32(*[100 * (g % 2) for g in range(1001)]), "prefix_len": i32(*[40] * 1000)},
+             [1] * 100, o=o)
+        assert kda.kda_get_device_status()[0] == 6
+        assert bool((o == 7.0).all())
+
+
+def test_no_tokens(kda):
+    c = build_branches([40], [[3, 4]], 16, 1, BF16, seed=41)
+    q = queries(0, 4, BF16, 41)
+    assert call(kda, q, c, [0, 0]).shape == (0, 4, 128)
+    assert kda.kda_get_device_status()[0] == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_loose_max_tokens(kda, dtype):
+    new = [1, 3, 2]
+    c = build_branches([200], [[9, 30, 100]], 32, 2, dtype, seed=43)
+    q = queries(sum(new), 8, dtype, 43)
+    for most in (3, 17, 100000):
+        check(call(kda, q, c, new, max_tokens=most), q, c, new)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("shape", [([3000, 500], [[40] * 9, [7] * 2], [1] * 11, 2, 8, 64),
+                                   ([9000], [[3, 700]], [2, 1], 1, 4, 32)])
+def test_replayed_from_a_graph_and_repeated_bit_for_bit(kda, shape, dtype):
+    """One capture over buffers whose contents, lengths and prefixes change between replays."""
+    prefix, mine, new, heads, group, page = shape
+    c = build_branches(prefix, mine, page, heads, dtype, seed=47)
+    q, cu = queries(sum(new), heads * group, dtype, 47), cu_of(new)
+    ask = lambda q, c: kda.kda_prefix_attention(q, c["pool"], c["table"], c["slot"], cu, c["kv_len"], c["cu_groups"],
+                                                c["prefix_len"], max_tokens=max(new))
+    want = ask(q, c)
+    busy = torch.randn((2048, 2048), device="cuda")
+    for i in range(10):
+        if i % 2:
+            torch.mm(busy, busy)  # the GPU in another state
+        assert torch.equal(ask(q, c), want)
+    buffers = {k: v.clone() for k, v in c.items()}
+    x = q.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = ask(x, buffers)
+    for shorter in (0, 37):  # the same rows with another cut between shared and own keys
+        other = {**c, "prefix_len": (c["prefix_len"] - shorter).contiguous()}
+        x.copy_(queries(sum(new), heads * group, dtype, 48 + shorter))
+        buffers["prefix_len"].copy_(other["prefix_len"])
+        graph.replay()
+        assert torch.equal(o, ask(x, other))
+        check(o, x, other, new)
+    assert kda.kda_get_device_status()[0] == 0
+
+
+def test_on_a_side_stream(kda):
+    """What the call allocates belongs to its stream, while the current stream allocates blocks of that size."""
+    new = [1, 2]
+    c = build_branches([500], [[9, 30]], 32, 2, BF16, seed=53)
+    q = queries(3, 16, BF16, 53)
+    want, cu = call(kda, q, c, new), cu_of(new)
+    side, busy = torch.cuda.Stream(), torch.randn((4096, 4096), device="cuda")
+    need = kda.kda_prefix_attention_workspace_size(BF16, 2, 3, 1, 16, 2)
+    for _ in range(10):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.mm(busy, busy)
+        o = kda.kda_prefix_attention(q, c["pool"], c["table"], c["slot"], cu, c["kv_len"], c["cu_groups"],
+                                     c["prefix_len"], max_tokens=2, stream=side)
+        blocks = [torch.full((need,), 1, dtype=torch.uint8, device="cuda") for _ in range(3)]
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(o, want)
+        del blocks
