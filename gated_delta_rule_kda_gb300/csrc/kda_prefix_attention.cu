@@ -18,7 +18,7 @@ using rows::kSmem;
 using rows::kThreads;
 using rows::kTile;
 
-constexpr int kCtas = 2 * 152;  // two an SM
+constexpr int kCtas = kPrefixCtas;  // two an SM
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) prefix_rows_kernel(const PrefixAttentionArgs a, const PrefixCut cut) {
@@ -50,8 +50,8 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_rows_kernel(const PrefixAt
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = 4 * ty + i;
-            *reinterpret_cast<float4 *>(slot + 4 * (tx * kRows + row)) = make_float4(st.o[i][0], st.o[i][1], st.o[i][2], st.o[i][3]);
-            *reinterpret_cast<float4 *>(slot + 4 * ((16 + tx) * kRows + row)) = make_float4(st.o[i][4], st.o[i][5], st.o[i][6], st.o[i][7]);
+            *reinterpret_cast<float4 *>(slot + kD * row + 4 * tx) = make_float4(st.o[i][0], st.o[i][1], st.o[i][2], st.o[i][3]);
+            *reinterpret_cast<float4 *>(slot + kD * row + 64 + 4 * tx) = make_float4(st.o[i][4], st.o[i][5], st.o[i][6], st.o[i][7]);
             if (tx == 0) *reinterpret_cast<float2 *>(slot + kD * kRows + 2 * row) = make_float2(st.m[i], st.l[i]);
         }
     }
@@ -109,8 +109,8 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_own_rows_kernel(const Pref
                 const float top = fmaxf(m, ml.x);
                 const float w = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : expf(m - top);  // (a NaN sum stays one)
                 const float v = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : expf(ml.x - top);
-                const float4 px = *reinterpret_cast<const float4 *>(slot + 4 * (tx * kRows + at));
-                const float4 py = *reinterpret_cast<const float4 *>(slot + 4 * ((16 + tx) * kRows + at));
+                const float4 px = *reinterpret_cast<const float4 *>(slot + kD * at + 4 * tx);
+                const float4 py = *reinterpret_cast<const float4 *>(slot + kD * at + 64 + 4 * tx);
                 x = make_float4(w * x.x + v * px.x, w * x.y + v * px.y, w * x.z + v * px.z, w * x.w + v * px.w);
                 y = make_float4(w * y.x + v * py.x, w * y.y + v * py.y, w * y.z + v * py.z, w * y.w + v * py.w);
                 l = w * l + v * ml.y;
@@ -149,15 +149,20 @@ cudaError_t launch_prefix_rows(const PrefixAttentionArgs &a, cudaStream_t stream
     return a.dtype == KDA_BF16 ? launch<__nv_bfloat16>(a, stream) : launch<float>(a, stream);
 }
 
-size_t prefix_attention_workspace(kda_dtype, int32_t, int32_t total_tokens, int32_t num_groups, int32_t num_q_heads,
+// (bf16: of either pair of launches, as the scale decides)
+size_t prefix_attention_workspace(kda_dtype dtype, int32_t, int32_t total_tokens, int32_t num_groups, int32_t num_q_heads,
                                   int32_t num_kv_heads) {
-    const PrefixCut cut = prefix_cut_rows(total_tokens, num_groups, num_q_heads, num_kv_heads);
-    return prefix_slots_at(num_groups) + (size_t)cut.slots * prefix_slot_floats(kRows) * sizeof(float);
+    const size_t rows = (size_t)prefix_cut_rows(total_tokens, num_groups, num_q_heads, num_kv_heads).slots * kRows;
+    const size_t tc = (size_t)prefix_cut_tc(total_tokens, num_groups, num_q_heads, num_kv_heads).slots * kPrefixTcRows;
+    return prefix_slots_at(num_groups) + (size_t)prefix_slot_floats(1) * sizeof(float) * (dtype == KDA_BF16 && tc > rows ? tc : rows);
 }
 
 cudaError_t launch_prefix_attention(const PrefixAttentionArgs &a, cudaStream_t stream) {
     if (a.cache.total_tokens == 0) return cudaSuccess;
-    return launch_prefix_rows(a, stream);
+    // The tensor-core kernels keep their running maximum on unscaled scores, in the order that a
+    // positive scale leaves alone; any other scale (and fp32) runs on the FMA units.
+    const bool tensor = a.dtype == KDA_BF16 && a.scale > 0.f && a.scale <= FLT_MAX;
+    return tensor ? launch_prefix_tc(a, stream) : launch_prefix_rows(a, stream);
 }
 
 }  // namespace kda

@@ -60,17 +60,21 @@ __device__ __forceinline__ PrefixGroup prefix_group(const PrefixAttentionArgs &a
     return x;
 }
 
-// The workspace: plan, a base a group, then the slots.
+// The workspace: plan, a word a CTA of the first launch (1: it has done its run), a base a group, then the slots.
+constexpr int32_t kPrefixCtas = 2 * 152;  // most of them
 __host__ __device__ inline size_t prefix_slots_at(int32_t num_groups) {
-    return (sizeof(PrefixPlan) + (size_t)num_groups * sizeof(PrefixBase) + 255) / 256 * 256;
+    return (sizeof(PrefixPlan) + kPrefixCtas * sizeof(uint32_t) + (size_t)num_groups * sizeof(PrefixBase) + 255) / 256 * 256;
 }
 __device__ __forceinline__ const PrefixPlan *prefix_plan(const PrefixAttentionArgs &a) {
     return static_cast<const PrefixPlan *>(a.workspace);
 }
-__device__ __forceinline__ const PrefixBase *prefix_bases(const PrefixAttentionArgs &a) {
-    return reinterpret_cast<const PrefixBase *>(prefix_plan(a) + 1);
+__device__ __forceinline__ uint32_t *prefix_done(const PrefixAttentionArgs &a) {
+    return reinterpret_cast<uint32_t *>(static_cast<PrefixPlan *>(a.workspace) + 1);
 }
-// A slot of `rows` rows: o as [128 / 4][rows][4], then (m, l) as [rows][2].
+__device__ __forceinline__ const PrefixBase *prefix_bases(const PrefixAttentionArgs &a) {
+    return reinterpret_cast<const PrefixBase *>(prefix_done(a) + kPrefixCtas);
+}
+// A slot of `rows` rows: o as [rows][128], then (m, l) as [rows][2].
 __host__ __device__ constexpr int64_t prefix_slot_floats(int32_t rows) { return (int64_t)rows * (kD + 2); }
 __device__ __forceinline__ float *prefix_slot(const PrefixAttentionArgs &a, int32_t rows, int64_t slot) {
     return reinterpret_cast<float *>(static_cast<unsigned char *>(a.workspace) + prefix_slots_at(a.num_groups)) +
@@ -205,14 +209,16 @@ struct PrefixWalk {
 struct PrefixSlots {
     int64_t first;           // the first slot
     int32_t count, step;     // of them, and from one to the next
+    int32_t cta;             // of the first; each slot's CTA is `step` after the one before
 };
 __device__ __forceinline__ PrefixSlots prefix_slots(const PrefixPlan &plan, const PrefixBase &base, const PrefixGroup &x,
                                                     int32_t h, int32_t index) {
-    if (x.items == 0) return PrefixSlots{0, 0, 0};
+    if (x.items == 0) return PrefixSlots{0, 0, 0, 0};
     const int32_t wide = (x.items + plan.width - 1) / plan.width, item = h * wide + index / plan.width;
     const int64_t u = base.units + (int64_t)item * x.tiles;
     const int32_t t0 = prefix_team(plan.units, u, plan.teams), t1 = prefix_team(plan.units, u + x.tiles - 1, plan.teams);
-    return PrefixSlots{((int64_t)base.items + item + t0) * plan.width + index % plan.width, t1 - t0 + 1, plan.width};
+    return PrefixSlots{((int64_t)base.items + item + t0) * plan.width + index % plan.width, t1 - t0 + 1, plan.width,
+                       t0 * plan.width + index % plan.width};
 }
 
 // Request b of the second launch, checked against its group; n = 0 when it is refused (then *bad).
@@ -246,6 +252,10 @@ __device__ __forceinline__ PrefixRequest prefix_request(const PrefixAttentionArg
     return r;
 }
 
+constexpr int32_t kPrefixTcRows = 256;  // of a slot of the tensor-core kernel: two row tiles
+cudaError_t launch_prefix_tc(const PrefixAttentionArgs &a, cudaStream_t stream);
+PrefixCut prefix_cut_tc(int32_t total_tokens, int32_t num_groups, int32_t num_q_heads, int32_t num_kv_heads);
+cudaError_t launch_prefix_own(const PrefixAttentionArgs &a, const PrefixCut &cut, cudaStream_t stream);
 PrefixCut prefix_cut_rows(int32_t total_tokens, int32_t num_groups, int32_t num_q_heads, int32_t num_kv_heads);
 cudaError_t launch_prefix_rows(const PrefixAttentionArgs &a, cudaStream_t stream);
 

@@ -133,13 +133,15 @@ __device__ __forceinline__ uint32_t remote_u32(uint32_t addr) {
 }
 
 constexpr uint64_t kAttnWaitNs = 2000000000ull;  // longest wait
-__device__ __forceinline__ uint64_t attn_wait_ns(const WindowAttentionArgs &a) {
+template <typename Args>
+__device__ __forceinline__ uint64_t attn_wait_ns(const Args &a) {
 #ifdef KDA_DEBUG
     if (a.withhold) return 1000000ull;
 #endif
     return kAttnWaitNs;
 }
-__device__ __forceinline__ bool attn_withhold(const WindowAttentionArgs &a) {
+template <typename Args>
+__device__ __forceinline__ bool attn_withhold(const Args &a) {
 #ifdef KDA_DEBUG
     return a.withhold != 0;
 #else
@@ -150,15 +152,17 @@ __device__ __forceinline__ bool attn_withhold(const WindowAttentionArgs &a) {
 __device__ __forceinline__ bool attn_given_up(const uint32_t *abort) {
     return *reinterpret_cast<const volatile uint32_t *>(abort) != 0;
 }
-__device__ __forceinline__ void attn_give_up(uint32_t *abort, const WindowAttentionArgs &a, uint32_t what) {
+template <typename Args>
+__device__ __forceinline__ void attn_give_up(uint32_t *abort, const Args &a, uint32_t what) {
     atomicExch(abort, 1u);
     record_status(a.status, KDA_ERR_DEVICE_TIMEOUT, what);
 }
 // A whole warp waits for a phase, for attn_wait_ns() at most or until another has given up.  Every lane gets the
 // same answer: what follows are full-mask exchanges and warp-wide instructions, which lanes that went
 // different ways could never meet in again.
+template <typename Args>
 __device__ __forceinline__ bool attn_wait_warp(uint64_t *bar, uint32_t parity, uint32_t *abort,
-                                               const WindowAttentionArgs &a, uint32_t what) {
+                                               const Args &a, uint32_t what) {
     constexpr uint32_t kAll = 0xffffffffu;
     bool done = tc::mbar_try_wait(bar, parity);
     if (__all_sync(kAll, done)) return true;
@@ -265,9 +269,11 @@ constexpr int kSplitRows = 32;  // most rows of a request and kv head that the s
 cudaError_t launch_window_attention_split(const WindowAttentionArgs &a, cudaStream_t stream);
 
 // A tensor map over kv_pool as rows of 128 channels, 64 channels x box_rows a box, 128-byte swizzle.
-bool encode_kv_map(CUtensorMap *m, const WindowAttentionArgs &a, int32_t box_rows);
+bool encode_kv_map(CUtensorMap *m, const void *kv_pool, const CacheArgs &c, int32_t num_kv_heads, int32_t box_rows);
 // The same rows seen as [k, v][half][row][64 channels] from a key row on: a box is the two halves of
 // box_rows keys, then those of their values.
-bool encode_kv_box_map(CUtensorMap *m, const WindowAttentionArgs &a, int32_t box_rows);
+bool encode_kv_box_map(CUtensorMap *m, const void *kv_pool, const CacheArgs &c, int32_t num_kv_heads, int32_t box_rows);
+// q [T][Hq][128], boxes of tq tokens x G heads x 64 channels.
+bool encode_q_map(CUtensorMap *m, const void *q, int32_t total_tokens, int32_t num_q_heads, int32_t G, int32_t tq);
 
 }  // namespace kda

@@ -19,6 +19,7 @@
 // over 65,536 to 131,072 (64 and 8 heads) 237 us, 6.35 TB/s; one token of one request 9.5 us.  A copy for
 // each half of a box's channels and for k and v apart: 196 and 294 us (the producer's loop sets the pace);
 // whole pages on the edges: 184; L2 prefetches four tiles ahead: 224.
+#include "kda_attention_mma.cuh"
 #include "kda_window_attention.cuh"
 #include "tc_primitives.cuh"
 
@@ -56,39 +57,9 @@ __device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity,
     return attn_wait_warp(bar, parity, &sh.abort, p.a, what);
 }
 
-__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
 // Whether some row of a request (tokens p0 .. last) must not see some of the keys [j, j + n).
 __device__ __forceinline__ bool some_hidden(const WindowAttentionArgs &a, int32_t j, int32_t n, int32_t p0, int32_t last) {
     return j + (n - 1) > p0 || (last - j >= a.window && j + (n - 1) >= a.sinks);
-}
-
-__device__ __forceinline__ void tma_load_box(uint32_t dst, const void *tmap, int y, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%3, %2, %3, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(y), "r"(0), "r"(smem_u32(bar))
-        : "memory");
 }
 
 // Fetches tiles [from, to) of the request's key tiles: whole pages (up to a tile), except that of a
@@ -383,8 +354,8 @@ cudaError_t launch_window_attention_split(const WindowAttentionArgs &a, cudaStre
     p.kv_rows = (int32_t)(2ll * a.cache.num_pages * a.num_kv_heads * a.cache.page_size);
     p.c = (float)((double)a.scale * 1.4426950408889634);
     p.page_shift = a.cache.page_size == 16 ? 4 : a.cache.page_size == 32 ? 5 : a.cache.page_size == 64 ? 6 : 7;
-    if (!encode_kv_box_map(&p.tm_kv, a, a.cache.page_size < kTile ? a.cache.page_size : kTile) ||
-        !encode_kv_box_map(&p.tm_edge, a, 16))
+    if (!encode_kv_box_map(&p.tm_kv, a.kv_pool, a.cache, a.num_kv_heads, a.cache.page_size < kTile ? a.cache.page_size : kTile) ||
+        !encode_kv_box_map(&p.tm_edge, a.kv_pool, a.cache, a.num_kv_heads, 16))
         return cudaErrorNotSupported;
     // Split as far as the CTAs are all resident at once (two an SM) and keep two tiles each: a second,
     // part-filled wave costs more than the longer rows (four requests of up to 131072 keys, 8 kv

@@ -38,6 +38,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include "kda_attention_tc.cuh"
 #include "kda_window_attention.cuh"
 #include "tc_primitives.cuh"
 
@@ -45,20 +46,12 @@ namespace kda {
 namespace {
 
 using namespace tc;
+using namespace attn_tc;
 
-constexpr int kThreads = 384;
-constexpr int kTile = 128;                    // rows of a row tile, keys of a key tile
-constexpr uint32_t kTileBytes = kTile * kD * 2;
-constexpr int kStages = 5;
 constexpr int kItems = 4;                     // work items announced ahead
 constexpr int kPitchO = kD + 4;               // floats of a row's partial result: o, m, l
 constexpr int kTainted = 200;                 // marked items a CTA keeps; it takes no more work near the end
 constexpr int kItemReaders = 11;              // warps that read them: softmax, MMA, values
-constexpr int kWarpTma = 8, kWarpMma = 9, kWarpScrub = 11;
-// 384 threads start with 168 registers; the softmax warps take 208, the others keep 88:
-// 256 * 208 + 128 * 88 = 384 * 168
-constexpr int kRegsSoftmax = 208, kRegsOther = 88;
-
 enum Bar {
     B_QFULL, B_QEMPTY, B_KVFULL, B_RAW = B_KVFULL + kStages, B_KVEMPTY = B_RAW + kStages,
     B_CLEAN = B_KVEMPTY + kStages,
@@ -79,21 +72,6 @@ struct Params {
     int32_t page_shift;  // log2 page_size
     float c;            // scale log2 e, > 0
 };
-
-// (a.x + b.x, a.y + b.y)
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    return fma2(a, make_float2(1.f, 1.f), b);
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int x, int y, int z, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
-}
 
 // One work item, found by the TMA warp and left in shared memory for the others.
 struct Item {
@@ -148,20 +126,6 @@ __device__ __forceinline__ bool wait_one(Shared &sh, int bar, uint32_t parity, c
 __device__ __forceinline__ bool wait(Shared &sh, int bar, uint32_t parity, const Params &p) {
     return attn_wait_warp(sh.bar + bar, parity, &sh.abort, p.a, (uint32_t)(64 + bar));
 }
-
-// The ring of k, v stages: tile loads in order, stage n % kStages, phase n / kStages.  A load
-// completes B_KVFULL of its stage, or B_RAW when the tile is values to be gone through first
-// (B_CLEAN follows); those barriers' phases are counted by use, a bit a stage.
-struct Ring {
-    int stage = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next() {
-        if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
-        }
-    }
-};
 
 // The items in turn, for the warps that read them.
 struct Items {
@@ -363,23 +327,6 @@ __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
 // ---------------------------------------------------------------------------
 // MMA
 // ---------------------------------------------------------------------------
-// One 128-wide product is eight MMAs of 64 cycles each, all issued by one thread: their matrix
-// descriptors differ from the first one's by constants (16-byte units of the address field).
-__device__ __forceinline__ void mma_scores(uint32_t tmem, uint64_t q_desc, uint64_t k_desc, int r, int from, int to) {
-#pragma unroll
-    for (int s = from; s < to; ++s) {
-        const uint64_t step = ((s >> 2) * (kTileBytes / 2) + (s & 3) * 32) / 16;
-        mma_bf16(tmem + 128 * r, q_desc + step, k_desc + step, idesc_bf16_f32(kTile, kTile), s > 0);
-    }
-}
-// Keys 64 half .. 64 half + 63 of a tile.
-__device__ __forceinline__ void mma_values(uint32_t tmem, uint64_t v_desc, int r, int half, bool first) {
-#pragma unroll
-    for (int s = 4 * half; s < 4 * half + 4; ++s)
-        mma_bf16_tmem_a(tmem + 256 + 128 * r, tmem + 128 * r + 8 * s, v_desc + s * (2048 / 16),
-                        idesc_bf16_f32(kTile, kD) | kIdescBMN, s > 0 ? 1u : !first);
-}
-
 // Row tile r's products, by one thread.  The tensor core runs them as they are issued, so what a
 // thread does between two products (waits, bookkeeping) is hidden by the other row tile's thread.
 // The two take turns, a tile's p v and the next one's q k^T at a time: left to interleave, both
@@ -530,23 +477,11 @@ __device__ void scrub_warp(const Params &p, Shared &sh, unsigned char *sm) {
 // ---------------------------------------------------------------------------
 // Softmax and epilogue
 // ---------------------------------------------------------------------------
-constexpr uint32_t kMinusInf = 0xff800000u;
-
 // The lowest n bits (none for n < 0, all from 32 on).
 __device__ __forceinline__ uint32_t low_mask(int32_t n) {
     uint32_t m;
     asm("bmsk.clamp.b32 %0, 0, %1;" : "=r"(m) : "r"(max(n, 0)));
     return m;
-}
-
-__device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
-    float a = __uint_as_float(s[0]), b = __uint_as_float(s[1]);
-#pragma unroll
-    for (int k = 2; k < 30; k += 4) {
-        a = fmaxf(fmaxf(a, __uint_as_float(s[k])), __uint_as_float(s[k + 1]));
-        b = fmaxf(fmaxf(b, __uint_as_float(s[k + 2])), __uint_as_float(s[k + 3]));
-    }
-    return fmaxf(fmaxf(a, b), fmaxf(__uint_as_float(s[30]), __uint_as_float(s[31])));
 }
 
 // A split item's partial results of one row: o as it is, then m and l.
@@ -869,26 +804,35 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 }  // namespace
 
-bool encode_kv_map(CUtensorMap *m, const WindowAttentionArgs &a, int32_t box_rows) {
+bool encode_kv_map(CUtensorMap *m, const void *kv_pool, const CacheArgs &c, int32_t num_kv_heads, int32_t box_rows) {
     auto fn = tensor_map_encoder();
     if (fn == nullptr) return false;
-    const CacheArgs &c = a.cache;
-    const cuuint64_t dims[2] = {kD, 2ull * c.num_pages * a.num_kv_heads * c.page_size};
+    const cuuint64_t dims[2] = {kD, 2ull * c.num_pages * num_kv_heads * c.page_size};
     const cuuint64_t strides[1] = {kD * 2};
     const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(a.kv_pool), dims, strides, box, estr,
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(kv_pool), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode_kv_box_map(CUtensorMap *m, const WindowAttentionArgs &a, int32_t box_rows) {
+bool encode_kv_box_map(CUtensorMap *m, const void *kv_pool, const CacheArgs &c, int32_t num_kv_heads, int32_t box_rows) {
     auto fn = tensor_map_encoder();
     if (fn == nullptr) return false;
-    const CacheArgs &c = a.cache;
-    const cuuint64_t dims[4] = {64, 2ull * c.num_pages * a.num_kv_heads * c.page_size, 2, 2};
-    const cuuint64_t strides[3] = {kD * 2, 128, (cuuint64_t)a.num_kv_heads * c.page_size * kD * 2};
+    const cuuint64_t dims[4] = {64, 2ull * c.num_pages * num_kv_heads * c.page_size, 2, 2};
+    const cuuint64_t strides[3] = {kD * 2, 128, (cuuint64_t)num_kv_heads * c.page_size * kD * 2};
     const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 2, 2}, estr[4] = {1, 1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(a.kv_pool), dims, strides, box, estr,
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(kv_pool), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_q_map(CUtensorMap *m, const void *q, int32_t total_tokens, int32_t num_q_heads, int32_t G, int32_t tq) {
+    auto fn = tensor_map_encoder();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[3] = {kD, (cuuint64_t)num_q_heads, (cuuint64_t)total_tokens};
+    const cuuint64_t strides[2] = {kD * 2, (cuuint64_t)num_q_heads * kD * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tq}, estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -902,14 +846,8 @@ cudaError_t launch_window_attention_tc(const WindowAttentionArgs &a, cudaStream_
     p.kv_rows = (int32_t)(2ll * a.cache.num_pages * a.num_kv_heads * a.cache.page_size);
     p.page_shift = a.cache.page_size == 16 ? 4 : a.cache.page_size == 32 ? 5 : a.cache.page_size == 64 ? 6 : 7;
     p.c = (float)((double)a.scale * 1.4426950408889634);
-    auto fn = tensor_map_encoder();
-    if (fn == nullptr || !encode_kv_map(&p.tm_kv, a, a.cache.page_size)) return cudaErrorNotSupported;
-    const cuuint64_t dims[3] = {kD, (cuuint64_t)a.num_q_heads, (cuuint64_t)a.cache.total_tokens};
-    const cuuint64_t strides[2] = {kD * 2, (cuuint64_t)a.num_q_heads * kD * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)p.tq}, estr[3] = {1, 1, 1};
-    if (fn(&p.tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dims, strides, box, estr,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    if (!encode_kv_map(&p.tm_kv, a.kv_pool, a.cache, a.num_kv_heads, a.cache.page_size) ||
+        !encode_q_map(&p.tm_q, a.q, a.cache.total_tokens, a.num_q_heads, p.G, p.tq))
         return cudaErrorNotSupported;
     // sum of ceil(n_b / tokens) over the requests, at most
     const int64_t tokens = 2 * p.tq;
