@@ -21,7 +21,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kFound = 512;  // candidates that are ranked by counting
 constexpr int kHeld = 384;   // vectors with a candidate that a CTA holds
-constexpr int kCtasSm = 4;
+constexpr int kCtasSm = 6;
 constexpr int kMaxN = KDA_MAX_BEAMS;
 
 // A segment's result: max (fp32), sum (fp32), then N keys, best first; 0: no logit.
@@ -192,12 +192,11 @@ __global__ void __launch_bounds__(kThreads, kCtasSm) beam_segments_kernel(const 
         }
     };
 
-    uint4 raw[kVecs], ahead[kVecs];
-    fetch(raw, 0);
+    uint4 raw[kVecs];
     float m = -INFINITY, sum = 0.f;  // of this thread's logits: the maximum, and the sum of e^(x - m)
     float bound = -INFINITY;
     for (int32_t c = 0; c < chunks; ++c) {
-        if (c + 1 < chunks) fetch(ahead, c + 1);
+        fetch(raw, c);
         if (off != 0) align(raw, c);
         const float top = V::template max_of<kVecs>(raw);
         if (c == 0) {
@@ -258,8 +257,6 @@ __global__ void __launch_bounds__(kThreads, kCtasSm) beam_segments_kernel(const 
                 add += tc::ex2_approx((V::clean(V::at(s_chunk[e / kN][tid], e % kN)) - shift) * kLog2e);
         }
         sum += add;
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) raw[i] = ahead[i];
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // the warps' maxima and sums
@@ -345,22 +342,24 @@ __device__ __forceinline__ double unordered64(uint64_t o) {
     return __longlong_as_double((long long)(o ^ ((o >> 63) ? 1ull << 63 : ~0ull)));
 }
 
-// Whether continuation (total, beam, key) x comes before y.
+// A continuation; total 0: there is none.
 struct Choice {
     uint64_t total, key;
     int32_t beam;
 };
+// Whether x comes before y.
 __device__ __forceinline__ bool before(const Choice &x, const Choice &y) {
     return x.total > y.total || (x.total == y.total && (x.beam < y.beam || (x.beam == y.beam && x.key > y.key)));
 }
 
 // A CTA a prompt.  Thread t owns the lists t, t + 256, ...: list i is segment i % S of beam i / S.
+// Bound by the chain of its steps (about 6 us: loads, exponentials and logarithms in 64 bits 3, the two rounds of
+// counting 2).
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelectArgs a, const Layout lay) {
     __shared__ double s_score[KDA_MAX_BEAMS], s_lse[KDA_MAX_BEAMS];
-    __shared__ uint64_t s_group[64];
+    __shared__ uint64_t s_group[64], s_total[kThreads], s_key[kThreads];
     __shared__ Choice s_found[kFound], s_best[2][kThreads / 32];
-    __shared__ uint64_t s_head[kThreads];
-    __shared__ int s_count, s_wins, s_win[kFound];
+    __shared__ int s_count;
     __shared__ uint32_t s_over[2];
     __shared__ float s_max[KDA_MAX_BEAMS];
     extern __shared__ uint8_t s_next[];  // of each list: its next key (one by one)
@@ -375,8 +374,11 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelectArg
         const uint32_t end = __ballot_sync(0xffffffffu, tid < K && a.ended != nullptr && a.ended[b * K + tid] != 0);
         if (lane == 0) s_over[warp] = end;
     }
-    if (tid == 0) s_count = s_wins = 0;
+    if (tid == 0) s_count = 0;
     grid_wait();
+    // A thread takes one of the first `depth` continuations of a list (lists <= 256): number n0 of list i0.
+    const int32_t depth = min(N, kThreads / lists), n0 = depth > 0 ? tid % depth : 0, i0 = depth > 0 ? tid / depth : lists;
+    const uint64_t key0 = i0 < lists ? list(i0)[1 + n0] : 0;
     __syncthreads();
     const uint64_t over = (uint64_t)s_over[1] << 32 | s_over[0];  // bit k: beam k has ended
     // Log-sum-exp in 64 bits, whose units are few: `width` lanes a beam, so that no lane is idle in short rows; the
@@ -385,17 +387,18 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelectArg
     for (int32_t k0 = 0; k0 < K; k0 += kThreads / width) {  // (whole warps go round)
         const int32_t k = k0 + tid / width, l = tid % width;
         const bool live = k < K && !(over >> k & 1);
-        float m = -INFINITY;
+        const uint64_t first = live && l < S ? list(k * S + l)[0] : 0xff800000u;  // (sum, maximum); none: 0, -inf
+        float m = __uint_as_float((uint32_t)first);
         if (live)
-            for (int32_t i = l; i < S; i += width) m = fmaxf(m, __uint_as_float((uint32_t)list(k * S + i)[0]));
+            for (int32_t i = l + width; i < S; i += width) m = fmaxf(m, __uint_as_float((uint32_t)list(k * S + i)[0]));
         for (int o = width >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        double sum = 0;
+        const auto part = [&](uint64_t w) {  // (of a segment without logits: nothing)
+            const float mi = __uint_as_float((uint32_t)w), x = __uint_as_float((uint32_t)(w >> 32));
+            return mi == m ? (double)x : mi > -INFINITY ? (double)x * exp((double)mi - (double)m) : 0.;
+        };
+        double sum = part(first);
         if (live)
-            for (int32_t i = l; i < S; i += width) {
-                const uint64_t w = list(k * S + i)[0];
-                const float mi = __uint_as_float((uint32_t)w);
-                if (mi > -INFINITY) sum += (double)__uint_as_float((uint32_t)(w >> 32)) * (mi == m ? 1. : exp((double)mi - (double)m));
-            }
+            for (int32_t i = l + width; i < S; i += width) sum += part(list(k * S + i)[0]);
         for (int o = width >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (live && l == 0) {
             s_max[k] = m;
@@ -405,19 +408,20 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelectArg
     __syncthreads();
     if (tid < K && !(over >> tid & 1)) s_lse[tid] = (double)s_max[tid] + log(s_lse[tid]);  // (without logits there are no keys)
     __syncthreads();
-    // Continuation n of list i; total 0: there is none.
-    const auto choice = [&](int32_t i, int32_t n) {
+    // Continuation n of list i, whose key is given.
+    const auto choice_of = [&](int32_t i, int32_t n, uint64_t key) {
         Choice c{0, 0, i / S};
         if (over >> c.beam & 1) {
             if (i % S != 0 || n > 0) return c;
             c.key = make_key(0.f, (uint32_t)a.end_token);
             c.total = ordered64(s_score[c.beam]);
-        } else if (n < N) {
-            c.key = list(i)[1 + n];
-            if (c.key != 0) c.total = ordered64(s_score[c.beam] + ((double)unordered((uint32_t)(c.key >> 32)) - s_lse[c.beam]));
+        } else if (key != 0) {
+            c.key = key;
+            c.total = ordered64(s_score[c.beam] + ((double)unordered((uint32_t)(key >> 32)) - s_lse[c.beam]));
         }
         return c;
     };
+    const auto choice = [&](int32_t i, int32_t n) { return choice_of(i, n, n < N ? list(i)[1 + n] : 0); };
     const auto give = [&](int32_t n, const Choice &c) {
         const int64_t at = (int64_t)b * N + n;
         const int32_t token = (int32_t)~(uint32_t)c.key;
@@ -426,16 +430,33 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelectArg
         a.score[at] = c.total == 0 ? -INFINITY : (float)unordered64(c.total);
         if (a.ended_out != nullptr) a.ended_out[at] = c.total != 0 && ((over >> c.beam & 1) || token == a.end_token);
     };
-    // A bound that N heads reach: with a list a thread the N-th best head, found by counting; with more, as in a
-    // segment, the smallest of the best heads of N or more groups of lists.
-    const Choice first = tid < lists ? choice(tid, 0) : Choice{0, 0, 0};
+    // A bound that N continuations reach: the N-th best of the threads' continuations, by counting (which are all there
+    // are where depth = N); with more lists than threads, the smallest of the best heads of N or more groups of lists.
+    // Then what reaches it, in every list whose head does.
     uint64_t bound = 1;
-    if (lists <= kThreads) {
-        s_head[tid] = first.total;
+    if (depth > 0) {
+        Choice c{0, 0, 0};
+        if (i0 < lists) c = choice_of(i0, n0, key0);
+        s_total[tid] = c.total;
+        s_key[tid] = c.key;
         __syncthreads();
+        // Those of one beam lie together: within it the key decides, between beams the total and then the beam.
+        const int taken = lists * depth, begin = min(taken, i0 / S * S * depth), end = min(taken, begin + S * depth);
         int rank = 0;
-        for (int32_t i = 0; i < lists; ++i) rank += s_head[i] > first.total || (s_head[i] == first.total && i < tid);
-        if (rank == N - 1 && tid < lists) s_group[0] = first.total;  // (0 where fewer lists hold anything)
+#pragma unroll 8
+        for (int j = 0; j < begin; ++j) rank += s_total[j] >= c.total;
+#pragma unroll 8
+        for (int j = begin; j < end; ++j) rank += s_key[j] > c.key;
+#pragma unroll 8
+        for (int j = end; j < taken; ++j) rank += s_total[j] > c.total;
+        if (depth == N) {
+            // (totals of 0 are none: they are left out, and what nothing is left for is filled in)
+            const int there = __syncthreads_count(c.total != 0);
+            if (c.total != 0 && rank < N) give(rank, c);
+            for (int n = there + tid; n < N; n += kThreads) give(n, Choice{0, 0, 0});
+            return;
+        }
+        if (c.total != 0 && rank == N - 1) s_group[0] = c.total;
         __syncthreads();
         bound = max(bound, s_group[0]);
     } else {
@@ -449,23 +470,14 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelectArg
         for (int32_t i = 0; i < groups; ++i) least = min(least, s_group[i]);
         bound = max(bound, least);
     }
-    // the lists whose heads reach it, and then what follows in each
-    for (int32_t i = tid; i < lists; i += kThreads) {
-        if ((i == tid ? first : choice(i, 0)).total < bound) continue;
-        const int at = atomicAdd(&s_wins, 1);
-        if (at < kFound) s_win[at] = i;
-    }
-    __syncthreads();
-    const int wins = s_wins;
-    if (wins <= kFound) {
-        for (int32_t i = tid; i < wins * N; i += kThreads) {
-            const Choice c = choice(s_win[i / N], i % N);
-            if (c.total < bound) continue;
-            const int at = atomicAdd(&s_count, 1);
-            if (at < kFound) s_found[at] = c;
-        }
-    } else if (tid == 0) {
-        s_count = wins;
+    for (int32_t at = tid; at < lists * N; at += kThreads) {
+        const int32_t i = at / N, n = at - i * N;
+        if ((depth > 0 ? s_total[i * depth] : choice(i, 0).total) < bound) continue;  // (a list falls)
+        const Choice c = choice(i, n);
+        if (c.total < bound) continue;
+        const int to = atomicAdd(&s_count, 1);
+        if (to >= kFound) continue;
+        s_found[to] = c;
     }
     __syncthreads();
     const int found = s_count;
@@ -477,7 +489,12 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelectArg
             }
             const Choice c = s_found[i];
             int rank = 0;
-            for (int j = 0; j < found; ++j) rank += before(s_found[j], c);
+#pragma unroll 4
+            for (int j = 0; j < found; ++j) {
+                const Choice x = s_found[j];
+                const bool same = x.beam == c.beam;
+                rank += same ? x.key > c.key : x.total > c.total || (x.total == c.total && x.beam < c.beam);
+            }
             if (rank < N) give(rank, c);
         }
         return;
@@ -519,7 +536,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelectArg
 
 constexpr int kVecs = 4;        // 16-byte vectors of a chunk, a thread
 constexpr int kMostChunks = 4;  // of a segment
-constexpr int kWaves = 8;       // CTAs an SM that short segments are for
+constexpr int kWaves = 5;       // CTAs an SM that short segments are for
 constexpr size_t kMostLists = KDA_MAX_BEAMS * ((1 << 21) / (kThreads * kVecs * 4));  // of a prompt
 
 Layout layout(kda_dtype dtype, int32_t vocab, int64_t rows) {
