@@ -1,11 +1,9 @@
-// Attention over a shared prefix, bf16: the second launch of kda_prefix_attention.  Each request and kv head
-// goes over its own keys, joins them with the parts that the first launch left of the prefix, and writes o:
-//   M = max m_i;  o = (sum_i 2^(c (m_i - M)) o_i) / (sum_i 2^(c (m_i - M)) l_i)
+// Attention over a shared prefix, bf16: each request's own keys, the second launch of kda_prefix_attention.
 //
-// Bound by reading the own keys and values once (and the parts of the prefix, from L2), so the work is cut
-// along the keys as in the windowed attention's kernel for few rows: a cluster of up to 16 CTAs takes
-// consecutive runs of 64-key tiles and joins through distributed shared memory, in an order that the sizes
-// alone decide.
+// Bound by reading the own keys and values once, so the work is cut along the keys as in the windowed
+// attention's kernel for few rows: a cluster of up to 16 CTAs takes consecutive runs of 64-key tiles and
+// joins them through distributed shared memory, in an order that the sizes alone decide; o (not divided), m
+// and l of each row go to the workspace.
 //
 // A row is a (token, query head of the group) pair; a CTA has up to 32 of them, in one or two blocks of 16,
 // and goes on to further ones where a request has more.  A producer warp fetches k and v by TMA, page by
@@ -14,7 +12,8 @@
 // running maximum moves lazily.  Scores, m, l and o are fp32; p is rounded to bf16 for its product (at most
 // 2^-8 of each weight).
 //
-// All this runs while the first launch finishes; only the join waits for it.
+// It comes up as soon as the prefixes' launch has, on the SMs that that leaves free, and waits for it only to
+// end after it.
 #include "kda_attention_mma.cuh"
 #include "kda_prefix_attention.cuh"
 
@@ -31,7 +30,6 @@ constexpr int kStages = 3;
 constexpr int kMaxSplits = 16;
 constexpr int kPitch = kD + 4;                // partial outputs: fragment stores hit distinct banks
 constexpr size_t kSmem = kStages * kStageBytes + 1024;  // the start is rounded up to 1024 bytes
-constexpr int kParts = (kPrefixCtas + 31) / 32;  // of a prefix, a lane
 
 struct Params {
     // The pool as [k, v][half of the channels][row][64 channels], boxes of both halves of both:
@@ -39,7 +37,7 @@ struct Params {
     CUtensorMap tm_edge;  // of 16 rows
     PrefixAttentionArgs a;
     PrefixCut cut;
-    int32_t G, tq, kv_rows, page_shift, chunks;
+    int32_t G, kv_rows, page_shift, chunks;
     float c;  // scale log2 e, > 0
 };
 
@@ -153,18 +151,15 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_own_kernel(const __grid_co
         sh.abort = sh.tainted = 0;
         fence_mbar_init();
     }
-    bool bad;
-    const PrefixRequest r = prefix_request(a, p.cut, b, &bad);
-    if (bad && rank == 0 && h == 0 && chunk0 == 0 && threadIdx.x == 0)
-        record_status(a.status, KDA_ERR_DEVICE_CHECK, (uint32_t)b);
-    const AttnRequest &req = r.req;
+    const PrefixRequest req = prefix_request(a, p.cut, prefix_group(a, p.cut, prefix_group_of(a, b)), b);
+    const PrefixPart part_of = prefix_part(prefix_space(a), 1);
     const int32_t num_rows = req.n * G, q0 = req.len - req.n;  // q0: index of the first token
     __syncthreads();
 
     uint32_t n0 = 0;  // tiles that went through the ring
     for (int32_t row_base = chunk0 * kRows; row_base < num_rows; row_base += p.chunks * kRows) {  // the same for the whole cluster
         const int32_t rows = min(kRows, num_rows - row_base);
-        const Own own{r.x.len, q0 + row_base / G, q0 + (row_base + rows - 1) / G};
+        const Own own{req.from, q0 + row_base / G, q0 + (row_base + rows - 1) / G};
         const int32_t tile0 = own.from / kTile, tiles = own.last / kTile + 1 - tile0;
         const int32_t from = tile0 + (int32_t)((int64_t)tiles * rank / splits);
         const int32_t to = tile0 + (int32_t)((int64_t)tiles * (rank + 1) / splits);
@@ -322,95 +317,52 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_own_kernel(const __grid_co
         cluster_sync();
 
         // Join: the rows go round the cluster's consumer warps, four channels a lane.
-        grid_wait();  // the prefix's parts are there
         bool failed = false, tainted = false;
         for (int32_t k = 0; k < splits; ++k) {
             failed |= remote_u32(remote(smem_u32(&sh.abort), k)) != 0;
             tainted |= remote_u32(remote(smem_u32(&sh.tainted), k)) != 0;
         }
-        const PrefixPlan plan = *prefix_plan(a);
-        if (plan.units < 0) {  // groups that overlap: nothing was computed
-            if (threadIdx.x == 0) record_status(a.status, KDA_ERR_DEVICE_CHECK, (uint32_t)b);
-            failed = true;
-        }
-        if (warp < kWarps && !failed) {
-            const PrefixBase base = prefix_bases(a)[r.g];
+        if (warp < kWarps) {
             for (int32_t row = rank * kWarps + warp; row < rows; row += splits * kWarps) {
                 const int32_t block = row >> 4, rr = row & 15, token = (row_base + row) / G, head = (row_base + row) - token * G;
                 const int64_t q_row = (int64_t)(req.first + token) * a.num_q_heads + h * G + head;
-                // its place among the group's rows
-                const int32_t t = req.first - r.x.first + token, tile = t / p.tq;
-                const PrefixSlots slots = prefix_slots(plan, base, r.x, h, tile >> 1);
-                const int32_t at = (tile & 1) * (kPrefixTcRows / 2) + (t - tile * p.tq) * G + head;
-                const int32_t sources = tainted ? 0 : splits * kGroups;  // at most 64: two a lane
-                float2 ml[2], pml[kParts];
-                bool lost = false;
+                const int32_t sources = splits * kGroups;  // at most 64: two a lane
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                float top = -INFINITY, sum = -1.f;  // a row that is lost is marked
+                if (!failed && tainted) {
+                    const float2 x = own_row(p, q_row, h, req.row, own, q0 + token, acc);
+                    top = x.x;
+                    sum = x.y;
+                } else if (!failed) {
+                    float2 ml[2];
 #pragma unroll
-                for (int u = 0; u < kParts; ++u) {
-                    const int32_t k = lane + 32 * u;
-                    pml[u] = make_float2(-INFINITY, 0.f);
-                    if (32 * u < slots.count && k < slots.count) {
-                        lost |= prefix_done(a)[slots.cta + k * slots.step] != 1;
-                        pml[u] = *reinterpret_cast<const float2 *>(prefix_slot(a, kPrefixTcRows, slots.first + (int64_t)k * slots.step) + kPrefixTcRows * kD + 2 * at);
+                    for (int u = 0; u < 2; ++u) {
+                        const int32_t i = lane + 32 * u;
+                        ml[u] = make_float2(-INFINITY, 0.f);
+                        if (i < sources) ml[u] = remote_float2(remote(smem_u32(&sh.ml[(i % kGroups) * kBlocks + block][rr]), i / kGroups));
+                    }
+                    top = fmaxf(ml[0].x, ml[1].x);
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
+                    float w[2];
+                    sum = 0.f;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {  // (a NaN sum stays one)
+                        w[u] = ml[u].x == -INFINITY ? (ml[u].y == 0.f ? 0.f : 1.f) : ex2_approx((ml[u].x - top) * p.c);
+                        sum = fmaf(w[u], ml[u].y, sum);
+                    }
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
+                    const uint32_t mine = smem_u32(sm) + (block * 16 + rr) * kPitch * 4 + 16 * lane;
+#pragma unroll 8
+                    for (int32_t i = 0; i < sources; ++i) {
+                        const float wi = __shfl_sync(kAll, i < 32 ? w[0] : w[1], i & 31);
+                        const float4 x = remote_float4(remote(mine + (i % kGroups) * kBlocks * 16 * kPitch * 4, i / kGroups));
+                        acc = make_float4(fmaf(wi, x.x, acc.x), fmaf(wi, x.y, acc.y), fmaf(wi, x.z, acc.z), fmaf(wi, x.w, acc.w));
                     }
                 }
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int32_t i = lane + 32 * u;
-                    ml[u] = make_float2(-INFINITY, 0.f);
-                    if (i < sources) ml[u] = remote_float2(remote(smem_u32(&sh.ml[(i % kGroups) * kBlocks + block][rr]), i / kGroups));
-                }
-                if (__any_sync(kAll, lost)) continue;  // the first launch gave up (and said so)
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (tainted) {
-                    const float2 x = own_row(p, q_row, h, req.row, own, q0 + token, acc);
-                    if (lane == 0) ml[0] = x;
-                }
-                float top = fmaxf(ml[0].x, ml[1].x);
-#pragma unroll
-                for (int u = 0; u < kParts; ++u) top = fmaxf(top, pml[u].x);
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
-                const auto weight = [&](float2 x) {  // (a NaN sum stays one)
-                    return x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2_approx((x.x - top) * p.c);
-                };
-                float w[2], pw[kParts], sum = 0.f;
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    w[u] = weight(ml[u]);
-                    sum = fmaf(w[u], ml[u].y, sum);
-                }
-#pragma unroll
-                for (int u = 0; u < kParts; ++u) {
-                    pw[u] = weight(pml[u]);
-                    sum = fmaf(pw[u], pml[u].y, sum);
-                }
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
-                const auto add = [&](float wi, float4 x) {
-                    acc = make_float4(fmaf(wi, x.x, acc.x), fmaf(wi, x.y, acc.y), fmaf(wi, x.z, acc.z), fmaf(wi, x.w, acc.w));
-                };
-                if (tainted) {
-                    const float wi = __shfl_sync(kAll, w[0], 0);
-                    acc = make_float4(wi * acc.x, wi * acc.y, wi * acc.z, wi * acc.w);
-                }
-                const uint32_t mine = smem_u32(sm) + (block * 16 + rr) * kPitch * 4 + 16 * lane;
-#pragma unroll 8
-                for (int32_t i = 0; i < sources; ++i)
-                    add(__shfl_sync(kAll, i < 32 ? w[0] : w[1], i & 31),
-                        remote_float4(remote(mine + (i % kGroups) * kBlocks * 16 * kPitch * 4, i / kGroups)));
-                const float *slot = prefix_slot(a, kPrefixTcRows, slots.first) + at * kD + 4 * lane;
-                const int64_t step = slots.step * prefix_slot_floats(kPrefixTcRows);
-#pragma unroll
-                for (int u = 0; u < kParts; ++u) {
-                    const int32_t here = min(slots.count - 32 * u, 32);
-#pragma unroll 4
-                    for (int32_t k = 0; k < here; ++k)
-                        add(__shfl_sync(kAll, pw[u], k), *reinterpret_cast<const float4 *>(slot + (32 * u + k) * step));
-                }
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                store4(static_cast<__nv_bfloat16 *>(a.o) + q_row * kD + 4 * lane,
-                       make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+                store4(part_of.o + q_row * kD + 4 * lane, acc);
+                if (lane == 0) part_of.ml[q_row] = make_float2(top, sum);
             }
         }
         __syncwarp();
@@ -419,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_own_kernel(const __grid_co
         if (threadIdx.x == 0) sh.tainted = 0;
         __syncthreads();
     }
-    grid_wait();  // this grid ends after the one before it, whatever it had to do
+    if (blockIdx.x == 0 && blockIdx.y == 0) grid_wait();  // the launch ends after the one before it
 }
 
 template <int kBlocks>
@@ -435,7 +387,6 @@ cudaError_t launch_prefix_own(const PrefixAttentionArgs &a, const PrefixCut &cut
     p.a = a;
     p.cut = cut;
     p.G = a.num_q_heads / a.num_kv_heads;
-    p.tq = kPrefixTcRows / 2 / p.G;
     p.kv_rows = (int32_t)(2ll * a.cache.num_pages * a.num_kv_heads * a.cache.page_size);
     p.c = (float)((double)a.scale * 1.4426950408889634);
     p.page_shift = a.cache.page_size == 16 ? 4 : a.cache.page_size == 32 ? 5 : a.cache.page_size == 64 ? 6 : 7;
