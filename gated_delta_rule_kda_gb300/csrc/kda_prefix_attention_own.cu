@@ -151,8 +151,11 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_own_kernel(const __grid_co
         sh.abort = sh.tainted = 0;
         fence_mbar_init();
     }
-    const PrefixRequest req = prefix_request(a, p.cut, prefix_group(a, p.cut, prefix_group_of(a, b)), b);
-    const PrefixPart part_of = prefix_part(prefix_space(a), 1);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join comes up when the last CTA has
+    const PrefixRequest req = prefix_request(a, p.cut, b);
+    if (!req.ok && rank == 0 && h == 0 && chunk0 == 0 && threadIdx.x == 0)
+        record_status(a.status, KDA_ERR_DEVICE_CHECK, (uint32_t)b);
+    const PrefixSpace space = prefix_space(a);
     const int32_t num_rows = req.n * G, q0 = req.len - req.n;  // q0: index of the first token
     __syncthreads();
 
@@ -322,18 +325,18 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_own_kernel(const __grid_co
             failed |= remote_u32(remote(smem_u32(&sh.abort), k)) != 0;
             tainted |= remote_u32(remote(smem_u32(&sh.tainted), k)) != 0;
         }
-        if (warp < kWarps) {
+        if (warp < kWarps && !failed) {  // (else the rows have no result)
             for (int32_t row = rank * kWarps + warp; row < rows; row += splits * kWarps) {
                 const int32_t block = row >> 4, rr = row & 15, token = (row_base + row) / G, head = (row_base + row) - token * G;
                 const int64_t q_row = (int64_t)(req.first + token) * a.num_q_heads + h * G + head;
                 const int32_t sources = splits * kGroups;  // at most 64: two a lane
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                float top = -INFINITY, sum = -1.f;  // a row that is lost is marked
-                if (!failed && tainted) {
+                float top, sum;
+                if (tainted) {
                     const float2 x = own_row(p, q_row, h, req.row, own, q0 + token, acc);
                     top = x.x;
                     sum = x.y;
-                } else if (!failed) {
+                } else {
                     float2 ml[2];
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
@@ -361,8 +364,8 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_own_kernel(const __grid_co
                         acc = make_float4(fmaf(wi, x.x, acc.x), fmaf(wi, x.y, acc.y), fmaf(wi, x.z, acc.z), fmaf(wi, x.w, acc.w));
                     }
                 }
-                store4(part_of.o + q_row * kD + 4 * lane, acc);
-                if (lane == 0) part_of.ml[q_row] = make_float2(top, sum);
+                store4(space.own_o + q_row * kD + 4 * lane, acc);
+                if (lane == 0) space.own[q_row] = make_float4(top, sum, req.from > 0, 0.f);
             }
         }
         __syncwarp();

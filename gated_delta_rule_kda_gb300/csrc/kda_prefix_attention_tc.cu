@@ -61,7 +61,7 @@ struct Params {
 
 // A stretch of an item, found by the TMA warp and left in shared memory for the others.
 struct Item {
-    int32_t goes_on;
+    int32_t goes_on, more;  // with an item that another CTA started; else: CTAs that go on with it
     int32_t first, tokens;  // its tokens: rows [first, first + tokens) of q
     int32_t h, row;         // kv head, row of the table
     int32_t len;            // of the prefix
@@ -81,7 +81,7 @@ struct Shared {
     float2 ml[kTile];         // one row tile: engine 1's m, l; then the weights of both engines
     uint32_t tmem, abort;
     PrefixRun run;
-    int64_t sums[kThreads / 32];
+    int64_t sums[2 * kThreads / 32];
 };
 
 // One thread waits for a phase, giving up after attn_wait_ns() or when another warp has given up.
@@ -218,6 +218,7 @@ __device__ void tma_warp(const Params &p, Shared &sh, unsigned char *sm) {
         if (more) {
             const int32_t t0 = s.index * p.cut.tile;
             it.goes_on = s.goes_on;
+            it.more = s.more;
             it.first = s.first + t0;
             it.tokens = min(p.cut.tile, s.tokens - t0);
             it.h = s.h;
@@ -519,7 +520,7 @@ __device__ void softmax_warps(const Params &p, Shared &sh, int r) {
         // The part's place, and each row's in it.
         const PrefixSpace space = prefix_space(p.a);
         const bool goes_on = it->goes_on;
-        const PrefixPart part = goes_on ? prefix_slot(space, p.cut, (int32_t)blockIdx.x) : prefix_part(space, 0);
+        float *slot = prefix_slot(space, p.cut, (int32_t)blockIdx.x), *part = goes_on ? slot : space.o;
         const auto row_at = [&](int rt) {  // row rt of the row tile
             const int k = (int)((uint32_t)rt * p.inv_g >> 16), t = (two ? r * p.tq : 0) + k;
             if (k >= p.tq || t >= it->tokens) return -1;
@@ -576,9 +577,15 @@ __device__ void softmax_warps(const Params &p, Shared &sh, int r) {
 #pragma unroll
                 for (int k = 0; k < 16; ++k) o[k] = fmaf(w.y, o1[k], w.x * o[k]);
             }
-            store16(o, part.o + 16 * c, to);
+            store16(o, part + 16 * c, to);
         }
-        if (mine >= 0 && (two || r == 0)) part.ml[mine] = make_float2(m, l);
+        if (mine >= 0 && (two || r == 0)) {
+            (goes_on ? prefix_slot_ml(slot, p.cut) : space.ml)[mine] = make_float2(m, l);
+            const int32_t head = row - tk * p.cut.G;  // where the token's parts lie is said once for its query heads
+            if (!goes_on && head == 0)
+                space.more[(int64_t)(it->first + token) * p.a.num_kv_heads + it->h] =
+                    make_int4((int32_t)blockIdx.x, it->more, sh.run.width, (two ? r * kTile : 0) + row);
+        }
         fence_before_sync();  // the next item's products write o after this engine's next p
         __syncwarp();
         if (!two) {  // nor before the other half of the warps has read it
@@ -612,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
     }
     fence_before_sync();
     grid_wait();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    prefix_begin(p.a, prefix_space(p.a));
     prefix_make_plan<kThreads>(p.a, p.cut, sh.run, sh.sums);  // (and __syncthreads)
     fence_after_sync();
     if (warp < 8) {
@@ -626,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
     }
     __syncthreads();
     if (warp == kWarpMma) tmem_dealloc(sh.tmem, 512);
-    if (threadIdx.x == 0) prefix_space(p.a).done[blockIdx.x] = sh.abort == 0;
+    if (threadIdx.x == 0) prefix_space(p.a).done[blockIdx.x] = !sh.run.bad && sh.abort == 0;
 }
 
 }  // namespace
@@ -653,14 +660,14 @@ static int32_t team_width(const PrefixAttentionArgs &a, int32_t tokens) {
 
 PrefixCut prefix_cut_tc(const PrefixAttentionArgs &a) {
     const int32_t G = a.num_q_heads / a.num_kv_heads, tq = kTile / G;
-    return PrefixCut{0, G, 2 * tq, tq, kTile, kCtas, 2 * kTile, a.num_groups > 0 ? team_width(a, 2 * tq) : 1, 1};
+    return PrefixCut{0, G, 2 * tq, kTile, kCtas, 2 * kTile, a.num_groups > 0 ? team_width(a, 2 * tq) : 1, 1.6f};
 }
 
 cudaError_t launch_prefix_tc(const PrefixAttentionArgs &a, const PrefixCut &cut, cudaStream_t stream) {
     Params p;
     p.a = a;
     p.cut = cut;
-    p.tq = cut.own_tile;
+    p.tq = cut.tile / 2;
     p.inv_g = (65536u + cut.G - 1) / cut.G;
     p.kv_rows = (int32_t)(2ll * a.cache.num_pages * a.num_kv_heads * a.cache.page_size);
     p.page_shift = a.cache.page_size == 16 ? 4 : a.cache.page_size == 32 ? 5 : a.cache.page_size == 64 ? 6 : 7;
