@@ -43,7 +43,7 @@ kda_status kda_prefix_attention(kda_dtype dtype, int32_t batch, int32_t total_to
         return KDA_ERR_INVALID_ARGUMENT;
     if (total_tokens > 0 && (!aligned(q, 16) || !aligned(o, 16) || q == o)) return KDA_ERR_INVALID_ARGUMENT;
     if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return KDA_ERR_UNSUPPORTED;
-    if ((int64_t)table_width * page_size > kInt32Max ||
+    if ((int64_t)table_width * page_size > kInt32Max - 127 ||
         2 * (int64_t)num_pages * page_size > kInt32Max / num_kv_heads || num_q_heads / num_kv_heads > 128 ||
         num_kv_heads > 65535 || (int64_t)total_tokens * num_q_heads > kInt32Max || batch > (1 << 20) ||
         num_groups > (1 << 20))

@@ -84,10 +84,11 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_own_rows_kernel(const Pref
 #pragma unroll
         for (int i = 0; i < 4; ++i) p[i] = r0 + 4 * ty + i < num_rows ? p0 + (r0 + 4 * ty + i) / G : -1;
         rows::State st;
-        const int32_t last = p0 + (min(r0 + kRows, num_rows) - 1) / G;  // no row sees a key behind it
-        for (int32_t t = req.from / kTile; t <= last / kTile; ++t)
-            rows::tile(tiles_of, s_keys, st, pool, a.cache, a.num_kv_heads, h, req.row, t * kTile, last + 1, a.scale,
-                       [&](int i, int32_t j) { return j >= req.from && j <= p[i]; });
+        const int32_t end = p0 + (min(r0 + kRows, num_rows) - 1) / G + 1;  // no row sees a key from here on
+        const int32_t tiles = (int32_t)(((uint32_t)(end - req.from) + kTile - 1) / kTile);
+        for (int32_t t = 0; t < tiles; ++t)
+            rows::tile(tiles_of, s_keys, st, pool, a.cache, a.num_kv_heads, h, req.row, req.from + t * kTile, end, a.scale,
+                       [&](int i, int32_t j) { return j <= p[i]; });
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = 4 * ty + i;

@@ -89,7 +89,7 @@ __device__ __forceinline__ PrefixRequest prefix_request(const PrefixAttentionArg
 // prefix, and the CTAs' slots (o, (m, l)).
 constexpr int32_t kPrefixCtas = 2 * 152;  // most of them
 struct PrefixSpace {
-    uint32_t *done;
+    uint32_t *done, *taken;  // taken: items of the second launch that a CTA has
     float *o, *own_o;
     float2 *ml;
     float4 *own;
@@ -107,7 +107,8 @@ __host__ __device__ inline size_t prefix_space_at(const PrefixAttentionArgs &a, 
         at += prefix_round(bytes);
         return p;
     };
-    s->done = reinterpret_cast<uint32_t *>(take(kPrefixCtas * sizeof(uint32_t)));
+    s->done = reinterpret_cast<uint32_t *>(take((kPrefixCtas + 1) * sizeof(uint32_t)));
+    s->taken = s->done + kPrefixCtas;
     s->o = reinterpret_cast<float *>(take(rows * kD * sizeof(float)));
     s->own_o = reinterpret_cast<float *>(take(rows * kD * sizeof(float)));
     s->ml = reinterpret_cast<float2 *>(take(rows * sizeof(float2)));
@@ -136,6 +137,7 @@ __device__ __forceinline__ void prefix_begin(const PrefixAttentionArgs &a, const
     const int64_t rows = (int64_t)a.cache.total_tokens * a.num_q_heads;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < rows; i += (int64_t)gridDim.x * blockDim.x)
         s.own[i] = make_float4(0.f, -1.f, 0.f, 0.f);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *s.taken = 0;
     __threadfence();
     __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

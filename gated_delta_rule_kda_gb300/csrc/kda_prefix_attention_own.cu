@@ -41,15 +41,19 @@ struct Params {
     float c;  // scale log2 e, > 0
 };
 
-struct Shared {
+struct Ring {
     uint64_t full[kStages], empty[kStages];
     int2 tile[kStages];       // first key; bit g: its keys 16 g .. have a page (and some row sees some)
+    uint32_t abort;
+};
+struct Shared {
+    Ring ring;
     float2 ml[kWarps][16];    // each warp's maximum reference and sum, by row
-    uint32_t abort, tainted;
+    uint32_t tainted;
 };
 
-__device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity, const Params &p, uint32_t what) {
-    return attn_wait_warp(bar, parity, &sh.abort, p.a, what);
+__device__ __forceinline__ bool wait(Ring &ring, uint64_t *bar, uint32_t parity, const Params &p, uint32_t what) {
+    return attn_wait_warp(bar, parity, &ring.abort, p.a, what);
 }
 
 // The own keys of a chunk's rows: [from, last], tokens p0 .. last.
@@ -61,13 +65,12 @@ struct Own {
 };
 
 // Fetches tiles [from, to) (numbers of 64-key tiles of the row): whole pages (up to a tile), except that of a
-// tile on an edge only the groups of 16 keys come that some row sees.  n0: tiles that went through the ring before.
-__device__ void produce(const Params &p, Shared &sh, unsigned char *sm, int32_t row, const Own &own, int32_t h,
-                        int32_t from, int32_t to, uint32_t n0) {
+// tile on an edge only the groups of 16 keys come that some row sees.  n: tiles that went through the ring.
+__device__ __forceinline__ bool produce(const Params &p, Ring &sh, unsigned char *sm, int32_t row, const Own &own, int32_t h,
+                                        int32_t from, int32_t to, uint32_t &n) {
     const int lane = threadIdx.x & 31;
     const PrefixAttentionArgs &a = p.a;
     const int32_t page_shift = p.page_shift;
-    uint32_t n = n0;
     for (int32_t i = from; i < to; ++i, ++n) {
         const int32_t s = n % kStages, j0 = i * kTile;
         const bool edge = own.some_hidden(j0, kTile);
@@ -78,7 +81,7 @@ __device__ void produce(const Params &p, Shared &sh, unsigned char *sm, int32_t 
         int32_t id = -1;
         if (mine && (!edge || (j <= own.last && j + 15 >= own.from))) id = attn_page(a.cache, row, own.last, j >> page_shift);
         const uint32_t exist = __ballot_sync(0xffffffffu, id >= 0);
-        if (n >= kStages && !wait(sh, &sh.empty[s], (n / kStages - 1) & 1, p, 196)) break;
+        if (n >= kStages && !wait(sh, &sh.empty[s], (n / kStages - 1) & 1, p, 196)) return false;
         if (lane == 0) {
             // a bit for 16 keys
             const uint32_t bits = shift == 4   ? exist
@@ -94,8 +97,11 @@ __device__ void produce(const Params &p, Shared &sh, unsigned char *sm, int32_t 
             tma_load_box(smem_u32(sm + s * kStageBytes + (lane << (shift + 9))), edge ? &p.tm_edge : &p.tm_kv, y, &sh.full[s]);
         }
     }
-    // Whichever warp gives up, the copies in flight land before the CTA leaves.
-    if (lane == 0)
+    return true;
+}
+// Whichever warp gives up, the copies in flight (of tiles before n, from n0 on) land before the CTA leaves.
+__device__ __forceinline__ void drain(Ring &sh, uint32_t n0, uint32_t n) {
+    if ((threadIdx.x & 31) == 0)
         for (uint32_t k = n > n0 + kStages ? n - kStages : n0; k < n; ++k)
             mbar_wait_bounded(&sh.full[k % kStages], (k / kStages) & 1, kAttnWaitNs);
 }
@@ -129,11 +135,136 @@ __device__ __noinline__ float2 own_row(const Params &p, int64_t q_row, int32_t h
     return make_float2(m, l);
 }
 
+// What a consumer warp holds of its 16 rows: this thread's are rows lane / 4 and lane / 4 + 8.
+struct Rows {
+    uint32_t q[8][4];
+    float o[16][4], m[2], l[2];  // channels 8 t + 2 (lane % 4) + {0, 1} of either row
+    int32_t pos[2];              // -1 sees nothing
+    uint32_t bad;                // some value that not all rows of the item see is not finite
+    __device__ __forceinline__ void clear() {
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+        bad = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    }
+};
+
+// A warp's share of the tile in stage s.
+template <int kBlocks>
+__device__ __forceinline__ void consume(const Params &p, const Ring &ring, unsigned char *sm, int32_t s, const Own &own, Rows &w) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    constexpr int kSteps = kTile / 16 * kBlocks / kWarps;  // steps of 16 keys of a warp
+    const int lane = threadIdx.x & 31, group = (threadIdx.x >> 5) / kBlocks;
+    auto &q = w.q;
+    auto &o = w.o;
+    auto &m = w.m;
+    auto &l = w.l;
+    auto &pos = w.pos;
+    const int2 info = ring.tile[s];
+    const int32_t j0 = info.x;
+    // some row must not see some key of the tile
+    const bool masked = (info.y & 15) != 15 || own.some_hidden(j0, kTile);
+    const uint32_t stage = smem_u32(sm + s * kStageBytes), shift = info.y >> 8, half_bytes = 128u << shift;
+#pragma unroll
+    for (int step = 0; step < kSteps; ++step) {
+        const int key0 = 16 * (group * kSteps + step);  // of the tile
+        // its box, and its place in it
+        const uint32_t k_addr = stage + ((key0 >> shift) << (shift + 9)) + ((key0 & ((1 << shift) - 1)) << 7);
+        const uint32_t v_addr = k_addr + 2 * half_bytes;
+        float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        {
+            // matrices: keys 0-7 / 8-15 x channels 0-7 / 8-15 of the step
+            const int row = (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const int chunk = 2 * (c & 3) + (lane >> 3 & 1);
+                uint32_t bm[4];
+                ldmatrix4(k_addr + (c >> 2) * half_bytes + row * 128 + ((chunk ^ (row & 7)) << 4), bm);
+                mma16816(sc[0], q[c], bm[0], bm[1]);
+                mma16816(sc[1], q[c], bm[2], bm[3]);
+            }
+        }
+        uint32_t keep[2] = {kAll, kAll}, part[2] = {0u, 0u};
+        if (masked) {
+            const bool mapped = info.y >> (key0 / 16) & 1;
+            // this thread's keys: 8 t + 2 (lane % 4) + {0, 1}
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int32_t j = j0 + key0 + 8 * t + 2 * (lane & 3) + e;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        if (!(mapped && own.visible(pos[u], j))) sc[t][2 * u + e] = -INFINITY;
+                    // of the values: keys that no row of the chunk sees are cleared, those that some see
+                    // are looked at
+                    const bool some = j >= own.from && j <= own.last, all = some && j <= own.p0;
+                    const uint32_t half = e ? 0xffff0000u : 0x0000ffffu;
+                    if (!some) keep[t] &= ~half;
+                    else if (!all) part[t] |= half;
+                }
+        }
+        float now[2], f[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            now[u] = fmaxf(fmaxf(sc[0][2 * u], sc[0][2 * u + 1]), fmaxf(sc[1][2 * u], sc[1][2 * u + 1]));
+            now[u] = fmaxf(now[u], __shfl_xor_sync(kAll, now[u], 1));
+            now[u] = fmaxf(now[u], __shfl_xor_sync(kAll, now[u], 2));
+        }
+        const bool move0 = (now[0] - m[0]) * p.c > 8.f, move1 = (now[1] - m[1]) * p.c > 8.f;
+        if (__any_sync(kAll, move0 || move1)) {
+            f[0] = move0 ? ex2_approx((m[0] - now[0]) * p.c) : 1.f;
+            f[1] = move1 ? ex2_approx((m[1] - now[1]) * p.c) : 1.f;
+            if (move0) m[0] = now[0];
+            if (move1) m[1] = now[1];
+            l[0] *= f[0];
+            l[1] *= f[1];
+#pragma unroll
+            for (int t = 0; t < 16; ++t) {
+                o[t][0] *= f[0];
+                o[t][1] *= f[0];
+                o[t][2] *= f[1];
+                o[t][3] *= f[1];
+            }
+        }
+        uint32_t pr[4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const float base = m[u] == -INFINITY ? 0.f : -m[u] * p.c;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const float x = ex2_approx(fmaf(sc[t][2 * u], p.c, base));
+                const float y = ex2_approx(fmaf(sc[t][2 * u + 1], p.c, base));
+                l[u] += x + y;
+                const __nv_bfloat162 hh = __floats2bfloat162_rn(x, y);
+                pr[2 * t + u] = *reinterpret_cast<const uint32_t *>(&hh);
+            }
+        }
+        // matrices: keys 0-7 / 8-15 x channels 0-7 / 8-15, transposed
+        const int row = lane & 15;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const int chunk = 2 * (c & 3) + (lane >> 4);
+            uint32_t bm[4];
+            ldmatrix4_trans(v_addr + (c >> 2) * half_bytes + row * 128 + ((chunk ^ (row & 7)) << 4), bm);
+            if (masked) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    w.bad |= any_nonfinite(bm[t] & part[t & 1]);
+                    bm[t] &= keep[t & 1];
+                }
+            }
+            mma16816(o[2 * c], pr, bm[0], bm[1]);
+            mma16816(o[2 * c + 1], pr, bm[2], bm[3]);
+        }
+    }
+}
+
 template <int kBlocks>
 __global__ void __launch_bounds__(kThreads, 2) prefix_own_kernel(const __grid_constant__ Params p) {
     constexpr int kRows = 16 * kBlocks;
     constexpr int kGroups = kWarps / kBlocks;         // key groups of a tile
-    constexpr int kSteps = kTile / 16 / kGroups;      // steps of 16 keys of a warp in a tile
     constexpr uint32_t kAll = 0xffffffffu;
     extern __shared__ unsigned char dyn[];
     __shared__ Shared sh;
@@ -145,10 +276,10 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_own_kernel(const __grid_co
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], kWarps);
+            mbar_init(&sh.ring.full[i], 1);
+            mbar_init(&sh.ring.empty[i], kWarps);
         }
-        sh.abort = sh.tainted = 0;
+        sh.ring.abort = sh.tainted = 0;
         fence_mbar_init();
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join comes up when the last CTA has
@@ -167,152 +298,52 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_own_kernel(const __grid_co
         const int32_t from = tile0 + (int32_t)((int64_t)tiles * rank / splits);
         const int32_t to = tile0 + (int32_t)((int64_t)tiles * (rank + 1) / splits);
         if (warp == kWarps) {
-            if (!attn_withhold(a)) produce(p, sh, sm, req.row, own, h, from, to, n0);
+            uint32_t n = n0;
+            if (!attn_withhold(a)) produce(p, sh.ring, sm, req.row, own, h, from, to, n);
+            drain(sh.ring, n0, n);
         } else {
             const int block = warp % kBlocks, group = warp / kBlocks;
             // this thread's two rows: 16 block + lane / 4 (+ 8)
             const int32_t row0 = 16 * block + (lane >> 2);
-            int32_t pos[2];
-            uint32_t q[8][4];
+            Rows w;
+            w.clear();
             {
                 const __nv_bfloat16 *base = static_cast<const __nv_bfloat16 *>(a.q) + 2 * (lane & 3);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int32_t row = row_base + row0 + 8 * u, token = row / G;
                     const bool live = row < num_rows;
-                    pos[u] = live ? q0 + token : -1;  // -1 sees nothing
+                    w.pos[u] = live ? q0 + token : -1;
                     const __nv_bfloat16 *src = base + ((int64_t)(req.first + (live ? token : 0)) * a.num_q_heads + h * G + (live ? row % G : 0)) * kD;
 #pragma unroll
                     for (int s = 0; s < 8; ++s) {
-                        q[s][u] = live ? *reinterpret_cast<const uint32_t *>(src + 16 * s) : 0u;
-                        q[s][2 + u] = live ? *reinterpret_cast<const uint32_t *>(src + 16 * s + 8) : 0u;
+                        w.q[s][u] = live ? *reinterpret_cast<const uint32_t *>(src + 16 * s) : 0u;
+                        w.q[s][2 + u] = live ? *reinterpret_cast<const uint32_t *>(src + 16 * s + 8) : 0u;
                     }
                 }
             }
-            float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-            uint32_t bad_values = 0;
-
             uint32_t n = n0;
             for (int32_t i = from; i < to; ++i, ++n) {
                 const int32_t s = n % kStages;
-                if (!wait(sh, &sh.full[s], (n / kStages) & 1, p, 197)) break;
-                const int2 info = sh.tile[s];
-                const int32_t j0 = info.x;
-                // some row must not see some key of the tile
-                const bool masked = (info.y & 15) != 15 || own.some_hidden(j0, kTile);
-                const uint32_t stage = smem_u32(sm + s * kStageBytes), shift = info.y >> 8, half_bytes = 128u << shift;
-#pragma unroll
-                for (int step = 0; step < kSteps; ++step) {
-                    const int key0 = 16 * (group * kSteps + step);  // of the tile
-                    // its box, and its place in it
-                    const uint32_t k_addr = stage + ((key0 >> shift) << (shift + 9)) + ((key0 & ((1 << shift) - 1)) << 7);
-                    const uint32_t v_addr = k_addr + 2 * half_bytes;
-                    float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-                    {
-                        // matrices: keys 0-7 / 8-15 x channels 0-7 / 8-15 of the step
-                        const int row = (lane & 7) + (lane >> 4) * 8;
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const int chunk = 2 * (c & 3) + (lane >> 3 & 1);
-                            uint32_t bm[4];
-                            ldmatrix4(k_addr + (c >> 2) * half_bytes + row * 128 + ((chunk ^ (row & 7)) << 4), bm);
-                            mma16816(sc[0], q[c], bm[0], bm[1]);
-                            mma16816(sc[1], q[c], bm[2], bm[3]);
-                        }
-                    }
-                    uint32_t keep[2] = {kAll, kAll}, part[2] = {0u, 0u};
-                    if (masked) {
-                        const bool mapped = info.y >> (key0 / 16) & 1;
-                        // this thread's keys: 8 t + 2 (lane % 4) + {0, 1}
-#pragma unroll
-                        for (int t = 0; t < 2; ++t)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int32_t j = j0 + key0 + 8 * t + 2 * (lane & 3) + e;
-#pragma unroll
-                                for (int u = 0; u < 2; ++u)
-                                    if (!(mapped && own.visible(pos[u], j))) sc[t][2 * u + e] = -INFINITY;
-                                // of the values: keys that no row of the chunk sees are cleared, those that some see
-                                // are looked at
-                                const bool some = j >= own.from && j <= own.last, all = some && j <= own.p0;
-                                const uint32_t half = e ? 0xffff0000u : 0x0000ffffu;
-                                if (!some) keep[t] &= ~half;
-                                else if (!all) part[t] |= half;
-                            }
-                    }
-                    float now[2], f[2];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        now[u] = fmaxf(fmaxf(sc[0][2 * u], sc[0][2 * u + 1]), fmaxf(sc[1][2 * u], sc[1][2 * u + 1]));
-                        now[u] = fmaxf(now[u], __shfl_xor_sync(kAll, now[u], 1));
-                        now[u] = fmaxf(now[u], __shfl_xor_sync(kAll, now[u], 2));
-                    }
-                    const bool move0 = (now[0] - m[0]) * p.c > 8.f, move1 = (now[1] - m[1]) * p.c > 8.f;
-                    if (__any_sync(kAll, move0 || move1)) {
-                        f[0] = move0 ? ex2_approx((m[0] - now[0]) * p.c) : 1.f;
-                        f[1] = move1 ? ex2_approx((m[1] - now[1]) * p.c) : 1.f;
-                        if (move0) m[0] = now[0];
-                        if (move1) m[1] = now[1];
-                        l[0] *= f[0];
-                        l[1] *= f[1];
-#pragma unroll
-                        for (int t = 0; t < 16; ++t) {
-                            o[t][0] *= f[0];
-                            o[t][1] *= f[0];
-                            o[t][2] *= f[1];
-                            o[t][3] *= f[1];
-                        }
-                    }
-                    uint32_t pr[4];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const float base = m[u] == -INFINITY ? 0.f : -m[u] * p.c;
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            const float x = ex2_approx(fmaf(sc[t][2 * u], p.c, base));
-                            const float y = ex2_approx(fmaf(sc[t][2 * u + 1], p.c, base));
-                            l[u] += x + y;
-                            const __nv_bfloat162 hh = __floats2bfloat162_rn(x, y);
-                            pr[2 * t + u] = *reinterpret_cast<const uint32_t *>(&hh);
-                        }
-                    }
-                    // matrices: keys 0-7 / 8-15 x channels 0-7 / 8-15, transposed
-                    const int row = lane & 15;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const int chunk = 2 * (c & 3) + (lane >> 4);
-                        uint32_t bm[4];
-                        ldmatrix4_trans(v_addr + (c >> 2) * half_bytes + row * 128 + ((chunk ^ (row & 7)) << 4), bm);
-                        if (masked) {
-#pragma unroll
-                            for (int t = 0; t < 4; ++t) {
-                                bad_values |= any_nonfinite(bm[t] & part[t & 1]);
-                                bm[t] &= keep[t & 1];
-                            }
-                        }
-                        mma16816(o[2 * c], pr, bm[0], bm[1]);
-                        mma16816(o[2 * c + 1], pr, bm[2], bm[3]);
-                    }
-                }
+                if (!wait(sh.ring, &sh.ring.full[s], (n / kStages) & 1, p, 197)) break;
+                consume<kBlocks>(p, sh.ring, sm, s, own, w);
                 __syncwarp();
-                if (lane == 0) arrive(&sh.empty[s]);
+                if (lane == 0) arrive(&sh.ring.empty[s]);
             }
-            if (bad_values) sh.tainted = 1;
+            if (w.bad) sh.tainted = 1;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                l[u] += __shfl_xor_sync(kAll, l[u], 1);
-                l[u] += __shfl_xor_sync(kAll, l[u], 2);
-                if ((lane & 3) == 0) sh.ml[warp][(lane >> 2) + 8 * u] = make_float2(m[u], l[u]);
+                w.l[u] += __shfl_xor_sync(kAll, w.l[u], 1);
+                w.l[u] += __shfl_xor_sync(kAll, w.l[u], 2);
+                if ((lane & 3) == 0) sh.ml[warp][(lane >> 2) + 8 * u] = make_float2(w.m[u], w.l[u]);
             }
             // every consumer is past the ring's last tile: the partial outputs take its place
             asm volatile("bar.sync 1, 128;" ::: "memory");
             float *part = reinterpret_cast<float *>(sm) + warp * 16 * kPitch + (lane >> 2) * kPitch + 2 * (lane & 3);
 #pragma unroll
             for (int t = 0; t < 16; ++t) {
-                *reinterpret_cast<float2 *>(part + 8 * t) = make_float2(o[t][0], o[t][1]);
-                *reinterpret_cast<float2 *>(part + 8 * kPitch + 8 * t) = make_float2(o[t][2], o[t][3]);
+                *reinterpret_cast<float2 *>(part + 8 * t) = make_float2(w.o[t][0], w.o[t][1]);
+                *reinterpret_cast<float2 *>(part + 8 * kPitch + 8 * t) = make_float2(w.o[t][2], w.o[t][3]);
             }
         }
         n0 += (uint32_t)(to - from);
@@ -322,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_own_kernel(const __grid_co
         // Join: the rows go round the cluster's consumer warps, four channels a lane.
         bool failed = false, tainted = false;
         for (int32_t k = 0; k < splits; ++k) {
-            failed |= remote_u32(remote(smem_u32(&sh.abort), k)) != 0;
+            failed |= remote_u32(remote(smem_u32(&sh.ring.abort), k)) != 0;
             tainted |= remote_u32(remote(smem_u32(&sh.tainted), k)) != 0;
         }
         if (warp < kWarps && !failed) {  // (else the rows have no result)
@@ -377,6 +408,254 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_own_kernel(const __grid_co
     if (blockIdx.x == 0 && blockIdx.y == 0) grid_wait();  // the launch ends after the one before it
 }
 
+// ---------------------------------------------------------------------------
+// Many requests of up to 16 rows a kv head each
+// ---------------------------------------------------------------------------
+// Here the CTAs stay and take item after item, (request, kv head) pairs, as they get done, so that an item's beginning and end hide behind its neighbours' keys: a sixth warp takes the items,
+// looks their requests up and brings q, and the fetching warp goes on to the next item's keys while the
+// consumers end the last one's.  Which CTA computes an item makes no difference to it.
+constexpr int kManyThreads = 32 * (kWarps + 2);
+constexpr int kItems = 4;                      // in the queue
+constexpr int kQPitch = 2 * kD + 16;           // bytes: the eight rows of a fragment in distinct banks
+constexpr size_t kManyQ = kStages * kStageBytes, kManySwap = kManyQ + 16 * kQPitch;
+constexpr size_t kManySmem = kManySwap + kWarps * 16 * 32 * sizeof(float) + 1024;
+
+struct Item {
+    int32_t first, rows;       // first token of the request; rows of the item (0: no more items)
+    int32_t h, table_row;
+    int32_t q0, from;          // indices of the request's first token and of its first own key
+    __device__ __forceinline__ Own own(int32_t G) const { return Own{from, q0, q0 + (rows - 1) / G}; }
+};
+struct ManyShared {
+    Ring ring;
+    uint64_t item_full[kItems], item_empty[kItems], q_full, q_empty;
+    Item item[kItems];
+    float2 ml[kWarps][16];
+};
+
+// Barrier 1 of the four consumer warps; whether any thread says x.
+__device__ __forceinline__ bool consumers_or(bool x) {
+    uint32_t any;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(any) : "r"((uint32_t)x) : "memory");
+    return any != 0;
+}
+
+// The sixth warp.
+__device__ void take_items(const Params &p, ManyShared &sh, unsigned char *sm, uint32_t *taken) {
+    const int lane = threadIdx.x & 31;
+    const PrefixAttentionArgs &a = p.a;
+    const uint32_t items = (uint32_t)a.cache.batch * (uint32_t)a.num_kv_heads;
+    const auto next = [&] {
+        uint32_t t = 0;
+        if (lane == 0) t = atomicAdd(taken, 1u);
+        return __shfl_sync(0xffffffffu, t, 0);
+    };
+    uint32_t n = 0;  // items published
+    for (uint32_t t = next();;) {
+        Item it{};
+        const bool end = t >= items;
+        if (!end) {
+            const uint32_t b = t / (uint32_t)a.num_kv_heads;
+            it.h = (int32_t)(t - b * (uint32_t)a.num_kv_heads);
+            t = next();  // (on its way while the request is looked up)
+            const PrefixRequest req = prefix_request(a, p.cut, (int32_t)b);
+            if (!req.ok && it.h == 0 && lane == 0) record_status(a.status, KDA_ERR_DEVICE_CHECK, b);
+            if (req.n == 0) continue;
+            it.first = req.first;
+            it.rows = req.n * p.G;
+            it.table_row = req.row;
+            it.q0 = req.len - req.n;
+            it.from = req.from;
+        }
+        const uint32_t s = n % kItems;
+        if (n >= kItems && !wait(sh.ring, &sh.item_empty[s], (n / kItems - 1) & 1, p, 198)) return;
+        if (lane == 0) {
+            sh.item[s] = it;
+            arrive(&sh.item_full[s]);
+        }
+        __syncwarp();
+        if (end) return;
+        uint4 x[8];  // rows lane / 16 + 2 i
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int32_t r = (lane >> 4) + 2 * i, token = r / p.G;
+            x[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < it.rows)
+                x[i] = *reinterpret_cast<const uint4 *>(
+                    static_cast<const __nv_bfloat16 *>(a.q) +
+                    ((int64_t)(it.first + token) * a.num_q_heads + it.h * p.G + r - token * p.G) * kD + 8 * (lane & 15));
+        }
+        if (n > 0 && !wait(sh.ring, &sh.q_empty, (n - 1) & 1, p, 199)) return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4 *>(sm + kManyQ + ((lane >> 4) + 2 * i) * kQPitch + 16 * (lane & 15)) = x[i];
+        __syncwarp();
+        if (lane == 0) arrive(&sh.q_full);
+        ++n;
+    }
+}
+
+__global__ void __launch_bounds__(kManyThreads, 2) prefix_own_many_kernel(const __grid_constant__ Params p) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    extern __shared__ unsigned char dyn[];
+    __shared__ ManyShared sh;
+    unsigned char *sm = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const PrefixAttentionArgs &a = p.a;
+    const int32_t G = p.G;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sh.ring.full[i], 1);
+            mbar_init(&sh.ring.empty[i], kWarps);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&sh.item_full[i], 1);
+            mbar_init(&sh.item_empty[i], kWarps + 1);
+        }
+        mbar_init(&sh.q_full, 1);
+        mbar_init(&sh.q_empty, kWarps);
+        sh.ring.abort = 0;
+        fence_mbar_init();
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join comes up when the last CTA has
+    const PrefixSpace space = prefix_space(a);
+    __syncthreads();
+
+    if (warp == kWarps + 1) {
+        take_items(p, sh, sm, space.taken);
+    } else if (warp == kWarps) {
+        uint32_t tiles = 0;
+        for (uint32_t n = 0; !attn_withhold(a); ++n) {
+            const uint32_t s = n % kItems;
+            if (!wait(sh.ring, &sh.item_full[s], (n / kItems) & 1, p, 200)) break;
+            const Item it = sh.item[s];
+            __syncwarp();
+            if (lane == 0) arrive(&sh.item_empty[s]);
+            if (it.rows == 0) break;
+            const Own own = it.own(G);
+            if (!produce(p, sh.ring, sm, it.table_row, own, it.h, own.from / kTile, own.last / kTile + 1, tiles)) break;
+        }
+        drain(sh.ring, 0, tiles);
+    } else {
+        uint32_t tiles = 0;
+        Rows w;
+        for (uint32_t n = 0;; ++n) {
+            const uint32_t s = n % kItems;
+            bool got = wait(sh.ring, &sh.item_full[s], (n / kItems) & 1, p, 201);
+            const Item it = sh.item[s];
+            __syncwarp();
+            if (lane == 0) arrive(&sh.item_empty[s]);
+            if (got && it.rows > 0) got = wait(sh.ring, &sh.q_full, n & 1, p, 202);
+            if (consumers_or(!got) || it.rows == 0) break;  // all four or none
+            {
+                const uint32_t at = smem_u32(sm) + (uint32_t)kManyQ + (lane & 15) * kQPitch + 16 * (lane >> 4);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) ldmatrix4(at + 32 * c, w.q[c]);
+            }
+            __syncwarp();
+            if (lane == 0) arrive(&sh.q_empty);
+            w.clear();
+            const Own own = it.own(G);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int32_t r = (lane >> 2) + 8 * u;
+                w.pos[u] = r < it.rows ? it.q0 + r / G : -1;
+            }
+            for (int32_t i = own.from / kTile; i <= own.last / kTile; ++i, ++tiles) {
+                const int32_t st = tiles % kStages;
+                if (!wait(sh.ring, &sh.ring.full[st], (tiles / kStages) & 1, p, 203)) break;
+                consume<1>(p, sh.ring, sm, st, own, w);
+                __syncwarp();
+                if (lane == 0) arrive(&sh.ring.empty[st]);
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                w.l[u] += __shfl_xor_sync(kAll, w.l[u], 1);
+                w.l[u] += __shfl_xor_sync(kAll, w.l[u], 2);
+                if ((lane & 3) == 0) sh.ml[warp][(lane >> 2) + 8 * u] = make_float2(w.m[u], w.l[u]);
+            }
+            if (consumers_or(attn_given_up(&sh.ring.abort))) break;  // (the rows have no result)
+            const auto place = [&](int32_t r) {  // row r of the item, as a row of [T][Hq]
+                const int32_t token = r / G;
+                return (int64_t)(it.first + token) * a.num_q_heads + it.h * G + (r - token * G);
+            };
+            if (consumers_or(w.bad != 0)) {
+                for (int32_t r = warp; r < it.rows; r += kWarps) {
+                    float4 acc;
+                    const int64_t at = place(r);
+                    const float2 x = own_row(p, at, it.h, it.table_row, own, it.q0 + r / G, acc);
+                    store4(space.own_o + at * kD + 4 * lane, acc);
+                    if (lane == 0) space.own[at] = make_float4(x.x, x.y, it.from > 0, 0.f);
+                }
+                continue;
+            }
+            // The warps' shares joined: warp w gets channels 32 w .. of every row from the other three, one after
+            // the other through 8 KB, lane to lane.
+            float top[2], sum[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float2 ml[kWarps];
+                top[u] = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < kWarps; ++k) {
+                    ml[k] = sh.ml[k][(lane >> 2) + 8 * u];
+                    top[u] = fmaxf(top[u], ml[k].x);
+                }
+                const auto weight = [&](float mx, float lx) {  // (a NaN sum stays one)
+                    return mx == -INFINITY ? (lx == 0.f ? 0.f : 1.f) : ex2_approx((mx - top[u]) * p.c);
+                };
+                sum[u] = 0.f;
+#pragma unroll
+                for (int k = 0; k < kWarps; ++k) sum[u] = fmaf(weight(ml[k].x, ml[k].y), ml[k].y, sum[u]);
+                const float mine = weight(w.m[u], w.l[u]);
+#pragma unroll
+                for (int t = 0; t < 16; ++t) {
+                    w.o[t][2 * u] *= mine;
+                    w.o[t][2 * u + 1] *= mine;
+                }
+            }
+            float4 acc[4];
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k)
+                if (k == warp)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) acc[t] = make_float4(w.o[4 * k + t][0], w.o[4 * k + t][1], w.o[4 * k + t][2], w.o[4 * k + t][3]);
+            float4 *swap = reinterpret_cast<float4 *>(sm + kManySwap) + lane;  // [receiver][4][lane]
+#pragma unroll 1
+            for (int turn = 1; turn < kWarps; ++turn) {
+                const int to = (warp + turn) % kWarps;
+#pragma unroll
+                for (int k = 0; k < kWarps; ++k)
+                    if (k == to)
+#pragma unroll
+                        for (int t = 0; t < 4; ++t)
+                            swap[(k * 4 + t) * 32] = make_float4(w.o[4 * k + t][0], w.o[4 * k + t][1], w.o[4 * k + t][2], w.o[4 * k + t][3]);
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const float4 x = swap[(warp * 4 + t) * 32];
+                    acc[t] = make_float4(acc[t].x + x.x, acc[t].y + x.y, acc[t].z + x.z, acc[t].w + x.w);
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int32_t r = (lane >> 2) + 8 * u;
+                if (r >= it.rows) continue;
+                const int64_t at = place(r);
+                float *o = space.own_o + at * kD + 32 * warp + 2 * (lane & 3);
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    *reinterpret_cast<float2 *>(o + 8 * t) = u ? make_float2(acc[t].z, acc[t].w) : make_float2(acc[t].x, acc[t].y);
+                if (warp == 0 && (lane & 3) == 0) space.own[at] = make_float4(top[u], sum[u], it.from > 0, 0.f);
+            }
+        }
+    }
+    __syncthreads();
+    if (blockIdx.x == 0) grid_wait();  // the launch ends after the one before it
+}
+
 template <int kBlocks>
 cudaError_t launch(const Params &p, int splits, cudaStream_t stream) {
     const dim3 grid((unsigned)((int64_t)splits * p.a.cache.batch * p.chunks), (unsigned)p.a.num_kv_heads);
@@ -410,6 +689,11 @@ cudaError_t launch_prefix_own(const PrefixAttentionArgs &a, const PrefixCut &cut
     int splits = 1;
     while (splits < kMaxSplits && ctas * splits <= device_sm_count() && tiles >= 4 * splits) splits *= 2;
     if (splits * B * p.chunks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    const int64_t most_ctas = 2 * device_sm_count();
+    if (rows == 16 && splits == 1 && ctas > most_ctas && ctas <= 0x7fffffff) {
+        const cudaError_t e = allow_smem(prefix_own_many_kernel, kManySmem);
+        return e == cudaSuccess ? launch_serial(prefix_own_many_kernel, dim3((unsigned)most_ctas), kManyThreads, kManySmem, stream, p) : e;
+    }
     return rows == 16 ? launch<1>(p, splits, stream) : launch<2>(p, splits, stream);
 }
 

@@ -805,12 +805,15 @@ size_t kda_prefix_attention_workspace_size(kda_dtype dtype, int32_t batch, int32
  * The same call gives the same bits again.
  * Errors: KDA_ERR_INVALID_ARGUMENT (null/misaligned pointers, sizes below 1,
  * T < 0, Hq not a multiple of Hkv, dtype), KDA_ERR_WORKSPACE,
- * KDA_ERR_UNSUPPORTED (as kda_window_attention; more than 2^20 requests or
- * groups), KDA_ERR_CUDA.  A request whose slot, kv_len or token range is out of
+ * KDA_ERR_UNSUPPORTED (as kda_window_attention, and M page_size above
+ * 2^31 - 128; more than 2^20 requests or groups; T * Hq above 2^31 - 1),
+ * KDA_ERR_CUDA.  A request whose slot, kv_len or token range is out of
  * range, that no group holds, or whose group's prefix_len is longer than
  * kv_len[row] - n_b or whose group's first slot is out of range, is refused by
  * the kernel (its rows of o stay as they are; KDA_ERR_DEVICE_CHECK with
- * detail = b).
+ * detail = b).  Where cu_groups falls from one entry to the next, or a launch
+ * gave up (KDA_ERR_DEVICE_TIMEOUT), no row of o is written; the detail is then
+ * the group.
  */
 kda_status kda_prefix_attention(kda_dtype dtype, int32_t batch, int32_t total_tokens,
                                 int32_t max_tokens, int32_t num_q_heads, int32_t num_kv_heads,

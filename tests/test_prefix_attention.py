@@ -89,6 +89,53 @@ def test_many_groups(kda):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("shape", [(7, 8, 4, 64, 4), (70, 8, 5, 16, 3), (43, 40, 1, 32, 16), (330, 1, 16, 128, 1)])
+def test_many_requests(kda, shape, dtype):
+    """More (request, kv head) pairs than CTAs fit on the GPU: requests of all lengths and numbers of tokens (also
+    none), one of them refused, and values that are not finite in the step's own tokens and where nothing is."""
+    B, heads, group, page, most = shape
+    rng = np.random.RandomState(B)
+    sizes = [B // 2, 0, B - B // 2 - 1, 1]
+    new = [int(rng.randint(1, most + 1)) if i % 5 else min(most, i) for i in range(B)]
+    mine = [[new[sum(sizes[:g]) + i] + int(rng.randint(0, 260)) * (i % 3) for i in range(n)] for g, n in enumerate(sizes)]
+    c = build_branches([300, 7, 0, 40], mine, page, heads, dtype, seed=B)
+    table, kv_len, slot = (c[k].cpu().numpy() for k in ("table", "kv_len", "slot"))
+    clean = {**c, "pool": c["pool"].clone()}
+    for b in range(0, B, 3):  # behind the last token of its page
+        n = int(kv_len[slot[b]])
+        if n % page:
+            c["pool"][table[slot[b], n // page], :, :, n % page:] = float("nan")
+    late = max(range(B), key=lambda b: new[b] * (b % 3 != 0))  # a value that only the last token sees
+    if new[late] > 1:
+        j = int(kv_len[slot[late]]) - 1
+        c["pool"][table[slot[late], j // page], 1, :, j % page, 5] = float("inf")
+    q = queries(sum(new), heads * group, dtype, B)
+    cu = cu_of(new).tolist()
+    refused = next(b for b in range(B // 2, B) if new[b] and b != late)
+    gone = torch.full_like(q, 7.0)
+    call(kda, q, {**c, "slot": c["slot"].clone().index_fill_(0, torch.tensor([refused], device="cuda"), -1)}, new, o=gone)
+    # (where it is the first of its group, the prefix is read through its row: then the group is refused)
+    ends = np.cumsum(sizes)
+    g = int(np.searchsorted(ends, refused, side="right"))
+    group_of = range(int(ends[g]) - sizes[g], int(ends[g]))
+    lost = list(group_of) if refused == group_of[0] else [refused]
+    status, detail = kda.kda_get_device_status()
+    assert status == 6 and detail in lost
+    o = call(kda, q, c, new)
+    assert kda.kda_get_device_status()[0] == 0
+    same = torch.ones(len(q), dtype=torch.bool, device="cuda")
+    for b in lost:
+        same[cu[b]:cu[b + 1]] = False
+    assert torch.equal(torch.nan_to_num(gone[same].float()), torch.nan_to_num(o[same].float()))
+    assert bool((gone[~same] == 7.0).all())
+    if new[late] > 1:
+        last = cu[late + 1] - 1
+        assert not torch.isfinite(o[last, :, 5]).any()
+        o[last] = call(kda, q, clean, new)[last]
+    check(o, q, clean, new)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_same_as_window_attention_without_a_window(kda, dtype):
     """Rows that share their prefix: the two calls differ by roundings alone."""
     new = [1, 2, 1, 4]
