@@ -64,6 +64,15 @@ struct Own {
     __device__ __forceinline__ bool some_hidden(int32_t j, int32_t n) const { return j < from || j + (n - 1) > p0; }
 };
 
+// tma_load_box of what is read once: it is the first to leave L2, where the prefixes' tiles are read again and again.
+__device__ __forceinline__ void load_once(uint32_t dst, const void *tmap, int y, uint64_t *bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {%3, %2, %3, %3}], [%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(y), "r"(0), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
 // Fetches tiles [from, to) (numbers of 64-key tiles of the row): whole pages (up to a tile), except that of a
 // tile on an edge only the groups of 16 keys come that some row sees.  n: tiles that went through the ring.
 __device__ __forceinline__ bool produce(const Params &p, Ring &sh, unsigned char *sm, int32_t row, const Own &own, int32_t h,
@@ -71,6 +80,8 @@ __device__ __forceinline__ bool produce(const Params &p, Ring &sh, unsigned char
     const int lane = threadIdx.x & 31;
     const PrefixAttentionArgs &a = p.a;
     const int32_t page_shift = p.page_shift;
+    uint64_t policy;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
     for (int32_t i = from; i < to; ++i, ++n) {
         const int32_t s = n % kStages, j0 = i * kTile;
         const bool edge = own.some_hidden(j0, kTile);
@@ -94,7 +105,7 @@ __device__ __forceinline__ bool produce(const Params &p, Ring &sh, unsigned char
         if (mine) {
             const int32_t y = id < 0 ? p.kv_rows  // out of range: zeros
                                      : ((id * 2 * a.num_kv_heads + h) << page_shift) + (j & ((1 << page_shift) - 1));
-            tma_load_box(smem_u32(sm + s * kStageBytes + (lane << (shift + 9))), edge ? &p.tm_edge : &p.tm_kv, y, &sh.full[s]);
+            load_once(smem_u32(sm + s * kStageBytes + (lane << (shift + 9))), edge ? &p.tm_edge : &p.tm_kv, y, &sh.full[s], policy);
         }
     }
     return true;
