@@ -1,10 +1,17 @@
 // C ABI of the operators that decode the branches of a request (attention over a shared prefix, beam
 // selection, beam reordering): argument validation on the host, then kernel launches.  Nothing here allocates.
+#include <atomic>
+
 #include "kda_common.cuh"
 
 using namespace kda;
 
 namespace {
+
+#ifdef KDA_DEBUG
+// Armed by kda_debug_inject_prefix_timeout, consumed by the next kda_prefix_attention.
+std::atomic<int> g_withhold_prefix{0};
+#endif
 
 constexpr int64_t kInt32Max = 0x7fffffffLL;
 
@@ -60,7 +67,19 @@ kda_status kda_prefix_attention(kda_dtype dtype, int32_t batch, int32_t total_to
                         page_table, slot, cu_tokens, kv_len};
     a.workspace = workspace;
     a.status = device_status();
+#ifdef KDA_DEBUG
+    a.withhold = g_withhold_prefix.exchange(0);
+#endif
     return from_cuda(launch_prefix_attention(a, static_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_debug_inject_prefix_timeout(void) {
+#ifdef KDA_DEBUG
+    g_withhold_prefix.store(1);
+    return KDA_OK;
+#else
+    return KDA_ERR_UNSUPPORTED;
+#endif
 }
 
 size_t kda_beam_select_workspace_size(int32_t batch, int32_t beams, int32_t vocab, int32_t choices) {

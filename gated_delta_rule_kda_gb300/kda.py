@@ -76,6 +76,7 @@ EXPORTED = (
     "kda_get_device_status",
     "kda_debug_inject_handoff_timeout",
     "kda_debug_inject_attention_timeout",
+    "kda_debug_inject_prefix_timeout",
 )
 
 # Capacity of the fixed scratch array behind kda_layer_core_noalloc (include/kda.h).
@@ -190,6 +191,8 @@ def _load() -> ctypes.CDLL:
     lib.kda_debug_inject_handoff_timeout.restype = ctypes.c_int
     lib.kda_debug_inject_attention_timeout.argtypes = []
     lib.kda_debug_inject_attention_timeout.restype = ctypes.c_int
+    lib.kda_debug_inject_prefix_timeout.argtypes = []
+    lib.kda_debug_inject_prefix_timeout.restype = ctypes.c_int
     return lib
 
 

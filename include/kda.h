@@ -978,6 +978,12 @@ kda_status kda_debug_inject_handoff_timeout(void);
  */
 kda_status kda_debug_inject_attention_timeout(void);
 
+/*
+ * kda_debug_inject_prefix_timeout - the same for kda_prefix_attention (detail:
+ * 128 and above).
+ */
+kda_status kda_debug_inject_prefix_timeout(void);
+
 #ifdef __cplusplus
 }
 #endif

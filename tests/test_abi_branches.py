@@ -49,8 +49,9 @@ def test_prefix_workspace(kda, dtype):
     need = kda.kda_prefix_attention_workspace_size(dtype, 2, 4, 1, 8, 2)
     assert need > 0
     assert prefix(lib, dt=code, ws=None) == prefix(lib, dt=code, ws=MIS) == prefix(lib, dt=code, wsb=need - 1) == 3
-    for more in ((2, 4000, 1, 8, 2), (2, 4, 9, 8, 2), (2, 4000, 1, 80, 2)):
+    for more in ((2, 4000, 1, 8, 2), (2, 4000, 1, 80, 2)):
         assert kda.kda_prefix_attention_workspace_size(dtype, *more) > need
+    assert kda.kda_prefix_attention_workspace_size(dtype, 2, 4, 9, 8, 2) >= need  # (nothing is kept by group)
     for bad in ((0, 4, 1, 8, 2), (2, -1, 1, 8, 2), (2, 4, 0, 8, 2), (2, 4, 1, 9, 2), (2, 4, 1, 0, 2), (2, 4, 1, 8, 0)):
         assert kda.kda_prefix_attention_workspace_size(dtype, *bad) == 0
 
@@ -269,3 +270,7 @@ def test_what_a_call_allocates_belongs_to_its_stream(kda, name, monkeypatch):
      "slots": lambda: kda.kda_beam_reorder(a["parent"], a["beams"], num_rows=9, stream=s)}[name]()
     assert launched == [0x1230]
     assert made and all(x is s for x in made)
+
+
+def test_normal_library_refuses_the_injection(kda):
+    assert kda.library().kda_debug_inject_prefix_timeout() == 2

@@ -5,6 +5,9 @@ at most 2^-8 of itself and so is the rounded output; the fp32 parts (128-term sc
 sums, the join of the parts) stay below 2^-12 of it.  With a = sum_j softmax_j |v_j| that is
 |o - ref| <= 2^-8 (a + |ref|) + 2^-12 a.  fp32: max-abs over rms 1e-5, the bound of every fp32 path here.
 """
+import ctypes
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -383,3 +386,64 @@ def test_on_a_side_stream(kda):
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(o, want)
         del blocks
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_two_calls_at_once(kda, dtype):
+    """Two streams, each with a workspace of its own, give what one after the other does."""
+    inputs = []
+    for seed, (prefix, mine, new) in enumerate([([3000, 40], [[9] * 40, [300] * 40], [1] * 80), ([700], [[50] * 200], [1] * 200)]):
+        c = build_branches(prefix, mine, 32, 2, dtype, seed=67 + seed)
+        inputs.append((queries(len(new), 16, dtype, 67 + seed), c, new))
+    want = [call(kda, *x) for x in inputs]
+    streams = [torch.cuda.Stream() for _ in inputs]
+    cu = [cu_of(new) for _, _, new in inputs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (q, c, new) in enumerate(inputs):
+            got[i].append(kda.kda_prefix_attention(q, c["pool"], c["table"], c["slot"], cu[i], c["kv_len"], c["cu_groups"],
+                                                   c["prefix_len"], max_tokens=1, stream=streams[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i in range(2) for o in got[i])
+    assert kda.kda_get_device_status()[0] == 0
+
+
+# prefixes, own keys and new tokens: one of each kind of kernel over the own keys (single rows of a cluster, two blocks
+# of rows, many requests), with prefixes and without
+GIVING_UP = [([300], [[9, 30]], [1, 1]), ([700], [[9, 30]], [7, 5]), ([300], [[20] * 160], [1] * 160),
+             ([0], [[9, 30]], [1, 1]), ([0], [[20] * 160], [1] * 160)]
+
+
+@pytest.mark.parametrize("shape", GIVING_UP)
+def test_waits_that_run_out_are_reported(kda, shape):
+    """The debug library arms one call whose load warps fetch nothing and whose waits give up after 1 ms: the call ends
+    soon, with the status and with o as it was, and the next one through the same workspace is right."""
+    from gated_delta_rule_kda_gb300 import build
+    prefix, mine, new = shape
+    c = build_branches(prefix, mine, 32, 2, BF16, seed=61)
+    q, cu, T, B = queries(sum(new), 8, BF16, 61), cu_of(new), sum(new), len(new)
+    want = call(kda, q, c, new)
+    check(want, q, c, new)
+    lib = ctypes.CDLL(build.build(debug=True))
+    lib.kda_prefix_attention.argtypes = kda.library().kda_prefix_attention.argtypes
+    lib.kda_get_device_status.argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_uint32)]
+    stream, detail, o = torch.cuda.current_stream().cuda_stream, ctypes.c_uint32(0), torch.full_like(q, -7.0)
+    size = kda.kda_prefix_attention_workspace_size(BF16, B, T, 1, 8, 2)
+    workspace = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+
+    def attend():
+        R, M = c["table"].shape
+        P = c["pool"].shape[0]
+        assert lib.kda_prefix_attention(0, B, T, max(new), 8, 2, P, 32, R, M, 1, q.data_ptr(), c["pool"].data_ptr(),
+                                        c["table"].data_ptr(), c["slot"].data_ptr(), cu.data_ptr(), c["kv_len"].data_ptr(),
+                                        c["cu_groups"].data_ptr(), c["prefix_len"].data_ptr(), 128 ** -0.5, o.data_ptr(),
+                                        workspace.data_ptr(), size, stream) == 0
+        return lib.kda_get_device_status(stream, ctypes.byref(detail))
+
+    assert lib.kda_debug_inject_prefix_timeout() == 0
+    t0 = time.perf_counter()
+    assert attend() == 5 and detail.value >= 128
+    assert time.perf_counter() - t0 < 0.5
+    assert bool((o == -7.0).all())
+    assert attend() == 0 and torch.equal(o, want)
