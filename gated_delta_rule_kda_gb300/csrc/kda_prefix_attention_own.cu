@@ -37,7 +37,9 @@ struct Params {
     CUtensorMap tm_edge;  // of 16 rows
     PrefixAttentionArgs a;
     PrefixCut cut;
-    int32_t G, kv_rows, page_shift, chunks;
+    int32_t G, kv_rows, page_shift;
+    int32_t chunks;     // a cluster a chunk of rows (and further ones)
+    int32_t heads;      // many requests: kv heads that a CTA takes at once
     float c;  // scale log2 e, > 0
 };
 
@@ -420,12 +422,13 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_own_kernel(const __grid_co
 }
 
 // ---------------------------------------------------------------------------
-// Many requests of up to 16 rows a kv head each
+// Many requests of a few rows a kv head each
 // ---------------------------------------------------------------------------
-// Here the CTAs stay and take item after item, (request, kv head) pairs, as they get done, so that an item's beginning and end hide behind its neighbours' keys: a sixth warp takes the items,
+// Here the CTAs stay and take work, kv heads of a request, 16 rows an item, as they get done, so that an item's beginning and end hide behind its neighbours' keys: a sixth warp takes the items,
 // looks their requests up and brings q, and the fetching warp goes on to the next item's keys while the
 // consumers end the last one's.  Which CTA computes an item makes no difference to it.
 constexpr int kManyThreads = 32 * (kWarps + 2);
+constexpr int kManyRows = 64;                 // most rows of a request and kv head
 constexpr int kItems = 4;                      // in the queue
 constexpr int kQPitch = 2 * kD + 16;           // bytes: the eight rows of a fragment in distinct banks
 constexpr size_t kManyQ = kStages * kStageBytes, kManySwap = kManyQ + 16 * kQPitch;
@@ -433,9 +436,10 @@ constexpr size_t kManySmem = kManySwap + kWarps * 16 * 32 * sizeof(float) + 1024
 
 struct Item {
     int32_t first, rows;       // first token of the request; rows of the item (0: no more items)
-    int32_t h, table_row;
-    int32_t q0, from;          // indices of the request's first token and of its first own key
-    __device__ __forceinline__ Own own(int32_t G) const { return Own{from, q0, q0 + (rows - 1) / G}; }
+    int32_t row_base, h;       // its first row, kv head
+    int32_t table_row, q0;     // q0: index of the request's first token
+    int32_t from, unused;
+    __device__ __forceinline__ Own own(int32_t G) const { return Own{from, q0 + row_base / G, q0 + (row_base + rows - 1) / G}; }
 };
 struct ManyShared {
     Ring ring;
@@ -456,55 +460,53 @@ __device__ __forceinline__ bool consumers_or(bool x) {
 __device__ void take_items(const Params &p, ManyShared &sh, unsigned char *sm, uint32_t *taken) {
     const int lane = threadIdx.x & 31;
     const PrefixAttentionArgs &a = p.a;
-    const uint32_t items = (uint32_t)a.cache.batch * (uint32_t)a.num_kv_heads;
-    const auto next = [&] {
-        uint32_t t = 0;
-        if (lane == 0) t = atomicAdd(taken, 1u);
-        return __shfl_sync(0xffffffffu, t, 0);
-    };
+    const uint32_t parts = (uint32_t)(a.num_kv_heads / p.heads), units = (uint32_t)a.cache.batch * parts;
     uint32_t n = 0;  // items published
-    for (uint32_t t = next();;) {
-        Item it{};
-        const bool end = t >= items;
-        if (!end) {
-            const uint32_t b = t / (uint32_t)a.num_kv_heads;
-            it.h = (int32_t)(t - b * (uint32_t)a.num_kv_heads);
-            t = next();  // (on its way while the request is looked up)
-            const PrefixRequest req = prefix_request(a, p.cut, (int32_t)b);
-            if (!req.ok && it.h == 0 && lane == 0) record_status(a.status, KDA_ERR_DEVICE_CHECK, b);
-            if (req.n == 0) continue;
-            it.first = req.first;
-            it.rows = req.n * p.G;
-            it.table_row = req.row;
-            it.q0 = req.len - req.n;
-            it.from = req.from;
-        }
+    const auto publish = [&](const Item &it) {
         const uint32_t s = n % kItems;
-        if (n >= kItems && !wait(sh.ring, &sh.item_empty[s], (n / kItems - 1) & 1, p, 198)) return;
+        if (n >= kItems && !wait(sh.ring, &sh.item_empty[s], (n / kItems - 1) & 1, p, 198)) return false;
         if (lane == 0) {
             sh.item[s] = it;
             arrive(&sh.item_full[s]);
         }
         __syncwarp();
-        if (end) return;
-        uint4 x[8];  // rows lane / 16 + 2 i
+        return true;
+    };
+    uint32_t ticket = 0;  // (lane 0's; on its way while the last one's items are published)
+    if (lane == 0) ticket = atomicAdd(taken, 1u);
+    while (true) {
+        const uint32_t t = __shfl_sync(0xffffffffu, ticket, 0);
+        if (t >= units) break;
+        if (lane == 0) ticket = atomicAdd(taken, 1u);
+        const uint32_t b = t / parts;
+        const int32_t h0 = (int32_t)(t - b * parts) * p.heads;
+        const PrefixRequest req = prefix_request(a, p.cut, (int32_t)b);
+        if (!req.ok && h0 == 0 && lane == 0) record_status(a.status, KDA_ERR_DEVICE_CHECK, b);
+        const int32_t num_rows = req.n * p.G;
+        for (int32_t h = h0; h < h0 + p.heads; ++h)
+            for (int32_t base = 0; base < num_rows; base += 16) {
+                const Item it{req.first, min(16, num_rows - base), base, h, req.row, req.len - req.n, req.from, 0};
+                if (!publish(it)) return;
+                uint4 x[8];  // rows lane / 16 + 2 i
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int32_t r = (lane >> 4) + 2 * i, token = r / p.G;
-            x[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < it.rows)
-                x[i] = *reinterpret_cast<const uint4 *>(
-                    static_cast<const __nv_bfloat16 *>(a.q) +
-                    ((int64_t)(it.first + token) * a.num_q_heads + it.h * p.G + r - token * p.G) * kD + 8 * (lane & 15));
-        }
-        if (n > 0 && !wait(sh.ring, &sh.q_empty, (n - 1) & 1, p, 199)) return;
+                for (int i = 0; i < 8; ++i) {
+                    const int32_t r = (lane >> 4) + 2 * i, token = (base + r) / p.G;
+                    x[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < it.rows)
+                        x[i] = *reinterpret_cast<const uint4 *>(
+                            static_cast<const __nv_bfloat16 *>(a.q) +
+                            ((int64_t)(req.first + token) * a.num_q_heads + h * p.G + base + r - token * p.G) * kD + 8 * (lane & 15));
+                }
+                if (n > 0 && !wait(sh.ring, &sh.q_empty, (n - 1) & 1, p, 199)) return;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4 *>(sm + kManyQ + ((lane >> 4) + 2 * i) * kQPitch + 16 * (lane & 15)) = x[i];
-        __syncwarp();
-        if (lane == 0) arrive(&sh.q_full);
-        ++n;
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint4 *>(sm + kManyQ + ((lane >> 4) + 2 * i) * kQPitch + 16 * (lane & 15)) = x[i];
+                __syncwarp();
+                if (lane == 0) arrive(&sh.q_full);
+                ++n;
+            }
     }
+    publish(Item{});
 }
 
 __global__ void __launch_bounds__(kManyThreads, 2) prefix_own_many_kernel(const __grid_constant__ Params p) {
@@ -571,7 +573,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) prefix_own_many_kernel(const 
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int32_t r = (lane >> 2) + 8 * u;
-                w.pos[u] = r < it.rows ? it.q0 + r / G : -1;
+                w.pos[u] = r < it.rows ? it.q0 + (it.row_base + r) / G : -1;
             }
             for (int32_t i = own.from / kTile; i <= own.last / kTile; ++i, ++tiles) {
                 const int32_t st = tiles % kStages;
@@ -588,14 +590,14 @@ __global__ void __launch_bounds__(kManyThreads, 2) prefix_own_many_kernel(const 
             }
             if (consumers_or(attn_given_up(&sh.ring.abort))) break;  // (the rows have no result)
             const auto place = [&](int32_t r) {  // row r of the item, as a row of [T][Hq]
-                const int32_t token = r / G;
-                return (int64_t)(it.first + token) * a.num_q_heads + it.h * G + (r - token * G);
+                const int32_t row = it.row_base + r, token = row / G;
+                return (int64_t)(it.first + token) * a.num_q_heads + it.h * G + (row - token * G);
             };
             if (consumers_or(w.bad != 0)) {
                 for (int32_t r = warp; r < it.rows; r += kWarps) {
                     float4 acc;
                     const int64_t at = place(r);
-                    const float2 x = own_row(p, at, it.h, it.table_row, own, it.q0 + r / G, acc);
+                    const float2 x = own_row(p, at, it.h, it.table_row, own, it.q0 + (it.row_base + r) / G, acc);
                     store4(space.own_o + at * kD + 4 * lane, acc);
                     if (lane == 0) space.own[at] = make_float4(x.x, x.y, it.from > 0, 0.f);
                 }
@@ -700,8 +702,10 @@ cudaError_t launch_prefix_own(const PrefixAttentionArgs &a, const PrefixCut &cut
     int splits = 1;
     while (splits < kMaxSplits && ctas * splits <= device_sm_count() && tiles >= 4 * splits) splits *= 2;
     if (splits * B * p.chunks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    const int64_t most_ctas = 2 * device_sm_count();
-    if (rows == 16 && splits == 1 && ctas > most_ctas && ctas <= 0x7fffffff) {
+    const int64_t most_ctas = 2 * device_sm_count(), items = B * a.num_kv_heads;
+    if (most <= kManyRows && splits == 1 && items > most_ctas && items < 0x7fffffff) {
+        p.heads = 1;
+        while (a.num_kv_heads % (2 * p.heads) == 0 && items >= 2 * p.heads * 8 * most_ctas) p.heads *= 2;
         const cudaError_t e = allow_smem(prefix_own_many_kernel, kManySmem);
         return e == cudaSuccess ? launch_serial(prefix_own_many_kernel, dim3((unsigned)most_ctas), kManyThreads, kManySmem, stream, p) : e;
     }
