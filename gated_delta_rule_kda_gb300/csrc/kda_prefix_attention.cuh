@@ -30,9 +30,9 @@ struct PrefixCut {
     int32_t width;
     float tile_us;      // what a key tile takes a CTA
 };
-constexpr int32_t kPrefixExtra = 2;
+constexpr int32_t kPrefixExtra = 3;
 // What an own key of a kv head, and a request and kv head, take of an SM: 512 bytes at some 75 GB/s.
-constexpr float kOwnKeyUs = 512.f / 75e3f, kOwnItemUs = 2.f;
+constexpr float kOwnKeyUs = 512.f / 75e3f, kOwnItemUs = 2.f, kOwnShortUs = 1.f;  // (short: below 48 keys on average)
 
 // Group g, checked; items = 0 when there is nothing to do for it (ok: whether it is well formed).
 struct PrefixGroup {
@@ -227,9 +227,9 @@ __device__ void prefix_make_plan(const PrefixAttentionArgs &a, const PrefixCut &
             // The own keys' launch gets the SMs that its work asks for.  Every team has a unit, so that the parts of an
             // item lie in neighbouring runs.
             const float work = (float)all * (float)cut.width * cut.tile_us;
-            const float own_work = (kOwnKeyUs * (float)max(own_keys, (int64_t)0) + kOwnItemUs * (float)B) * (float)Hkv;
+            const float own_work = (kOwnKeyUs * (float)max(own_keys, (int64_t)0) + (own_keys < 48ll * B ? kOwnShortUs : kOwnItemUs) * (float)B) * (float)Hkv;
             int32_t teams = (int32_t)((float)cut.ctas * work / (work + own_work) / (float)cut.width + 0.5f);
-            teams = max(1, min(teams, cut.ctas / cut.width));
+            teams = max(cut.ctas / (8 * cut.width), min(teams, cut.ctas / cut.width));
             run.teams = teams = (int32_t)min((int64_t)teams, all);
             run.all = all;
             run.width = cut.width;

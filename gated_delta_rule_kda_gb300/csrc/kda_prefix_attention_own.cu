@@ -75,41 +75,45 @@ __device__ __forceinline__ void load_once(uint32_t dst, const void *tmap, int y,
         : "memory");
 }
 
-// Fetches tiles [from, to) (numbers of 64-key tiles of the row): whole pages (up to a tile), except that of a
-// tile on an edge only the groups of 16 keys come that some row sees.  n: tiles that went through the ring.
+// Fetches a tile, keys [j0, j0 + 64): whole pages (up to a tile), except that on an edge (j0 a multiple of 16, else
+// of 64) only the groups of 16 keys come that some row sees.  n: tiles that went through the ring.
 __device__ __forceinline__ bool produce(const Params &p, Ring &sh, unsigned char *sm, int32_t row, const Own &own, int32_t h,
-                                        int32_t from, int32_t to, uint32_t &n) {
+                                        int32_t j0, bool edge, uint32_t &n) {
     const int lane = threadIdx.x & 31;
     const PrefixAttentionArgs &a = p.a;
-    const int32_t page_shift = p.page_shift;
+    const int32_t page_shift = p.page_shift, s = n % kStages;
     uint64_t policy;
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
-    for (int32_t i = from; i < to; ++i, ++n) {
-        const int32_t s = n % kStages, j0 = i * kTile;
-        const bool edge = own.some_hidden(j0, kTile);
-        // lane b: box b of the tile
-        const int32_t shift = edge ? 4 : min(page_shift, 6);
-        const bool mine = lane << shift < kTile;
-        const int32_t j = mine ? j0 + (lane << shift) : j0;
-        int32_t id = -1;
-        if (mine && (!edge || (j <= own.last && j + 15 >= own.from))) id = attn_page(a.cache, row, own.last, j >> page_shift);
-        const uint32_t exist = __ballot_sync(0xffffffffu, id >= 0);
-        if (n >= kStages && !wait(sh, &sh.empty[s], (n / kStages - 1) & 1, p, 196)) return false;
-        if (lane == 0) {
-            // a bit for 16 keys
-            const uint32_t bits = shift == 4   ? exist
-                                  : shift == 5 ? (exist & 1) * 3 + (exist & 2) * 6
-                                               : exist * 15;
-            sh.tile[s] = make_int2(j0, (int)(bits | (uint32_t)shift << 8));
-            mbar_arrive_expect_tx(&sh.full[s], kStageBytes);
-        }
-        __syncwarp();
-        if (mine) {
-            const int32_t y = id < 0 ? p.kv_rows  // out of range: zeros
-                                     : ((id * 2 * a.num_kv_heads + h) << page_shift) + (j & ((1 << page_shift) - 1));
-            load_once(smem_u32(sm + s * kStageBytes + (lane << (shift + 9))), edge ? &p.tm_edge : &p.tm_kv, y, &sh.full[s], policy);
-        }
+    // lane b: box b of the tile
+    const int32_t shift = edge ? 4 : min(page_shift, 6);
+    const bool mine = lane << shift < kTile;
+    const int32_t j = mine ? j0 + (lane << shift) : j0;
+    int32_t id = -1;
+    if (mine && (!edge || (j <= own.last && j + 15 >= own.from))) id = attn_page(a.cache, row, own.last, j >> page_shift);
+    const uint32_t exist = __ballot_sync(0xffffffffu, id >= 0);
+    if (n >= kStages && !wait(sh, &sh.empty[s], (n / kStages - 1) & 1, p, 196)) return false;
+    if (lane == 0) {
+        // a bit for 16 keys
+        const uint32_t bits = shift == 4   ? exist
+                              : shift == 5 ? (exist & 1) * 3 + (exist & 2) * 6
+                                           : exist * 15;
+        sh.tile[s] = make_int2(j0, (int)(bits | (uint32_t)shift << 8));
+        mbar_arrive_expect_tx(&sh.full[s], kStageBytes);
     }
+    __syncwarp();
+    if (mine) {
+        const int32_t y = id < 0 ? p.kv_rows  // out of range: zeros
+                                 : ((id * 2 * a.num_kv_heads + h) << page_shift) + (j & ((1 << page_shift) - 1));
+        load_once(smem_u32(sm + s * kStageBytes + (lane << (shift + 9))), edge ? &p.tm_edge : &p.tm_kv, y, &sh.full[s], policy);
+    }
+    ++n;
+    return true;
+}
+// Tiles [from, to) (numbers of 64-key tiles of the row).
+__device__ __forceinline__ bool produce(const Params &p, Ring &sh, unsigned char *sm, int32_t row, const Own &own, int32_t h,
+                                        int32_t from, int32_t to, uint32_t &n) {
+    for (int32_t i = from; i < to; ++i)
+        if (!produce(p, sh, sm, row, own, h, i * kTile, own.some_hidden(i * kTile, kTile), n)) return false;
     return true;
 }
 // Whichever warp gives up, the copies in flight (of tiles before n, from n0 on) land before the CTA leaves.
@@ -163,7 +167,27 @@ struct Rows {
     }
 };
 
-// A warp's share of the tile in stage s.
+// q of rows row0 .. row0 + 15 (of num_rows) of a request and kv head.
+__device__ __forceinline__ void load_q(const PrefixAttentionArgs &a, int32_t G, int32_t first, int32_t h, int32_t row0,
+                                       int32_t num_rows, int32_t q0, Rows &w) {
+    const int lane = threadIdx.x & 31;
+    const __nv_bfloat16 *base = static_cast<const __nv_bfloat16 *>(a.q) + 2 * (lane & 3);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int32_t row = row0 + (lane >> 2) + 8 * u, token = row / G;
+        const bool live = row < num_rows;
+        w.pos[u] = live ? q0 + token : -1;
+        const __nv_bfloat16 *src = base + ((int64_t)(first + (live ? token : 0)) * a.num_q_heads + h * G + (live ? row % G : 0)) * kD;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            w.q[s][u] = live ? *reinterpret_cast<const uint32_t *>(src + 16 * s) : 0u;
+            w.q[s][2 + u] = live ? *reinterpret_cast<const uint32_t *>(src + 16 * s + 8) : 0u;
+        }
+    }
+}
+
+// A warp's share of the tile in stage s: all of it (kBlocks = kWarps; then steps that no row sees are passed over), or
+// every key group of kWarps / kBlocks.
 template <int kBlocks>
 __device__ __forceinline__ void consume(const Params &p, const Ring &ring, unsigned char *sm, int32_t s, const Own &own, Rows &w) {
     constexpr uint32_t kAll = 0xffffffffu;
@@ -179,9 +203,10 @@ __device__ __forceinline__ void consume(const Params &p, const Ring &ring, unsig
     // some row must not see some key of the tile
     const bool masked = (info.y & 15) != 15 || own.some_hidden(j0, kTile);
     const uint32_t stage = smem_u32(sm + s * kStageBytes), shift = info.y >> 8, half_bytes = 128u << shift;
-#pragma unroll
+#pragma unroll (kBlocks == kWarps ? 1 : kSteps)
     for (int step = 0; step < kSteps; ++step) {
         const int key0 = 16 * (group * kSteps + step);  // of the tile
+        if (kBlocks == kWarps && (j0 + key0 > own.last || j0 + key0 + 15 < own.from)) continue;
         // its box, and its place in it
         const uint32_t k_addr = stage + ((key0 >> shift) << (shift + 9)) + ((key0 & ((1 << shift) - 1)) << 7);
         const uint32_t v_addr = k_addr + 2 * half_bytes;
@@ -315,26 +340,10 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_own_kernel(const __grid_co
             if (!attn_withhold(a)) produce(p, sh.ring, sm, req.row, own, h, from, to, n);
             drain(sh.ring, n0, n);
         } else {
-            const int block = warp % kBlocks, group = warp / kBlocks;
-            // this thread's two rows: 16 block + lane / 4 (+ 8)
-            const int32_t row0 = 16 * block + (lane >> 2);
+            const int block = warp % kBlocks;
             Rows w;
             w.clear();
-            {
-                const __nv_bfloat16 *base = static_cast<const __nv_bfloat16 *>(a.q) + 2 * (lane & 3);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int32_t row = row_base + row0 + 8 * u, token = row / G;
-                    const bool live = row < num_rows;
-                    w.pos[u] = live ? q0 + token : -1;
-                    const __nv_bfloat16 *src = base + ((int64_t)(req.first + (live ? token : 0)) * a.num_q_heads + h * G + (live ? row % G : 0)) * kD;
-#pragma unroll
-                    for (int s = 0; s < 8; ++s) {
-                        w.q[s][u] = live ? *reinterpret_cast<const uint32_t *>(src + 16 * s) : 0u;
-                        w.q[s][2 + u] = live ? *reinterpret_cast<const uint32_t *>(src + 16 * s + 8) : 0u;
-                    }
-                }
-            }
+            load_q(a, G, req.first, h, row_base + 16 * block, num_rows, q0, w);
             uint32_t n = n0;
             for (int32_t i = from; i < to; ++i, ++n) {
                 const int32_t s = n % kStages;
@@ -424,22 +433,27 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_own_kernel(const __grid_co
 // ---------------------------------------------------------------------------
 // Many requests of a few rows a kv head each
 // ---------------------------------------------------------------------------
-// Here the CTAs stay and take work, kv heads of a request, 16 rows an item, as they get done, so that an item's beginning and end hide behind its neighbours' keys: a sixth warp takes the items,
+// Here the CTAs stay and take work, kv heads of a request, as they get done, so that an item's beginning and end hide behind its neighbours' keys: a sixth warp takes the items,
 // looks their requests up and brings q, and the fetching warp goes on to the next item's keys while the
 // consumers end the last one's.  Which CTA computes an item makes no difference to it.
 constexpr int kManyThreads = 32 * (kWarps + 2);
-constexpr int kManyRows = 64;                 // most rows of a request and kv head
+constexpr int kManyRows = 16 * kWarps;        // most of a request and kv head
 constexpr int kItems = 4;                      // in the queue
 constexpr int kQPitch = 2 * kD + 16;           // bytes: the eight rows of a fragment in distinct banks
 constexpr size_t kManyQ = kStages * kStageBytes, kManySwap = kManyQ + 16 * kQPitch;
 constexpr size_t kManySmem = kManySwap + kWarps * 16 * 32 * sizeof(float) + 1024;
 
 struct Item {
-    int32_t first, rows;       // first token of the request; rows of the item (0: no more items)
-    int32_t row_base, h;       // its first row, kv head
-    int32_t table_row, q0;     // q0: index of the request's first token
-    int32_t from, unused;
-    __device__ __forceinline__ Own own(int32_t G) const { return Own{from, q0 + row_base / G, q0 + (row_base + rows - 1) / G}; }
+    int32_t first, rows;       // first token and rows of the request (0: no more items)
+    int32_t table_row, q0;     // q0: index of the first token
+    int32_t from, h;           // first own key, kv head
+    int32_t heads;             // 0: the four warps share the keys of a block of 16 rows, or two and two those of two blocks
+                               // else: a warp a block of 16 rows of kv heads h .., and all keys
+    int32_t short_keys;        // all own keys are in one tile, from key() on
+    __device__ __forceinline__ Own own(int32_t G) const { return Own{from, q0, q0 + (rows - 1) / G}; }
+    __device__ __forceinline__ int32_t key() const { return from & ~15; }
+    __device__ __forceinline__ int32_t tile0() const { return from / kTile; }
+    __device__ __forceinline__ int32_t tiles(const Own &o) const { return short_keys ? heads : o.last / kTile + 1 - tile0(); }
 };
 struct ManyShared {
     Ring ring;
@@ -447,6 +461,26 @@ struct ManyShared {
     Item item[kItems];
     float2 ml[kWarps][16];
 };
+
+// Row r of a kv head of a request whose first token is `first`, as a row of [T][Hq].
+__device__ __forceinline__ int64_t place(const Params &p, int32_t first, int32_t h, int32_t r) {
+    const int32_t token = r / p.G;
+    return (int64_t)(first + token) * p.a.num_q_heads + h * p.G + (r - token * p.G);
+}
+
+// Rows r0, r0 + step .. below r1 of a kv head by own_row.
+__device__ __forceinline__ void own_rows(const Params &p, const Item &it, int32_t h, const Own &own, int32_t r0, int32_t r1,
+                                         int32_t step) {
+    const int lane = threadIdx.x & 31;
+    const PrefixSpace space = prefix_space(p.a);
+    for (int32_t r = r0; r < r1; r += step) {
+        float4 acc;
+        const int64_t at = place(p, it.first, h, r);
+        const float2 x = own_row(p, at, h, it.table_row, own, it.q0 + r / p.G, acc);
+        store4(space.own_o + at * kD + 4 * lane, acc);
+        if (lane == 0) space.own[at] = make_float4(x.x, x.y, it.from > 0, 0.f);
+    }
+}
 
 // Barrier 1 of the four consumer warps; whether any thread says x.
 __device__ __forceinline__ bool consumers_or(bool x) {
@@ -461,7 +495,7 @@ __device__ void take_items(const Params &p, ManyShared &sh, unsigned char *sm, u
     const int lane = threadIdx.x & 31;
     const PrefixAttentionArgs &a = p.a;
     const uint32_t parts = (uint32_t)(a.num_kv_heads / p.heads), units = (uint32_t)a.cache.batch * parts;
-    uint32_t n = 0;  // items published
+    uint32_t n = 0, with_q = 0;  // items published; those of one head
     const auto publish = [&](const Item &it) {
         const uint32_t s = n % kItems;
         if (n >= kItems && !wait(sh.ring, &sh.item_empty[s], (n / kItems - 1) & 1, p, 198)) return false;
@@ -470,6 +504,7 @@ __device__ void take_items(const Params &p, ManyShared &sh, unsigned char *sm, u
             arrive(&sh.item_full[s]);
         }
         __syncwarp();
+        ++n;
         return true;
     };
     uint32_t ticket = 0;  // (lane 0's; on its way while the last one's items are published)
@@ -483,30 +518,119 @@ __device__ void take_items(const Params &p, ManyShared &sh, unsigned char *sm, u
         const PrefixRequest req = prefix_request(a, p.cut, (int32_t)b);
         if (!req.ok && h0 == 0 && lane == 0) record_status(a.status, KDA_ERR_DEVICE_CHECK, b);
         const int32_t num_rows = req.n * p.G;
-        for (int32_t h = h0; h < h0 + p.heads; ++h)
-            for (int32_t base = 0; base < num_rows; base += 16) {
-                const Item it{req.first, min(16, num_rows - base), base, h, req.row, req.len - req.n, req.from, 0};
-                if (!publish(it)) return;
-                uint4 x[8];  // rows lane / 16 + 2 i
+        if (num_rows == 0) continue;
+        Item it{req.first, num_rows, req.row, req.len - req.n, req.from, 0, 0, 0};
+        const int32_t blocks = (num_rows + 15) / 16;
+        it.short_keys = p.heads * blocks > 1 && req.len - it.key() <= kTile;
+        const int32_t each = it.short_keys ? kWarps / blocks : 1;  // heads of an item
+        for (int32_t h = h0; h < h0 + p.heads; h += each) {
+            it.h = h;
+            it.heads = it.short_keys || blocks > 2 ? min(each, h0 + p.heads - h) : 0;
+            if (!publish(it)) return;
+            if (it.heads > 0 || blocks > 1) continue;
+            uint4 x[8];  // rows lane / 16 + 2 i
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int32_t r = (lane >> 4) + 2 * i, token = (base + r) / p.G;
-                    x[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < it.rows)
-                        x[i] = *reinterpret_cast<const uint4 *>(
-                            static_cast<const __nv_bfloat16 *>(a.q) +
-                            ((int64_t)(req.first + token) * a.num_q_heads + h * p.G + base + r - token * p.G) * kD + 8 * (lane & 15));
-                }
-                if (n > 0 && !wait(sh.ring, &sh.q_empty, (n - 1) & 1, p, 199)) return;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    *reinterpret_cast<uint4 *>(sm + kManyQ + ((lane >> 4) + 2 * i) * kQPitch + 16 * (lane & 15)) = x[i];
-                __syncwarp();
-                if (lane == 0) arrive(&sh.q_full);
-                ++n;
+            for (int i = 0; i < 8; ++i) {
+                const int32_t r = (lane >> 4) + 2 * i, token = r / p.G;
+                x[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < num_rows)
+                    x[i] = *reinterpret_cast<const uint4 *>(
+                        static_cast<const __nv_bfloat16 *>(a.q) +
+                        ((int64_t)(req.first + token) * a.num_q_heads + h * p.G + r - token * p.G) * kD + 8 * (lane & 15));
             }
+            if (with_q > 0 && !wait(sh.ring, &sh.q_empty, (with_q - 1) & 1, p, 199)) return;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4 *>(sm + kManyQ + ((lane >> 4) + 2 * i) * kQPitch + 16 * (lane & 15)) = x[i];
+            __syncwarp();
+            if (lane == 0) arrive(&sh.q_full);
+            ++with_q;
+        }
     }
     publish(Item{});
+}
+
+// An item of two blocks of rows: consumer warps b and b + 2 share the keys of block b.  False: a wait gave up.
+__device__ __forceinline__ bool two_blocks(const Params &p, ManyShared &sh, unsigned char *sm, const Item &it, uint32_t &tiles,
+                                           Rows &w) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp >> 1;
+    const int32_t r0 = 16 * (warp & 1);
+    const PrefixSpace space = prefix_space(p.a);
+    const Own own = it.own(p.G);
+    w.clear();
+    load_q(p.a, p.G, it.first, it.h, r0, it.rows, it.q0, w);
+    const int32_t count = it.tiles(own);
+    for (int32_t i = 0; i < count; ++i, ++tiles) {
+        const int32_t st = tiles % kStages;
+        if (!wait(sh.ring, &sh.ring.full[st], (tiles / kStages) & 1, p, 205)) break;
+        consume<2>(p, sh.ring, sm, st, own, w);
+        __syncwarp();
+        if (lane == 0) arrive(&sh.ring.empty[st]);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        w.l[u] += __shfl_xor_sync(0xffffffffu, w.l[u], 1);
+        w.l[u] += __shfl_xor_sync(0xffffffffu, w.l[u], 2);
+        if ((lane & 3) == 0) sh.ml[warp][(lane >> 2) + 8 * u] = make_float2(w.m[u], w.l[u]);
+    }
+    if (consumers_or(attn_given_up(&sh.ring.abort))) return false;
+    if (consumers_or(w.bad != 0)) {
+        own_rows(p, it, it.h, own, warp, it.rows, kWarps);
+        return true;
+    }
+    float top[2], sum[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const float2 x = sh.ml[warp & 1][(lane >> 2) + 8 * u], y = sh.ml[warp | 2][(lane >> 2) + 8 * u];
+        top[u] = fmaxf(x.x, y.x);
+        const auto weight = [&](float mx, float lx) {  // (a NaN sum stays one)
+            return mx == -INFINITY ? (lx == 0.f ? 0.f : 1.f) : ex2_approx((mx - top[u]) * p.c);
+        };
+        sum[u] = fmaf(weight(y.x, y.y), y.y, weight(x.x, x.y) * x.y);
+        const float mine = weight(w.m[u], w.l[u]);
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            w.o[t][2 * u] *= mine;
+            w.o[t][2 * u + 1] *= mine;
+        }
+    }
+    // Each keeps half of the channels and gets the other's share of them, a quarter at a time.
+    float4 *swap = reinterpret_cast<float4 *>(sm + kManySwap) + lane;  // [sender][4][lane]
+#pragma unroll
+    for (int turn = 0; turn < 2; ++turn) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int a = 4 * turn + t, b = 8 + a;  // group 1's gift, group 0's
+            swap[(warp * 4 + t) * 32] = group ? make_float4(w.o[a][0], w.o[a][1], w.o[a][2], w.o[a][3])
+                                              : make_float4(w.o[b][0], w.o[b][1], w.o[b][2], w.o[b][3]);
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const float4 x = swap[((warp ^ 2) * 4 + t) * 32];
+            const int a = 4 * turn + t, b = 8 + a;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float y = e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w;
+                if (group) w.o[b][e] += y;
+                else w.o[a][e] += y;
+            }
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int32_t r = r0 + (lane >> 2) + 8 * u;
+        if (r >= it.rows) continue;
+        const int64_t at = place(p, it.first, it.h, r);
+        float *o = space.own_o + at * kD + 64 * group + 2 * (lane & 3);
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+            *reinterpret_cast<float2 *>(o + 8 * t) = group ? make_float2(w.o[8 + t][2 * u], w.o[8 + t][2 * u + 1])
+                                                           : make_float2(w.o[t][2 * u], w.o[t][2 * u + 1]);
+        if (group == 0 && (lane & 3) == 0) space.own[at] = make_float4(top[u], sum[u], it.from > 0, 0.f);
+    }
+    return true;
 }
 
 __global__ void __launch_bounds__(kManyThreads, 2) prefix_own_many_kernel(const __grid_constant__ Params p) {
@@ -547,11 +671,18 @@ __global__ void __launch_bounds__(kManyThreads, 2) prefix_own_many_kernel(const 
             if (lane == 0) arrive(&sh.item_empty[s]);
             if (it.rows == 0) break;
             const Own own = it.own(G);
-            if (!produce(p, sh.ring, sm, it.table_row, own, it.h, own.from / kTile, own.last / kTile + 1, tiles)) break;
+            const int32_t count = it.tiles(own);
+            bool ok = true;
+            for (int32_t i = 0; ok && i < count; ++i) {
+                const int32_t j0 = it.short_keys ? it.key() : (it.tile0() + i) * kTile;
+                ok = produce(p, sh.ring, sm, it.table_row, own, it.short_keys ? it.h + i : it.h, j0,
+                             it.short_keys || own.some_hidden(j0, kTile), tiles);
+            }
+            if (!ok) break;
         }
         drain(sh.ring, 0, tiles);
     } else {
-        uint32_t tiles = 0;
+        uint32_t tiles = 0, with_q = 0;
         Rows w;
         for (uint32_t n = 0;; ++n) {
             const uint32_t s = n % kItems;
@@ -559,7 +690,47 @@ __global__ void __launch_bounds__(kManyThreads, 2) prefix_own_many_kernel(const 
             const Item it = sh.item[s];
             __syncwarp();
             if (lane == 0) arrive(&sh.item_empty[s]);
-            if (got && it.rows > 0) got = wait(sh.ring, &sh.q_full, n & 1, p, 202);
+            if (it.heads > 0) {
+                // Everyone waits for every tile and frees it, so that none falls behind the ring.
+                const Own own = it.own(G);
+                const int32_t blocks = (it.rows + 15) / 16, head = warp / blocks, h = it.h + head;
+                const int32_t r0 = 16 * (warp - head * blocks), r1 = min(r0 + 16, it.rows), count = it.tiles(own);
+                const bool mine = got && head < it.heads;
+                w.clear();
+                if (mine) load_q(a, G, it.first, h, r0, it.rows, it.q0, w);
+                for (int32_t i = 0; got && i < count; ++i, ++tiles) {
+                    const int32_t st = tiles % kStages;
+                    if (!(got = wait(sh.ring, &sh.ring.full[st], (tiles / kStages) & 1, p, 204))) break;
+                    if (mine && (!it.short_keys || i == head)) consume<kWarps>(p, sh.ring, sm, st, own, w);
+                    __syncwarp();
+                    if (lane == 0) arrive(&sh.ring.empty[st]);
+                }
+                if (consumers_or(!got)) break;
+                if (!mine) continue;
+                if (__any_sync(kAll, w.bad != 0)) {
+                    own_rows(p, it, h, own, r0, r1, 1);
+                    continue;
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    w.l[u] += __shfl_xor_sync(kAll, w.l[u], 1);
+                    w.l[u] += __shfl_xor_sync(kAll, w.l[u], 2);
+                    const int32_t r = r0 + (lane >> 2) + 8 * u;
+                    if (r >= r1) continue;
+                    const int64_t at = place(p, it.first, h, r);
+                    float *o = space.own_o + at * kD + 2 * (lane & 3);
+#pragma unroll
+                    for (int t = 0; t < 16; ++t) *reinterpret_cast<float2 *>(o + 8 * t) = make_float2(w.o[t][2 * u], w.o[t][2 * u + 1]);
+                    if ((lane & 3) == 0) space.own[at] = make_float4(w.m[u], w.l[u], it.from > 0, 0.f);
+                }
+                continue;
+            }
+            if (it.rows > 16) {
+                if (consumers_or(!got)) break;
+                if (!two_blocks(p, sh, sm, it, tiles, w)) break;
+                continue;
+            }
+            if (got && it.rows > 0) got = wait(sh.ring, &sh.q_full, with_q++ & 1, p, 202);
             if (consumers_or(!got) || it.rows == 0) break;  // all four or none
             {
                 const uint32_t at = smem_u32(sm) + (uint32_t)kManyQ + (lane & 15) * kQPitch + 16 * (lane >> 4);
@@ -573,7 +744,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) prefix_own_many_kernel(const 
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int32_t r = (lane >> 2) + 8 * u;
-                w.pos[u] = r < it.rows ? it.q0 + (it.row_base + r) / G : -1;
+                w.pos[u] = r < it.rows ? it.q0 + r / G : -1;
             }
             for (int32_t i = own.from / kTile; i <= own.last / kTile; ++i, ++tiles) {
                 const int32_t st = tiles % kStages;
@@ -589,18 +760,8 @@ __global__ void __launch_bounds__(kManyThreads, 2) prefix_own_many_kernel(const 
                 if ((lane & 3) == 0) sh.ml[warp][(lane >> 2) + 8 * u] = make_float2(w.m[u], w.l[u]);
             }
             if (consumers_or(attn_given_up(&sh.ring.abort))) break;  // (the rows have no result)
-            const auto place = [&](int32_t r) {  // row r of the item, as a row of [T][Hq]
-                const int32_t row = it.row_base + r, token = row / G;
-                return (int64_t)(it.first + token) * a.num_q_heads + it.h * G + (row - token * G);
-            };
             if (consumers_or(w.bad != 0)) {
-                for (int32_t r = warp; r < it.rows; r += kWarps) {
-                    float4 acc;
-                    const int64_t at = place(r);
-                    const float2 x = own_row(p, at, it.h, it.table_row, own, it.q0 + (it.row_base + r) / G, acc);
-                    store4(space.own_o + at * kD + 4 * lane, acc);
-                    if (lane == 0) space.own[at] = make_float4(x.x, x.y, it.from > 0, 0.f);
-                }
+                own_rows(p, it, it.h, own, warp, it.rows, kWarps);
                 continue;
             }
             // The warps' shares joined: warp w gets channels 32 w .. of every row from the other three, one after
@@ -656,7 +817,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) prefix_own_many_kernel(const 
             for (int u = 0; u < 2; ++u) {
                 const int32_t r = (lane >> 2) + 8 * u;
                 if (r >= it.rows) continue;
-                const int64_t at = place(r);
+                const int64_t at = place(p, it.first, it.h, r);
                 float *o = space.own_o + at * kD + 32 * warp + 2 * (lane & 3);
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
@@ -705,7 +866,7 @@ cudaError_t launch_prefix_own(const PrefixAttentionArgs &a, const PrefixCut &cut
     const int64_t most_ctas = 2 * device_sm_count(), items = B * a.num_kv_heads;
     if (most <= kManyRows && splits == 1 && items > most_ctas && items < 0x7fffffff) {
         p.heads = 1;
-        while (a.num_kv_heads % (2 * p.heads) == 0 && items >= 2 * p.heads * 8 * most_ctas) p.heads *= 2;
+        while (a.num_kv_heads % (2 * p.heads) == 0 && items >= 2 * p.heads * 4 * most_ctas) p.heads *= 2;
         const cudaError_t e = allow_smem(prefix_own_many_kernel, kManySmem);
         return e == cudaSuccess ? launch_serial(prefix_own_many_kernel, dim3((unsigned)most_ctas), kManyThreads, kManySmem, stream, p) : e;
     }

@@ -92,7 +92,8 @@ def test_many_groups(kda):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
-@pytest.mark.parametrize("shape", [(7, 8, 4, 64, 4), (70, 8, 5, 16, 3), (43, 40, 1, 32, 16), (330, 1, 16, 128, 1)])
+@pytest.mark.parametrize("shape", [(7, 8, 4, 64, 4), (70, 8, 5, 16, 3), (43, 40, 1, 32, 16), (330, 1, 16, 128, 1),
+                                   (90, 4, 6, 16, 4), (90, 4, 8, 64, 7), (330, 8, 4, 32, 2), (330, 8, 5, 32, 7)])
 def test_many_requests(kda, shape, dtype):
     """More (request, kv head) pairs than CTAs fit on the GPU: requests of all lengths and numbers of tokens (also
     none), one of them refused, and values that are not finite in the step's own tokens and where nothing is."""
