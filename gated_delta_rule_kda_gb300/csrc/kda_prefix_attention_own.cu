@@ -491,6 +491,7 @@ __device__ __forceinline__ bool consumers_or(bool x) {
 }
 
 // The sixth warp.
+template <int kRowBlocks, bool kShort>
 __device__ void take_items(const Params &p, ManyShared &sh, unsigned char *sm, uint32_t *taken) {
     const int lane = threadIdx.x & 31;
     const PrefixAttentionArgs &a = p.a;
@@ -521,13 +522,13 @@ __device__ void take_items(const Params &p, ManyShared &sh, unsigned char *sm, u
         if (num_rows == 0) continue;
         Item it{req.first, num_rows, req.row, req.len - req.n, req.from, 0, 0, 0};
         const int32_t blocks = (num_rows + 15) / 16;
-        it.short_keys = p.heads * blocks > 1 && req.len - it.key() <= kTile;
+        it.short_keys = kShort && p.heads * blocks > 1 && req.len - it.key() <= kTile;
         const int32_t each = it.short_keys ? kWarps / blocks : 1;  // heads of an item
         for (int32_t h = h0; h < h0 + p.heads; h += each) {
             it.h = h;
-            it.heads = it.short_keys || blocks > 2 ? min(each, h0 + p.heads - h) : 0;
+            it.heads = it.short_keys ? min(each, h0 + p.heads - h) : kRowBlocks == kWarps;
             if (!publish(it)) return;
-            if (it.heads > 0 || blocks > 1) continue;
+            if (kRowBlocks > 1 || it.heads > 0) continue;
             uint4 x[8];  // rows lane / 16 + 2 i
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -633,6 +634,110 @@ __device__ __forceinline__ bool two_blocks(const Params &p, ManyShared &sh, unsi
     return true;
 }
 
+// An item of one block of rows: the four warps share its keys.  False: a wait gave up.
+__device__ __forceinline__ bool one_block(const Params &p, ManyShared &sh, unsigned char *sm, const Item &it, uint32_t &tiles,
+                                          Rows &w) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const PrefixSpace space = prefix_space(p.a);
+    {
+        const uint32_t at = smem_u32(sm) + (uint32_t)kManyQ + (lane & 15) * kQPitch + 16 * (lane >> 4);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) ldmatrix4(at + 32 * c, w.q[c]);
+    }
+    __syncwarp();
+    if (lane == 0) arrive(&sh.q_empty);
+    w.clear();
+    const Own own = it.own(p.G);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int32_t r = (lane >> 2) + 8 * u;
+        w.pos[u] = r < it.rows ? it.q0 + r / p.G : -1;
+    }
+    for (int32_t i = own.from / kTile; i <= own.last / kTile; ++i, ++tiles) {
+        const int32_t st = tiles % kStages;
+        if (!wait(sh.ring, &sh.ring.full[st], (tiles / kStages) & 1, p, 203)) break;
+        consume<1>(p, sh.ring, sm, st, own, w);
+        __syncwarp();
+        if (lane == 0) arrive(&sh.ring.empty[st]);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        w.l[u] += __shfl_xor_sync(kAll, w.l[u], 1);
+        w.l[u] += __shfl_xor_sync(kAll, w.l[u], 2);
+        if ((lane & 3) == 0) sh.ml[warp][(lane >> 2) + 8 * u] = make_float2(w.m[u], w.l[u]);
+    }
+    if (consumers_or(attn_given_up(&sh.ring.abort))) return false;  // (the rows have no result)
+    if (consumers_or(w.bad != 0)) {
+        own_rows(p, it, it.h, own, warp, it.rows, kWarps);
+        return true;
+    }
+    // The warps' shares joined: warp w gets channels 32 w .. of every row from the other three, one after
+    // the other through 8 KB, lane to lane.
+    float top[2], sum[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        float2 ml[kWarps];
+        top[u] = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+            ml[k] = sh.ml[k][(lane >> 2) + 8 * u];
+            top[u] = fmaxf(top[u], ml[k].x);
+        }
+        const auto weight = [&](float mx, float lx) {  // (a NaN sum stays one)
+            return mx == -INFINITY ? (lx == 0.f ? 0.f : 1.f) : ex2_approx((mx - top[u]) * p.c);
+        };
+        sum[u] = 0.f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) sum[u] = fmaf(weight(ml[k].x, ml[k].y), ml[k].y, sum[u]);
+        const float mine = weight(w.m[u], w.l[u]);
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            w.o[t][2 * u] *= mine;
+            w.o[t][2 * u + 1] *= mine;
+        }
+    }
+    float4 acc[4];
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k)
+        if (k == warp)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) acc[t] = make_float4(w.o[4 * k + t][0], w.o[4 * k + t][1], w.o[4 * k + t][2], w.o[4 * k + t][3]);
+    float4 *swap = reinterpret_cast<float4 *>(sm + kManySwap) + lane;  // [receiver][4][lane]
+#pragma unroll 1
+    for (int turn = 1; turn < kWarps; ++turn) {
+        const int to = (warp + turn) % kWarps;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k)
+            if (k == to)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    swap[(k * 4 + t) * 32] = make_float4(w.o[4 * k + t][0], w.o[4 * k + t][1], w.o[4 * k + t][2], w.o[4 * k + t][3]);
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const float4 x = swap[(warp * 4 + t) * 32];
+            acc[t] = make_float4(acc[t].x + x.x, acc[t].y + x.y, acc[t].z + x.z, acc[t].w + x.w);
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int32_t r = (lane >> 2) + 8 * u;
+        if (r >= it.rows) continue;
+        const int64_t at = place(p, it.first, it.h, r);
+        float *o = space.own_o + at * kD + 32 * warp + 2 * (lane & 3);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            *reinterpret_cast<float2 *>(o + 8 * t) = u ? make_float2(acc[t].z, acc[t].w) : make_float2(acc[t].x, acc[t].y);
+        if (warp == 0 && (lane & 3) == 0) space.own[at] = make_float4(top[u], sum[u], it.from > 0, 0.f);
+    }
+    return true;
+}
+
+// Requests of up to kRowBlocks blocks; kShort: with items whose keys are all in one tile.  (Apart, since all of it
+// together costs 16 x 4 beams 92 us instead of 80: instructions to fetch, and registers that spill.)
+template <int kRowBlocks, bool kShort>
 __global__ void __launch_bounds__(kManyThreads, 2) prefix_own_many_kernel(const __grid_constant__ Params p) {
     constexpr uint32_t kAll = 0xffffffffu;
     extern __shared__ unsigned char dyn[];
@@ -660,7 +765,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) prefix_own_many_kernel(const 
     __syncthreads();
 
     if (warp == kWarps + 1) {
-        take_items(p, sh, sm, space.taken);
+        take_items<kRowBlocks, kShort>(p, sh, sm, space.taken);
     } else if (warp == kWarps) {
         uint32_t tiles = 0;
         for (uint32_t n = 0; !attn_withhold(a); ++n) {
@@ -690,7 +795,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) prefix_own_many_kernel(const 
             const Item it = sh.item[s];
             __syncwarp();
             if (lane == 0) arrive(&sh.item_empty[s]);
-            if (it.heads > 0) {
+            if ((kShort || kRowBlocks == kWarps) && it.heads > 0) {
                 // Everyone waits for every tile and frees it, so that none falls behind the ring.
                 const Own own = it.own(G);
                 const int32_t blocks = (it.rows + 15) / 16, head = warp / blocks, h = it.h + head;
@@ -725,104 +830,13 @@ __global__ void __launch_bounds__(kManyThreads, 2) prefix_own_many_kernel(const 
                 }
                 continue;
             }
-            if (it.rows > 16) {
-                if (consumers_or(!got)) break;
-                if (!two_blocks(p, sh, sm, it, tiles, w)) break;
-                continue;
-            }
-            if (got && it.rows > 0) got = wait(sh.ring, &sh.q_full, with_q++ & 1, p, 202);
+            if (kRowBlocks == 1 && got && it.rows > 0) got = wait(sh.ring, &sh.q_full, with_q++ & 1, p, 202);
             if (consumers_or(!got) || it.rows == 0) break;  // all four or none
-            {
-                const uint32_t at = smem_u32(sm) + (uint32_t)kManyQ + (lane & 15) * kQPitch + 16 * (lane >> 4);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) ldmatrix4(at + 32 * c, w.q[c]);
+            if constexpr (kRowBlocks == 2) {
+                if (!two_blocks(p, sh, sm, it, tiles, w)) break;
             }
-            __syncwarp();
-            if (lane == 0) arrive(&sh.q_empty);
-            w.clear();
-            const Own own = it.own(G);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int32_t r = (lane >> 2) + 8 * u;
-                w.pos[u] = r < it.rows ? it.q0 + r / G : -1;
-            }
-            for (int32_t i = own.from / kTile; i <= own.last / kTile; ++i, ++tiles) {
-                const int32_t st = tiles % kStages;
-                if (!wait(sh.ring, &sh.ring.full[st], (tiles / kStages) & 1, p, 203)) break;
-                consume<1>(p, sh.ring, sm, st, own, w);
-                __syncwarp();
-                if (lane == 0) arrive(&sh.ring.empty[st]);
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                w.l[u] += __shfl_xor_sync(kAll, w.l[u], 1);
-                w.l[u] += __shfl_xor_sync(kAll, w.l[u], 2);
-                if ((lane & 3) == 0) sh.ml[warp][(lane >> 2) + 8 * u] = make_float2(w.m[u], w.l[u]);
-            }
-            if (consumers_or(attn_given_up(&sh.ring.abort))) break;  // (the rows have no result)
-            if (consumers_or(w.bad != 0)) {
-                own_rows(p, it, it.h, own, warp, it.rows, kWarps);
-                continue;
-            }
-            // The warps' shares joined: warp w gets channels 32 w .. of every row from the other three, one after
-            // the other through 8 KB, lane to lane.
-            float top[2], sum[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float2 ml[kWarps];
-                top[u] = -INFINITY;
-#pragma unroll
-                for (int k = 0; k < kWarps; ++k) {
-                    ml[k] = sh.ml[k][(lane >> 2) + 8 * u];
-                    top[u] = fmaxf(top[u], ml[k].x);
-                }
-                const auto weight = [&](float mx, float lx) {  // (a NaN sum stays one)
-                    return mx == -INFINITY ? (lx == 0.f ? 0.f : 1.f) : ex2_approx((mx - top[u]) * p.c);
-                };
-                sum[u] = 0.f;
-#pragma unroll
-                for (int k = 0; k < kWarps; ++k) sum[u] = fmaf(weight(ml[k].x, ml[k].y), ml[k].y, sum[u]);
-                const float mine = weight(w.m[u], w.l[u]);
-#pragma unroll
-                for (int t = 0; t < 16; ++t) {
-                    w.o[t][2 * u] *= mine;
-                    w.o[t][2 * u + 1] *= mine;
-                }
-            }
-            float4 acc[4];
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k)
-                if (k == warp)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) acc[t] = make_float4(w.o[4 * k + t][0], w.o[4 * k + t][1], w.o[4 * k + t][2], w.o[4 * k + t][3]);
-            float4 *swap = reinterpret_cast<float4 *>(sm + kManySwap) + lane;  // [receiver][4][lane]
-#pragma unroll 1
-            for (int turn = 1; turn < kWarps; ++turn) {
-                const int to = (warp + turn) % kWarps;
-#pragma unroll
-                for (int k = 0; k < kWarps; ++k)
-                    if (k == to)
-#pragma unroll
-                        for (int t = 0; t < 4; ++t)
-                            swap[(k * 4 + t) * 32] = make_float4(w.o[4 * k + t][0], w.o[4 * k + t][1], w.o[4 * k + t][2], w.o[4 * k + t][3]);
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const float4 x = swap[(warp * 4 + t) * 32];
-                    acc[t] = make_float4(acc[t].x + x.x, acc[t].y + x.y, acc[t].z + x.z, acc[t].w + x.w);
-                }
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int32_t r = (lane >> 2) + 8 * u;
-                if (r >= it.rows) continue;
-                const int64_t at = place(p, it.first, it.h, r);
-                float *o = space.own_o + at * kD + 32 * warp + 2 * (lane & 3);
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    *reinterpret_cast<float2 *>(o + 8 * t) = u ? make_float2(acc[t].z, acc[t].w) : make_float2(acc[t].x, acc[t].y);
-                if (warp == 0 && (lane & 3) == 0) space.own[at] = make_float4(top[u], sum[u], it.from > 0, 0.f);
+            if constexpr (kRowBlocks == 1) {
+                if (!one_block(p, sh, sm, it, tiles, w)) break;
             }
         }
     }
@@ -834,6 +848,12 @@ template <int kBlocks>
 cudaError_t launch(const Params &p, int splits, cudaStream_t stream) {
     const dim3 grid((unsigned)((int64_t)splits * p.a.cache.batch * p.chunks), (unsigned)p.a.num_kv_heads);
     return launch_clusters(prefix_own_kernel<kBlocks>, grid, splits, kThreads, kSmem, stream, p);
+}
+
+template <int kRowBlocks, bool kShort>
+cudaError_t launch_many(const Params &p, unsigned ctas, cudaStream_t stream) {
+    const cudaError_t e = allow_smem(prefix_own_many_kernel<kRowBlocks, kShort>, kManySmem);
+    return e == cudaSuccess ? launch_serial(prefix_own_many_kernel<kRowBlocks, kShort>, dim3(ctas), kManyThreads, kManySmem, stream, p) : e;
 }
 
 }  // namespace
@@ -867,8 +887,10 @@ cudaError_t launch_prefix_own(const PrefixAttentionArgs &a, const PrefixCut &cut
     if (most <= kManyRows && splits == 1 && items > most_ctas && items < 0x7fffffff) {
         p.heads = 1;
         while (a.num_kv_heads % (2 * p.heads) == 0 && items >= 2 * p.heads * 4 * most_ctas) p.heads *= 2;
-        const cudaError_t e = allow_smem(prefix_own_many_kernel, kManySmem);
-        return e == cudaSuccess ? launch_serial(prefix_own_many_kernel, dim3((unsigned)most_ctas), kManyThreads, kManySmem, stream, p) : e;
+        const unsigned n = (unsigned)most_ctas;
+        if (most > 32) return launch_many<4, true>(p, n, stream);
+        if (most > 16) return launch_many<2, true>(p, n, stream);
+        return p.heads > 1 ? launch_many<1, true>(p, n, stream) : launch_many<1, false>(p, n, stream);
     }
     return rows == 16 ? launch<1>(p, splits, stream) : launch<2>(p, splits, stream);
 }
