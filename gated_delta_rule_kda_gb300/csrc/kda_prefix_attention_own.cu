@@ -881,13 +881,13 @@ cudaError_t launch_prefix_own(const PrefixAttentionArgs &a, const PrefixCut &cut
     const int64_t tiles = ((int64_t)a.cache.table_width * a.cache.page_size + kTile - 1) / kTile;
     const int64_t ctas = B * a.num_kv_heads * p.chunks;
     int splits = 1;
-    while (splits < kMaxSplits && ctas * splits <= device_sm_count() && tiles >= 4 * splits) splits *= 2;
+    while (splits < kMaxSplits && ctas * splits <= device_sm_count() / 2 && tiles >= 4 * splits) splits *= 2;
     if (splits * B * p.chunks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     const int64_t most_ctas = 2 * device_sm_count(), items = B * a.num_kv_heads;
-    if (most <= kManyRows && splits == 1 && items > most_ctas && items < 0x7fffffff) {
+    if (most <= kManyRows && splits == 1 && items > device_sm_count() && items < 0x7fffffff) {
         p.heads = 1;
         while (a.num_kv_heads % (2 * p.heads) == 0 && items >= 2 * p.heads * 4 * most_ctas) p.heads *= 2;
-        const unsigned n = (unsigned)most_ctas;
+        const unsigned n = (unsigned)(items < most_ctas ? items : most_ctas);
         if (most > 32) return launch_many<4, true>(p, n, stream);
         if (most > 16) return launch_many<2, true>(p, n, stream);
         return p.heads > 1 ? launch_many<1, true>(p, n, stream) : launch_many<1, false>(p, n, stream);
