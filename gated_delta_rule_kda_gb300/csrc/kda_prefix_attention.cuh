@@ -227,7 +227,10 @@ __device__ void prefix_make_plan(const PrefixAttentionArgs &a, const PrefixCut &
             // The own keys' launch gets the SMs that its work asks for.  Every team has a unit, so that the parts of an
             // item lie in neighbouring runs.
             const float work = (float)all * (float)cut.width * cut.tile_us;
-            const float own_work = (kOwnKeyUs * (float)max(own_keys, (int64_t)0) + (own_keys < 48ll * B ? kOwnShortUs : kOwnItemUs) * (float)B) * (float)Hkv;
+            // (twice for more than 32 rows of a request, and so on)
+            const float rows = (float)a.cache.total_tokens / (float)B * (float)(a.num_q_heads / Hkv);
+            const float own_item = own_keys < 48ll * B ? kOwnShortUs : kOwnItemUs;
+            const float own_work = (kOwnKeyUs * (float)max(own_keys, (int64_t)0) + own_item * (float)B) * (float)Hkv * fmaxf(1.f, rows / 32.f);
             int32_t teams = (int32_t)((float)cut.ctas * work / (work + own_work) / (float)cut.width + 0.5f);
             teams = max(cut.ctas / (8 * cut.width), min(teams, cut.ctas / cut.width));
             run.teams = teams = (int32_t)min((int64_t)teams, all);

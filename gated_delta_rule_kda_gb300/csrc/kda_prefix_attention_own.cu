@@ -437,23 +437,20 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_own_kernel(const __grid_co
 // looks their requests up and brings q, and the fetching warp goes on to the next item's keys while the
 // consumers end the last one's.  Which CTA computes an item makes no difference to it.
 constexpr int kManyThreads = 32 * (kWarps + 2);
-constexpr int kManyRows = 16 * kWarps;        // most of a request and kv head
 constexpr int kItems = 4;                      // in the queue
 constexpr int kQPitch = 2 * kD + 16;           // bytes: the eight rows of a fragment in distinct banks
 constexpr size_t kManyQ = kStages * kStageBytes, kManySwap = kManyQ + 16 * kQPitch;
 constexpr size_t kManySmem = kManySwap + kWarps * 16 * 32 * sizeof(float) + 1024;
 
 struct Item {
-    int32_t first, rows;       // first token and rows of the request (0: no more items)
-    int32_t table_row, q0;     // q0: index of the first token
-    int32_t from, h;           // first own key, kv head
-    int32_t heads;             // 0: the four warps share the keys of a block of 16 rows, or two and two those of two blocks
-                               // else: a warp a block of 16 rows of kv heads h .., and all keys
-    int32_t short_keys;        // all own keys are in one tile, from key() on
-    __device__ __forceinline__ Own own(int32_t G) const { return Own{from, q0, q0 + (rows - 1) / G}; }
+    int32_t first, base, rows;  // first token of the request; its rows base .. base + rows - 1 (0: no more items)
+    int32_t table_row, q0;      // q0: index of the request's first token
+    int32_t from, h;            // first own key, kv head
+    // 0: the four warps share the keys of a block of 16 rows, or two and two those of two blocks.  Else all of the keys
+    // are in one tile, from key() on, and a warp has a block of rows of one of the kv heads h .. h + heads - 1.
+    int32_t heads;
+    __device__ __forceinline__ Own own(int32_t G) const { return Own{from, q0 + base / G, q0 + (base + rows - 1) / G}; }
     __device__ __forceinline__ int32_t key() const { return from & ~15; }
-    __device__ __forceinline__ int32_t tile0() const { return from / kTile; }
-    __device__ __forceinline__ int32_t tiles(const Own &o) const { return short_keys ? heads : o.last / kTile + 1 - tile0(); }
 };
 struct ManyShared {
     Ring ring;
@@ -462,21 +459,21 @@ struct ManyShared {
     float2 ml[kWarps][16];
 };
 
-// Row r of a kv head of a request whose first token is `first`, as a row of [T][Hq].
-__device__ __forceinline__ int64_t place(const Params &p, int32_t first, int32_t h, int32_t r) {
-    const int32_t token = r / p.G;
-    return (int64_t)(first + token) * p.a.num_q_heads + h * p.G + (r - token * p.G);
+// Row r of an item, in kv head h, as a row of [T][Hq].
+__device__ __forceinline__ int64_t place(const Params &p, const Item &it, int32_t h, int32_t r) {
+    const int32_t row = it.base + r, token = row / p.G;
+    return (int64_t)(it.first + token) * p.a.num_q_heads + h * p.G + (row - token * p.G);
 }
 
-// Rows r0, r0 + step .. below r1 of a kv head by own_row.
+// Rows r0, r0 + step .. below r1 of an item, in kv head h, by own_row.
 __device__ __forceinline__ void own_rows(const Params &p, const Item &it, int32_t h, const Own &own, int32_t r0, int32_t r1,
                                          int32_t step) {
     const int lane = threadIdx.x & 31;
     const PrefixSpace space = prefix_space(p.a);
     for (int32_t r = r0; r < r1; r += step) {
         float4 acc;
-        const int64_t at = place(p, it.first, h, r);
-        const float2 x = own_row(p, at, h, it.table_row, own, it.q0 + r / p.G, acc);
+        const int64_t at = place(p, it, h, r);
+        const float2 x = own_row(p, at, h, it.table_row, own, it.q0 + (it.base + r) / p.G, acc);
         store4(space.own_o + at * kD + 4 * lane, acc);
         if (lane == 0) space.own[at] = make_float4(x.x, x.y, it.from > 0, 0.f);
     }
@@ -495,7 +492,8 @@ template <int kRowBlocks, bool kShort>
 __device__ void take_items(const Params &p, ManyShared &sh, unsigned char *sm, uint32_t *taken) {
     const int lane = threadIdx.x & 31;
     const PrefixAttentionArgs &a = p.a;
-    const uint32_t parts = (uint32_t)(a.num_kv_heads / p.heads), units = (uint32_t)a.cache.batch * parts;
+    // units: the row blocks of heads of a request, all of a request's heads before its next row blocks
+    const uint32_t parts = (uint32_t)(a.num_kv_heads / p.heads) * (uint32_t)p.chunks, units = (uint32_t)a.cache.batch * parts;
     uint32_t n = 0, with_q = 0;  // items published; those of one head
     const auto publish = [&](const Item &it) {
         const uint32_t s = n % kItems;
@@ -515,37 +513,38 @@ __device__ void take_items(const Params &p, ManyShared &sh, unsigned char *sm, u
         if (t >= units) break;
         if (lane == 0) ticket = atomicAdd(taken, 1u);
         const uint32_t b = t / parts;
-        const int32_t h0 = (int32_t)(t - b * parts) * p.heads;
+        const int32_t part = (int32_t)(t - b * parts), chunk = part % p.chunks, h0 = part / p.chunks * p.heads;
         const PrefixRequest req = prefix_request(a, p.cut, (int32_t)b);
-        if (!req.ok && h0 == 0 && lane == 0) record_status(a.status, KDA_ERR_DEVICE_CHECK, b);
-        const int32_t num_rows = req.n * p.G;
-        if (num_rows == 0) continue;
-        Item it{req.first, num_rows, req.row, req.len - req.n, req.from, 0, 0, 0};
-        const int32_t blocks = (num_rows + 15) / 16;
-        it.short_keys = kShort && p.heads * blocks > 1 && req.len - it.key() <= kTile;
-        const int32_t each = it.short_keys ? kWarps / blocks : 1;  // heads of an item
-        for (int32_t h = h0; h < h0 + p.heads; h += each) {
-            it.h = h;
-            it.heads = it.short_keys ? min(each, h0 + p.heads - h) : kRowBlocks == kWarps;
-            if (!publish(it)) return;
-            if (kRowBlocks > 1 || it.heads > 0) continue;
-            uint4 x[8];  // rows lane / 16 + 2 i
+        if (!req.ok && part == 0 && lane == 0) record_status(a.status, KDA_ERR_DEVICE_CHECK, b);
+        const int32_t num_rows = req.n * p.G, step = 16 * kRowBlocks;
+        for (int32_t base = step * chunk; base < num_rows; base += step * p.chunks) {
+            Item it{req.first, base, min(step, num_rows - base), req.row, req.len - req.n, req.from, 0, 0};
+            const int32_t blocks = (it.rows + 15) / 16;
+            const bool short_keys = kShort && p.heads * blocks > 1 && it.own(p.G).last - it.key() < kTile;
+            const int32_t each = short_keys ? kWarps / blocks : 1;  // heads of an item
+            for (int32_t h = h0; h < h0 + p.heads; h += each) {
+                it.h = h;
+                it.heads = short_keys ? min(each, h0 + p.heads - h) : 0;
+                if (!publish(it)) return;
+                if (kRowBlocks > 1 || it.heads > 0) continue;
+                uint4 x[8];  // rows lane / 16 + 2 i
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int32_t r = (lane >> 4) + 2 * i, token = r / p.G;
-                x[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (r < num_rows)
-                    x[i] = *reinterpret_cast<const uint4 *>(
-                        static_cast<const __nv_bfloat16 *>(a.q) +
-                        ((int64_t)(req.first + token) * a.num_q_heads + h * p.G + r - token * p.G) * kD + 8 * (lane & 15));
+                for (int i = 0; i < 8; ++i) {
+                    const int32_t r = (lane >> 4) + 2 * i, token = (base + r) / p.G;
+                    x[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < it.rows)
+                        x[i] = *reinterpret_cast<const uint4 *>(
+                            static_cast<const __nv_bfloat16 *>(a.q) +
+                            ((int64_t)(req.first + token) * a.num_q_heads + h * p.G + base + r - token * p.G) * kD + 8 * (lane & 15));
+                }
+                if (with_q > 0 && !wait(sh.ring, &sh.q_empty, (with_q - 1) & 1, p, 199)) return;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint4 *>(sm + kManyQ + ((lane >> 4) + 2 * i) * kQPitch + 16 * (lane & 15)) = x[i];
+                __syncwarp();
+                if (lane == 0) arrive(&sh.q_full);
+                ++with_q;
             }
-            if (with_q > 0 && !wait(sh.ring, &sh.q_empty, (with_q - 1) & 1, p, 199)) return;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4 *>(sm + kManyQ + ((lane >> 4) + 2 * i) * kQPitch + 16 * (lane & 15)) = x[i];
-            __syncwarp();
-            if (lane == 0) arrive(&sh.q_full);
-            ++with_q;
         }
     }
     publish(Item{});
@@ -559,9 +558,8 @@ __device__ __forceinline__ bool two_blocks(const Params &p, ManyShared &sh, unsi
     const PrefixSpace space = prefix_space(p.a);
     const Own own = it.own(p.G);
     w.clear();
-    load_q(p.a, p.G, it.first, it.h, r0, it.rows, it.q0, w);
-    const int32_t count = it.tiles(own);
-    for (int32_t i = 0; i < count; ++i, ++tiles) {
+    load_q(p.a, p.G, it.first, it.h, it.base + r0, it.base + it.rows, it.q0, w);
+    for (int32_t i = own.from / kTile; i <= own.last / kTile; ++i, ++tiles) {
         const int32_t st = tiles % kStages;
         if (!wait(sh.ring, &sh.ring.full[st], (tiles / kStages) & 1, p, 205)) break;
         consume<2>(p, sh.ring, sm, st, own, w);
@@ -623,7 +621,7 @@ __device__ __forceinline__ bool two_blocks(const Params &p, ManyShared &sh, unsi
     for (int u = 0; u < 2; ++u) {
         const int32_t r = r0 + (lane >> 2) + 8 * u;
         if (r >= it.rows) continue;
-        const int64_t at = place(p, it.first, it.h, r);
+        const int64_t at = place(p, it, it.h, r);
         float *o = space.own_o + at * kD + 64 * group + 2 * (lane & 3);
 #pragma unroll
         for (int t = 0; t < 8; ++t)
@@ -652,7 +650,7 @@ __device__ __forceinline__ bool one_block(const Params &p, ManyShared &sh, unsig
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         const int32_t r = (lane >> 2) + 8 * u;
-        w.pos[u] = r < it.rows ? it.q0 + r / p.G : -1;
+        w.pos[u] = r < it.rows ? it.q0 + (it.base + r) / p.G : -1;
     }
     for (int32_t i = own.from / kTile; i <= own.last / kTile; ++i, ++tiles) {
         const int32_t st = tiles % kStages;
@@ -725,7 +723,7 @@ __device__ __forceinline__ bool one_block(const Params &p, ManyShared &sh, unsig
     for (int u = 0; u < 2; ++u) {
         const int32_t r = (lane >> 2) + 8 * u;
         if (r >= it.rows) continue;
-        const int64_t at = place(p, it.first, it.h, r);
+        const int64_t at = place(p, it, it.h, r);
         float *o = space.own_o + at * kD + 32 * warp + 2 * (lane & 3);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
@@ -735,7 +733,7 @@ __device__ __forceinline__ bool one_block(const Params &p, ManyShared &sh, unsig
     return true;
 }
 
-// Requests of up to kRowBlocks blocks; kShort: with items whose keys are all in one tile.  (Apart, since all of it
+// Items of up to kRowBlocks blocks of rows; kShort: with items whose keys are all in one tile.  (Apart, since all of it
 // together costs 16 x 4 beams 92 us instead of 80: instructions to fetch, and registers that spill.)
 template <int kRowBlocks, bool kShort>
 __global__ void __launch_bounds__(kManyThreads, 2) prefix_own_many_kernel(const __grid_constant__ Params p) {
@@ -745,7 +743,6 @@ __global__ void __launch_bounds__(kManyThreads, 2) prefix_own_many_kernel(const 
     unsigned char *sm = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const PrefixAttentionArgs &a = p.a;
-    const int32_t G = p.G;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sh.ring.full[i], 1);
@@ -775,14 +772,11 @@ __global__ void __launch_bounds__(kManyThreads, 2) prefix_own_many_kernel(const 
             __syncwarp();
             if (lane == 0) arrive(&sh.item_empty[s]);
             if (it.rows == 0) break;
-            const Own own = it.own(G);
-            const int32_t count = it.tiles(own);
+            const Own own = it.own(p.G);
             bool ok = true;
-            for (int32_t i = 0; ok && i < count; ++i) {
-                const int32_t j0 = it.short_keys ? it.key() : (it.tile0() + i) * kTile;
-                ok = produce(p, sh.ring, sm, it.table_row, own, it.short_keys ? it.h + i : it.h, j0,
-                             it.short_keys || own.some_hidden(j0, kTile), tiles);
-            }
+            if (it.heads == 0) ok = produce(p, sh.ring, sm, it.table_row, own, it.h, own.from / kTile, own.last / kTile + 1, tiles);
+            for (int32_t i = 0; ok && i < it.heads; ++i)
+                ok = produce(p, sh.ring, sm, it.table_row, own, it.h + i, it.key(), true, tiles);
             if (!ok) break;
         }
         drain(sh.ring, 0, tiles);
@@ -795,18 +789,18 @@ __global__ void __launch_bounds__(kManyThreads, 2) prefix_own_many_kernel(const 
             const Item it = sh.item[s];
             __syncwarp();
             if (lane == 0) arrive(&sh.item_empty[s]);
-            if ((kShort || kRowBlocks == kWarps) && it.heads > 0) {
+            if (kShort && it.heads > 0) {
                 // Everyone waits for every tile and frees it, so that none falls behind the ring.
-                const Own own = it.own(G);
+                const Own own = it.own(p.G);
                 const int32_t blocks = (it.rows + 15) / 16, head = warp / blocks, h = it.h + head;
-                const int32_t r0 = 16 * (warp - head * blocks), r1 = min(r0 + 16, it.rows), count = it.tiles(own);
+                const int32_t r0 = 16 * (warp - head * blocks), r1 = min(r0 + 16, it.rows);
                 const bool mine = got && head < it.heads;
                 w.clear();
-                if (mine) load_q(a, G, it.first, h, r0, it.rows, it.q0, w);
-                for (int32_t i = 0; got && i < count; ++i, ++tiles) {
+                if (mine) load_q(a, p.G, it.first, h, it.base + r0, it.base + it.rows, it.q0, w);
+                for (int32_t i = 0; got && i < it.heads; ++i, ++tiles) {
                     const int32_t st = tiles % kStages;
                     if (!(got = wait(sh.ring, &sh.ring.full[st], (tiles / kStages) & 1, p, 204))) break;
-                    if (mine && (!it.short_keys || i == head)) consume<kWarps>(p, sh.ring, sm, st, own, w);
+                    if (mine && i == head) consume<kWarps>(p, sh.ring, sm, st, own, w);
                     __syncwarp();
                     if (lane == 0) arrive(&sh.ring.empty[st]);
                 }
@@ -822,7 +816,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) prefix_own_many_kernel(const 
                     w.l[u] += __shfl_xor_sync(kAll, w.l[u], 2);
                     const int32_t r = r0 + (lane >> 2) + 8 * u;
                     if (r >= r1) continue;
-                    const int64_t at = place(p, it.first, h, r);
+                    const int64_t at = place(p, it, h, r);
                     float *o = space.own_o + at * kD + 2 * (lane & 3);
 #pragma unroll
                     for (int t = 0; t < 16; ++t) *reinterpret_cast<float2 *>(o + 8 * t) = make_float2(w.o[t][2 * u], w.o[t][2 * u + 1]);
@@ -873,8 +867,9 @@ cudaError_t launch_prefix_own(const PrefixAttentionArgs &a, const PrefixCut &cut
     // (a request that brings most of the step's tokens takes several turns then).
     const int64_t T = a.cache.total_tokens, B = a.cache.batch;
     const int64_t most = (a.max_tokens < T ? a.max_tokens : T) * p.G;
-    const int rows = most <= 16 ? 16 : 32;
-    const int64_t need = (most + rows - 1) / rows, share = (2 * ((T + B - 1) / B) * p.G + rows - 1) / rows;
+    const int64_t average = (T + B - 1) / B * p.G;
+    const int rows = most <= 16 || average <= 16 ? 16 : 32;
+    const int64_t need = (most + rows - 1) / rows, share = (2 * average + rows - 1) / rows;
     p.chunks = (int32_t)(need < share ? need : share);
     // Split a request's keys over a cluster as far as the CTAs are all resident at once (two an SM) and keep two
     // tiles each, as far as the table's width can tell.
@@ -883,13 +878,12 @@ cudaError_t launch_prefix_own(const PrefixAttentionArgs &a, const PrefixCut &cut
     int splits = 1;
     while (splits < kMaxSplits && ctas * splits <= device_sm_count() / 2 && tiles >= 4 * splits) splits *= 2;
     if (splits * B * p.chunks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    const int64_t most_ctas = 2 * device_sm_count(), items = B * a.num_kv_heads;
-    if (most <= kManyRows && splits == 1 && items > device_sm_count() && items < 0x7fffffff) {
+    if (splits == 1 && ctas > device_sm_count() && ctas < 0x7fffffff) {
+        const int64_t most_ctas = 2 * device_sm_count();
         p.heads = 1;
-        while (a.num_kv_heads % (2 * p.heads) == 0 && items >= 2 * p.heads * 4 * most_ctas) p.heads *= 2;
-        const unsigned n = (unsigned)(items < most_ctas ? items : most_ctas);
-        if (most > 32) return launch_many<4, true>(p, n, stream);
-        if (most > 16) return launch_many<2, true>(p, n, stream);
+        while (a.num_kv_heads % (2 * p.heads) == 0 && ctas >= 2 * p.heads * 4 * most_ctas) p.heads *= 2;
+        const unsigned n = (unsigned)(ctas < most_ctas ? ctas : most_ctas);
+        if (rows > 16) return launch_many<2, true>(p, n, stream);
         return p.heads > 1 ? launch_many<1, true>(p, n, stream) : launch_many<1, false>(p, n, stream);
     }
     return rows == 16 ? launch<1>(p, splits, stream) : launch<2>(p, splits, stream);

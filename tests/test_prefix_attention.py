@@ -140,6 +140,36 @@ def test_many_requests(kda, shape, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("group,heads,most", [(6, 2, 40), (6, 2, 100000), (5, 16, 40), (13, 2, 40)])
+def test_a_few_long_requests_among_many(kda, group, heads, most, dtype):
+    """Single tokens for the most part, and some requests that bring many row blocks, with short and long own keys.
+
+    fp32: 1e-5 of the root mean square is a typical error's bound, and too little for the largest of 4 million
+    elements (1.04e-5 was seen).  What holds for each: a score is 128 fused steps and a multiplication, off by at most
+    129 half steps of A = scale sum_i |q_i| |k_ji|; less the maximum (a difference of at most 2 A) by 2 more; its
+    exponential (two units) by 2^-22 of itself.  So a weight is off by a factor within e^(+-D), D = 131 * 2^-24 A + 2^-22;
+    sums of n < 512 of them, weighted or not, by n half steps each; their ratio rounds twice (1 / l, and the product).
+    |o - ref| <= (e^(2 D + 2 n 2^-24 + 2^-22) - 1) a with a = sum_j softmax_j |v_j|.
+    """
+    B = 300
+    new = [1] * B
+    for b, n in ((0, 13), (7, 40), (150, 3), (151, 0), (299, 29)):
+        new[b] = n
+    mine = [[n + (b * 37) % (90 if b % 4 else 9) for b, n in enumerate(new)]]
+    c = build_branches([70], mine, 32, heads, dtype, seed=most % 97)
+    q = queries(sum(new), heads * group, dtype, 71)
+    o = call(kda, q, c, new, max_tokens=most)
+    assert kda.kda_get_device_status()[0] == 0
+    if dtype == BF16:
+        return check(o, q, c, new)
+    ref, a = prefix64(q, c, new)
+    k = c["pool"][:, 0].transpose(0, 1).reshape(heads, -1, 128).abs()
+    most_a = torch.stack([(x.abs() @ k[h].T).amax(-1) for h, x in enumerate(q.reshape(len(q), heads, group, 128).unbind(1))], 1)
+    d = 131 * 2.0 ** -24 * 128 ** -0.5 * to64(most_a).reshape(len(q), heads * group, 1) + 2.0 ** -22
+    assert (np.abs(to64(o) - ref) <= np.expm1(2 * d + 2 * 512 * 2.0 ** -24 + 2.0 ** -22) * a).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_same_as_window_attention_without_a_window(kda, dtype):
     """Rows that share their prefix: the two calls differ by roundings alone."""
     new = [1, 2, 1, 4]
