@@ -68,6 +68,15 @@ def test_ties_go_to_the_lowest_index(kda, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("B,K,V,N", [(2, 32, 60000, 64), (1, 64, 20001, 64), (3, 24, 33000, 40)])
+@pytest.mark.parametrize("apart", [0.0, 0.5, 3.0, 40.0])
+def test_some_beams_ahead(kda, B, K, V, N, apart, dtype):
+    """Many choices of many beams, the lower ones better by more and more: all of the best come from a few of them."""
+    logits, scores = make(B, K, V, dtype, seed=K + N)
+    check(kda, logits, scores / 9 - apart * torch.arange(K, device="cuda"), N)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("V", [37, 3000, 70000])
 def test_masked_tokens(kda, V, dtype):
     """-inf, the type's lowest value, NaN and +inf among the logits; rows of nothing else; beams that do not exist."""
