@@ -354,7 +354,7 @@ __device__ __forceinline__ bool before(const Choice &x, const Choice &y) {
 
 // A CTA a prompt.  Thread t owns the lists t, t + 256, ...: list i is segment i % S of beam i / S.
 // Bound by the chain of its steps (about 6 us: loads, exponentials and logarithms in 64 bits 3, the two rounds of
-// counting 2).
+// counting 2): 64 prompts of 8 beams 8.7 us, of which 6.5 show behind the segments.
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamSelectArgs a, const Layout lay) {
     __shared__ double s_score[KDA_MAX_BEAMS], s_lse[KDA_MAX_BEAMS];
     __shared__ uint64_t s_group[64], s_total[kThreads], s_key[kThreads];

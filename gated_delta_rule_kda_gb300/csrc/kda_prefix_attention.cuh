@@ -30,9 +30,15 @@ struct PrefixCut {
     int32_t width;
     float tile_us;      // what a key tile takes a CTA
 };
+// In tiles.  With 2: 42 prompts x 60 beams 224 us instead of 215, 47 x 100 branches of few keys 1,115 instead of 970; no
+// difference to long items.
 constexpr int32_t kPrefixExtra = 3;
-// What an own key of a kv head, and a request and kv head, take of an SM: 512 bytes at some 75 GB/s.
-constexpr float kOwnKeyUs = 512.f / 75e3f, kOwnItemUs = 2.f, kOwnShortUs = 1.f;  // (short: below 48 keys on average)
+// What an own key of a kv head, and a request and kv head, take of an SM: 512 bytes at some 75 GB/s, and what their
+// beginning and end cost, less where most keys are few (below 48 on average: heads go side by side).  They only say
+// how SMs are shared out.  Too little for the own keys: 16 prompts x 4 beams 90 us with 0.7 instead of 79 with 2;
+// too much: 256 requests behind a system prompt 253 us with 3, 236 with 2; 42 x 60 beams of 14 own keys 215 us
+// with 2 for short ones too, 186 with 1.
+constexpr float kOwnKeyUs = 512.f / 75e3f, kOwnItemUs = 2.f, kOwnShortUs = 1.f;
 
 // Group g, checked; items = 0 when there is nothing to do for it (ok: whether it is well formed).
 struct PrefixGroup {
@@ -224,8 +230,10 @@ __device__ void prefix_make_plan(const PrefixAttentionArgs &a, const PrefixCut &
         falls = __syncthreads_or(falls);
         if (falls) all = 0;
         if (tid == 0) {
-            // The own keys' launch gets the SMs that its work asks for.  Every team has a unit, so that the parts of an
-            // item lie in neighbouring runs.
+            // The own keys' launch gets the SMs that its work asks for, though never more than seven of eight: what is left
+            // of it flows to SMs that the prefixes leave, the other way round it does not (1,210 branches of one own
+            // key and 64 shared ones: 64 us, without 176).  Every team has a unit, so that the parts of an item
+            // lie in neighbouring runs.
             const float work = (float)all * (float)cut.width * cut.tile_us;
             // (twice for more than 32 rows of a request, and so on)
             const float rows = (float)a.cache.total_tokens / (float)B * (float)(a.num_q_heads / Hkv);

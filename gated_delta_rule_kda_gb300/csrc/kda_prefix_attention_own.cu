@@ -1,9 +1,11 @@
 // Attention over a shared prefix, bf16: each request's own keys, the second launch of kda_prefix_attention.
 //
-// Bound by reading the own keys and values once, so the work is cut along the keys as in the windowed
-// attention's kernel for few rows: a cluster of up to 16 CTAs takes consecutive runs of 64-key tiles and
-// joins them through distributed shared memory, in an order that the sizes alone decide; o (not divided), m
-// and l of each row go to the workspace.
+// Bound by reading the own keys and values once.  Two ways to fill the GPU with that:
+//   few requests   the work is cut along the keys as in the windowed attention's kernel for few rows: a cluster of
+//                  up to 16 CTAs takes consecutive runs of 64-key tiles and joins them through distributed shared
+//                  memory, in an order that the sizes alone decide
+//   many           CTAs that stay take one (request, kv heads, rows) after the other, see below
+// o (not divided), m and l of each row go to the workspace.
 //
 // A row is a (token, query head of the group) pair; a CTA has up to 32 of them, in one or two blocks of 16,
 // and goes on to further ones where a request has more.  A producer warp fetches k and v by TMA, page by
@@ -433,9 +435,12 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_own_kernel(const __grid_co
 // ---------------------------------------------------------------------------
 // Many requests of a few rows a kv head each
 // ---------------------------------------------------------------------------
-// Here the CTAs stay and take work, kv heads of a request, as they get done, so that an item's beginning and end hide behind its neighbours' keys: a sixth warp takes the items,
+// Here the CTAs (two an SM) stay and take work, kv heads of a request, as they get done, so that an item's beginning and end hide behind its neighbours' keys: a sixth warp takes the items,
 // looks their requests up and brings q, and the fetching warp goes on to the next item's keys while the
-// consumers end the last one's.  Which CTA computes an item makes no difference to it.
+// consumers end the last one's.  Which CTA computes an item makes no difference to it.  Own keys that fit in one tile
+// go a warp a head (or row block), without a join.  256 requests of 1 to 2048 own keys (8 heads of 12 rows, 1.07 GB)
+// take 182 us alone, 6.1 TB/s: HBM, and a tail of some 25 us while the last items end.  2,520 requests of 14 own keys
+// in 4 heads: 69 us a call (a head at a time 123); there the time goes into items' beginnings and ends.
 constexpr int kManyThreads = 32 * (kWarps + 2);
 constexpr int kItems = 4;                      // in the queue
 constexpr int kQPitch = 2 * kD + 16;           // bytes: the eight rows of a fragment in distinct banks
@@ -871,15 +876,21 @@ cudaError_t launch_prefix_own(const PrefixAttentionArgs &a, const PrefixCut &cut
     const int rows = most <= 16 || average <= 16 ? 16 : 32;
     const int64_t need = (most + rows - 1) / rows, share = (2 * average + rows - 1) / rows;
     p.chunks = (int32_t)(need < share ? need : share);
-    // Split a request's keys over a cluster as far as the CTAs are all resident at once (two an SM) and keep two
-    // tiles each, as far as the table's width can tell.
+    // Split a request's keys over a cluster as far as the CTAs fit on half of the SMs (two an SM; the other half may
+    // have prefixes for long, and a cluster only starts whole) and keep two tiles each, as far as the table's width can
+    // tell.  Six prompts of one request: 30 us; 33 with clusters for all SMs; six prompts of 21 requests with
+    // up to 2,100 own keys the other way round, 41.7 against 40.8.
     const int64_t tiles = ((int64_t)a.cache.table_width * a.cache.page_size + kTile - 1) / kTile;
     const int64_t ctas = B * a.num_kv_heads * p.chunks;
     int splits = 1;
     while (splits < kMaxSplits && ctas * splits <= device_sm_count() / 2 && tiles >= 4 * splits) splits *= 2;
     if (splits * B * p.chunks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    // From one item an SM on the CTAs stay.  2 prompts x 26 beams in 4 heads: 68 us, 72 with a CTA an item; with 126
+    // long items (6 x 21 beams, one head) 52, and 41 in clusters.
     if (splits == 1 && ctas > device_sm_count() && ctas < 0x7fffffff) {
         const int64_t most_ctas = 2 * device_sm_count();
+        // Heads one by one balance best (16 prompts x 4 beams: 80 us, 94 with short keys a warp a head); where each CTA
+        // gets many, several at once (1,210 requests of 10 own keys, 8 heads: 78 us instead of 129, without prefixes).
         p.heads = 1;
         while (a.num_kv_heads % (2 * p.heads) == 0 && ctas >= 2 * p.heads * 4 * most_ctas) p.heads *= 2;
         const unsigned n = (unsigned)(ctas < most_ctas ? ctas : most_ctas);
