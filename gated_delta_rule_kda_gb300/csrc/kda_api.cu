@@ -74,7 +74,7 @@ const char *kda_status_string(kda_status status) {
     return "KDA_UNKNOWN_STATUS";
 }
 
-int32_t kda_version(void) { return 300; }  // 0.3.0: paged cache, windowed attention, q/k norm + rotation
+int32_t kda_version(void) { return 400; }  // 0.4.0: branches of a request (prefix attention, beam selection and reordering)
 
 size_t kda_prefill_workspace_size(int32_t num_seqs, int32_t total_tokens, int32_t num_heads,
                                   kda_dtype in_dtype) {

@@ -497,7 +497,7 @@ template <int kRowBlocks, bool kShort>
 __device__ void take_items(const Params &p, ManyShared &sh, unsigned char *sm, uint32_t *taken) {
     const int lane = threadIdx.x & 31;
     const PrefixAttentionArgs &a = p.a;
-    // units: the row blocks of heads of a request, all of a request's heads before its next row blocks
+    // units: row blocks of heads of a request; those of the same heads run side by side and find the keys in L2
     const uint32_t parts = (uint32_t)(a.num_kv_heads / p.heads) * (uint32_t)p.chunks, units = (uint32_t)a.cache.batch * parts;
     uint32_t n = 0, with_q = 0;  // items published; those of one head
     const auto publish = [&](const Item &it) {

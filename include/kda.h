@@ -811,9 +811,9 @@ size_t kda_prefix_attention_workspace_size(kda_dtype dtype, int32_t batch, int32
  * range, that no group holds, or whose group's prefix_len is longer than
  * kv_len[row] - n_b or whose group's first slot is out of range, is refused by
  * the kernel (its rows of o stay as they are; KDA_ERR_DEVICE_CHECK with
- * detail = b).  Where cu_groups falls from one entry to the next, or a launch
- * gave up (KDA_ERR_DEVICE_TIMEOUT), no row of o is written; the detail is then
- * the group.
+ * detail = b).  Where cu_groups falls from one entry to the next, no row of o
+ * is written (detail: the group); after a KDA_ERR_DEVICE_TIMEOUT the rows that
+ * were not computed stay as they are.
  */
 kda_status kda_prefix_attention(kda_dtype dtype, int32_t batch, int32_t total_tokens,
                                 int32_t max_tokens, int32_t num_q_heads, int32_t num_kv_heads,

@@ -370,7 +370,8 @@ def test_loose_max_tokens(kda, dtype):
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("shape", [([3000, 500], [[40] * 9, [7] * 2], [1] * 11, 2, 8, 64),
-                                   ([9000], [[3, 700]], [2, 1], 1, 4, 32)])
+                                   ([9000], [[3, 700]], [2, 1], 1, 4, 32),
+                                   ([300, 64], [[9, 50] * 60, [130] * 60], [1, 3] * 90, 2, 6, 32)])
 def test_replayed_from_a_graph_and_repeated_bit_for_bit(kda, shape, dtype):
     """One capture over buffers whose contents, lengths and prefixes change between replays."""
     prefix, mine, new, heads, group, page = shape
