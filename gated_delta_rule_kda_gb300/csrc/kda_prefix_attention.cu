@@ -109,67 +109,103 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_own_rows_kernel(const Pref
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 
-// A warp a row of [T][Hq], four channels a lane.  c: 2^(c m) is what a maximum m of the parts stands for.
-// Bound by two rounds of loads one after the other (where the row's parts lie; the parts): 24,576 rows 15 us, most of
-// it from L2.  With each row's parts worked out from the plan again instead of looked up: 22 us.
-template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixAttentionArgs a, const PrefixCut cut, float c) {
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
-    const PrefixSpace space = prefix_space(a);
-    const bool live = row < (int64_t)a.cache.total_tokens * a.num_q_heads;
-    const int32_t token = live ? (int32_t)(row / a.num_q_heads) : 0, head = live ? (int32_t)(row - (int64_t)token * a.num_q_heads) : 0;
-    const int64_t more_at = cut.by_rows ? row : (int64_t)token * a.num_kv_heads + head / cut.G;
-    grid_wait();
-    const float4 own = live ? space.own[row] : make_float4(0.f, -1.f, 0.f, 0.f);
-    float4 acc = live ? load4(space.own_o + row * kD + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-    // Where a CTA of the first launch gave up (and said so), nothing is joined: where parts lie may be unsaid.
-    bool lost = false;
-    for (int32_t i = threadIdx.x; i < cut.ctas; i += kJoinThreads) lost |= space.done[i] != 1;
-    if (__syncthreads_or(lost) || own.y < 0.f) return;  // (or the row's request was refused)
-    float top = own.x, sum = own.y;
-    // 2^(c (m - M)); of a part without keys 0, but a NaN sum stays one
-    const auto add = [&](float2 ml, float4 y) {
+// What some parts come to, four channels a lane.  A maximum m stands for 2^(c m).
+struct Joined {
+    float top = -INFINITY, sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    __device__ __forceinline__ void add(float2 ml, float4 y, float c) {
         const float now = fmaxf(top, ml.x);
-        const auto weight = [&](float m, float l) {
+        const auto weight = [&](float m, float l) {  // of a part without keys 0, but a NaN sum stays one
             return m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : tc::ex2_approx((m - now) * c);
         };
         const float keep = weight(top, sum), w = weight(ml.x, ml.y);
         top = now;
         sum = fmaf(sum, keep, w * ml.y);
-        acc = make_float4(fmaf(acc.x, keep, w * y.x), fmaf(acc.y, keep, w * y.y), fmaf(acc.z, keep, w * y.z), fmaf(acc.w, keep, w * y.w));
-    };
-    if (own.z != 0.f) {
-        const int4 more = space.more[more_at];
-        const float2 ml = space.ml[row];
-        const float4 y = load4(space.o + row * kD + 4 * lane);
+        o = make_float4(fmaf(o.x, keep, w * y.x), fmaf(o.y, keep, w * y.y), fmaf(o.z, keep, w * y.z), fmaf(o.w, keep, w * y.w));
+    }
+};
+
+// kWarps warps a row of [T][Hq], which take its parts in turns.  Bound by rounds of loads one after the other (where the
+// row's parts lie; the parts, four at a time): 24,576 rows of two or three parts 15 us, most of it from L2.  With each
+// row's parts worked out from the plan again instead of looked up: 22 us.
+template <typename T, int kWarps>
+__global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixAttentionArgs a, const PrefixCut cut, float c) {
+    constexpr int kRowsCta = kJoinThreads / 32 / kWarps;
+    __shared__ float4 s_o[kJoinThreads / 32][32];
+    __shared__ float2 s_ml[kJoinThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, turn = warp % kWarps;
+    const int64_t row = (int64_t)blockIdx.x * kRowsCta + warp / kWarps;
+    const PrefixSpace space = prefix_space(a);
+    const bool live = row < (int64_t)a.cache.total_tokens * a.num_q_heads;
+    const int32_t token = live ? (int32_t)(row / a.num_q_heads) : 0, head = live ? (int32_t)(row - (int64_t)token * a.num_q_heads) : 0;
+    const int64_t more_at = cut.by_rows ? row : (int64_t)token * a.num_kv_heads + head / cut.G;
+    grid_wait();
+    // (all that may be wanted at once; what nothing was written to is not used)
+    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool first = live && turn == 0;
+    const float4 own = live ? space.own[row] : make_float4(0.f, -1.f, 0.f, 0.f);
+    const int4 more = live ? space.more[more_at] : make_int4(0, 0, 0, 0);
+    const float4 own_o = first ? load4(space.own_o + row * kD + 4 * lane) : none, o = first ? load4(space.o + row * kD + 4 * lane) : none;
+    const float2 ml = first ? space.ml[row] : make_float2(-INFINITY, 0.f);
+    // Where a CTA of the first launch gave up (and said so), nothing is joined: where parts lie may be unsaid.
+    bool lost = false;
+    for (int32_t i = threadIdx.x; i < cut.ctas; i += kJoinThreads) lost |= space.done[i] != 1;
+    if (__syncthreads_or(lost)) return;
+    const bool wanted = own.y >= 0.f;  // (else the row's request was refused)
+    Joined x;
+    if (wanted && turn == 0) {
+        x.top = own.x;
+        x.sum = own.y;
+        x.o = own_o;
+    }
+    if (wanted && own.z != 0.f) {
         const int32_t r = more.w + (cut.by_rows ? 0 : head % cut.G);
-        add(ml, y);
-        for (int32_t k0 = 1; k0 <= more.y; k0 += 4) {  // four parts' loads at a time
+        if (turn == 0) x.add(ml, o, c);
+        for (int32_t k0 = 1 + turn; k0 <= more.y; k0 += 4 * kWarps) {  // four parts' loads at a time
             float2 mls[4];
             float4 ys[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 mls[k] = make_float2(-INFINITY, 0.f);
                 ys[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (k0 + k > more.y) continue;
-                const int32_t cta = more.x + (k0 + k) * more.z;
-                float *slot = prefix_slot(space, cut, cta);
+                if (k0 + k * kWarps > more.y) continue;
+                float *slot = prefix_slot(space, cut, more.x + (k0 + k * kWarps) * more.z);
                 mls[k] = prefix_slot_ml(slot, cut)[r];
                 ys[k] = load4(slot + (int64_t)r * kD + 4 * lane);
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) add(mls[k], ys[k]);
+            for (int k = 0; k < 4; ++k) x.add(mls[k], ys[k], c);
         }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    store4(static_cast<T *>(a.o) + row * kD + 4 * lane, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    if constexpr (kWarps > 1) {
+        s_o[warp][lane] = x.o;
+        if (lane == 0) s_ml[warp] = make_float2(x.top, x.sum);
+        __syncthreads();
+        if (turn != 0) return;
+#pragma unroll
+        for (int k = 1; k < kWarps; ++k) x.add(s_ml[warp + k], s_o[warp + k][lane], c);
+    }
+    if (!wanted) return;
+    const float inv = x.sum == 0.f ? 0.f : 1.f / x.sum;
+    store4(static_cast<T *>(a.o) + row * kD + 4 * lane, make_float4(x.o.x * inv, x.o.y * inv, x.o.z * inv, x.o.w * inv));
 }
 
+// Warps a row by how many parts its prefix may come in: an item's key tiles, or the CTAs that an item gets.
+// 10 beams behind 32,768 tokens, one kv head (151 parts): 54 us with one, 33 with eight.  64 x 2 tokens behind 131,072
+// (up to 5 parts, 8,192 rows): 393 us with one, 405 with four.
 template <typename T>
 cudaError_t launch_join(const PrefixAttentionArgs &a, const PrefixCut &cut, float c, cudaStream_t stream) {
-    const int64_t rows = (int64_t)a.cache.total_tokens * a.num_q_heads, per = kJoinThreads / 32;
-    return launch_serial(prefix_join_kernel<T>, dim3((unsigned)((rows + per - 1) / per)), kJoinThreads, 0, stream, a, cut, c);
+    const int64_t rows = (int64_t)a.cache.total_tokens * a.num_q_heads, Ng = a.num_groups;
+    const int64_t per_group = (a.cache.total_tokens + Ng - 1) / Ng * (cut.by_rows ? cut.G : 1);
+    const int64_t items = Ng * a.num_kv_heads * ((per_group + cut.tile - 1) / cut.tile);
+    const int64_t tiles = ((int64_t)a.cache.table_width * a.cache.page_size + cut.keys - 1) / cut.keys;
+    const int64_t share = cut.ctas / items + 1, parts = share < tiles ? share : tiles;
+    const auto launch = [&](auto kernel, int warps) {
+        const int64_t per = kJoinThreads / 32 / warps;
+        return launch_serial(kernel, dim3((unsigned)((rows + per - 1) / per)), kJoinThreads, 0, stream, a, cut, c);
+    };
+    if (parts > 16) return launch(prefix_join_kernel<T, 8>, 8);
+    return parts > 8 ? launch(prefix_join_kernel<T, 4>, 4) : launch(prefix_join_kernel<T, 1>, 1);
 }
 
 template <typename T>
