@@ -9,8 +9,9 @@
 // A CTA holds its segment in registers.  Its candidates are found with a bound: threads are taken in
 // groups, as many as N or more, and the smallest of the groups' maxima has at least N logits at or
 // above it (g groups of random logits: about g ln g).  What reaches the bound is ranked by counting.
-// Where too much does (few distinct values, a mask of the lowest value, a short segment) the CTA takes
-// its best logits one by one.
+// Where too much does, the logits are gone through once more with the bound of all of them, and where that
+// leaves too much as well (few distinct values, a mask of the lowest value, a short segment) the CTA takes its
+// best logits one by one.
 // Bound: reading the logits once.
 #include "kda_common.cuh"
 #include "tc_primitives.cuh"
@@ -266,18 +267,55 @@ __global__ void __launch_bounds__(kThreads, kCtasSm) beam_segments_kernel(const 
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
     if (lane == 0) s_sum[warp] = make_float2(all, sum);
     __syncthreads();
-    const int held = s_held;
-    if (held <= kHeld) {  // the logits themselves (above the bound or not: the N that reached it first are among them)
-        for (int i = tid; i < held * kN; i += kThreads) {
-            const float y = V::at(s_vector[i / kN], i % kN);
-            if (!(y >= bound && y > -INFINITY)) continue;
-            const int at = atomicAdd(&s_count, 1);
-            if (at < kFound) s_found[at] = make_key(V::clean(y), s_token[i / kN] + i % kN);
+    // The held vectors' logits that reach the bound (above it or not: the N that reached it first are among them).
+    const auto expand = [&] {
+        const int held = s_held;
+        if (held <= kHeld) {
+            for (int i = tid; i < held * kN; i += kThreads) {
+                const float y = V::at(s_vector[i / kN], i % kN);
+                if (!(y >= bound && y > -INFINITY)) continue;
+                const int at = atomicAdd(&s_count, 1);
+                if (at < kFound) s_found[at] = make_key(V::clean(y), s_token[i / kN] + i % kN);
+            }
+            __syncthreads();
+        }
+        return held <= kHeld && s_count <= kFound;
+    };
+    bool few = expand();
+    if (!few) {
+        // The first chunk's bound was too low for the others (it may be masked for the most part, or N be large): the N-th
+        // best of all threads' maxima, and the logits once more (4 prompts x 32 beams, 64 chosen, a fifth of 243,478
+        // tokens masked: 95 us, and 410 one by one).
+        __syncthreads();
+        s_top[tid] = m;
+        if (tid == 0) s_held = s_count = 0;
+        __syncthreads();
+        int r = 0;
+#pragma unroll 16
+        for (int i = 0; i < kThreads; ++i) r += s_top[i] > m || (s_top[i] == m && i < tid);
+        if (r == N - 1) s_bound = m;
+        __syncthreads();
+        bound = s_bound;
+#pragma unroll 1
+        for (int32_t c = 0; c < chunks; ++c) {
+            fetch(raw, c);
+            if (off != 0) align(raw, c);
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                const float y = V::max_of(raw + i);
+                if (!(y >= bound && y > -INFINITY)) continue;
+                const int at = atomicAdd(&s_held, 1);
+                if (at < kHeld) {
+                    s_vector[at] = raw[i];
+                    s_token[at] = token(c, i * kN);
+                }
+            }
         }
         __syncthreads();
+        few = expand();
     }
     int found = s_count;
-    if (held > kHeld || found > kFound) {
+    if (!few) {
         // Too many: each chunk's best, one by one, beside the best of those before.
         found = 0;
         for (int32_t c = 0; c < chunks; ++c) {

@@ -100,6 +100,21 @@ def test_masked_tokens(kda, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("N", [3, 64])
+def test_the_best_come_late(kda, N, dtype):
+    """Logits that rise along the vocabulary, or whose first tokens are masked: what a segment's beginning says about its
+    best is of no use."""
+    V = 150000
+    logits, scores = make(3, 2, V, dtype, seed=N)
+    logits = logits.clone()
+    logits[0] += torch.linspace(0, 40, V, device="cuda").to(dtype)
+    logits[1, :, :140000] = -INF
+    logits[2, 0, ::2] = torch.finfo(dtype).min
+    logits[2, 1, : V // 2] = torch.finfo(dtype).min
+    check(kda, logits, scores, N)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_ended_beams(kda, dtype):
     logits, scores = make(8, 4, 900, dtype, seed=3)
     g = torch.Generator(device="cuda")
