@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const PrefixA
     bool lost = false;
     for (int32_t i = threadIdx.x; i < cut.ctas; i += kJoinThreads) lost |= space.done[i] != 1;
     if (__syncthreads_or(lost)) return;
-    const bool wanted = own.y >= 0.f;  // (else the row's request was refused)
+    const bool wanted = !(own.y < 0.f);  // (else the row has no result; a NaN sum is one)
     Joined x;
     if (wanted && turn == 0) {
         x.top = own.x;

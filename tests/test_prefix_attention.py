@@ -479,3 +479,56 @@ def test_waits_that_run_out_are_reported(kda, shape):
     assert time.perf_counter() - t0 < 0.5
     assert bool((o == -7.0).all())
     assert attend() == 0 and torch.equal(o, want)
+
+
+# One of each kind of kernel over the own keys: single rows of a cluster, two blocks of rows, many requests head by head,
+# several heads at once (with own keys in one tile and in many), and with two blocks of rows.  No request brings more rows
+# than most.
+OWN_KERNELS = [
+    ([300, 0], [[9, 70], [33]], [1, 1, 1], 2, 4, 32),
+    ([300], [[20, 300]], [7, 7], 2, 4, 32),
+    ([100], [[3 + 40 * (i % 5) for i in range(160)]], [1] * 160, 2, 4, 32),
+    ([90], [[3 + 50 * (i % 3) for i in range(330)]], [1] * 330, 8, 2, 16),
+    ([90], [[3 + 50 * (i % 3) for i in range(100)]], [3] * 100, 2, 8, 64),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("where", ["q", "k"])
+@pytest.mark.parametrize("shape", OWN_KERNELS)
+def test_scores_that_are_not_finite_give_nan(kda, shape, where, value, dtype):
+    """A NaN or infinity in a query, or in an own key that some tokens see: their rows are what the definition gives (NaN
+    where a score is NaN or +inf), not what o held before, and all others are untouched by it.
+
+    fp32: the bound of test_a_few_long_requests_among_many with what the join adds to a weight, a difference of maxima (at
+    most 2 A), its product with log2 e (rounded itself) and an approximate 2^x: 6 A half steps and 2^-22 more."""
+    prefix, mine, new, heads, group, page = shape
+    c = build_branches(prefix, mine, page, heads, dtype, seed=73)
+    q = queries(sum(new), heads * group, dtype, 73)
+    slot, kv_len, table, cu = c["slot"].tolist(), c["kv_len"].tolist(), c["table"].tolist(), cu_of(new).tolist()
+    hit = sorted({0, 1, len(new) - 1})
+    clean_q, clean_k = q.clone(), c["pool"][:, 0].clone()
+    for b in hit:
+        if where == "q":
+            q[cu[b + 1] - 1, (3 * b) % (heads * group), 7] = value
+        else:
+            j = kv_len[slot[b]] - 1 - new[b] // 2  # seen by the later ones of its tokens
+            c["pool"][table[slot[b]][j // page], 0, b % heads, j % page, 7] = value
+    o = torch.full_like(q, 7.0)
+    call(kda, q, c, new, o=o)
+    assert kda.kda_get_device_status()[0] == 0
+    with np.errstate(invalid="ignore"):
+        ref, a = prefix64(q, c, new)
+    o64, lost = to64(o), np.isnan(ref).any(-1)
+    assert lost.any() and not lost.all()
+    assert np.isnan(ref[lost]).all() and np.isnan(o64[lost]).all()
+    o64, ref, a = o64[~lost], ref[~lost], a[~lost]
+    if dtype == BF16:
+        bound = 2.0 ** -8 * (a + np.abs(ref)) + 2.0 ** -12 * a
+    else:
+        size = torch.einsum("thgd,hkd->thgk", clean_q.double().abs().reshape(len(q), heads, group, 128),
+                            clean_k.double().abs().transpose(0, 1).reshape(heads, -1, 128)).amax(-1)
+        d = 137 * 2.0 ** -24 * 128 ** -0.5 * to64(size).reshape(len(q), heads * group, 1)[~lost] + 2.0 ** -21
+        bound = np.expm1(2 * d + 2 * max(kv_len) * 2.0 ** -24 + 2.0 ** -22) * a
+    assert (np.abs(o64 - ref) <= bound).all()
