@@ -424,6 +424,9 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_own_kernel(const __grid_co
             }
         }
         __syncwarp();
+        // The partial outputs (plain stores) lie where the next rows' tiles go (TMA): the barrier orders the two only for those
+        // who have said this.
+        fence_proxy_async_smem();
         cluster_sync();  // the partials have been read: no CTA goes on to further rows, or leaves, before
         if (failed) break;
         if (threadIdx.x == 0) sh.tainted = 0;

@@ -532,3 +532,26 @@ def test_scores_that_are_not_finite_give_nan(kda, shape, where, value, dtype):
         d = 137 * 2.0 ** -24 * 128 ** -0.5 * to64(size).reshape(len(q), heads * group, 1)[~lost] + 2.0 ** -21
         bound = np.expm1(2 * d + 2 * max(kv_len) * 2.0 ** -24 + 2.0 ** -22) * a
     assert (np.abs(o64 - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("mine,new,heads,group,page", [
+    ([1100, 300, 9, 40], [100, 1, 1, 1], 1, 4, 32),                       # two turns of 32 rows, clusters of four
+    ([1500, 20, 3, 1, 70, 5, 9, 600], [200] + [1] * 7, 2, 4, 64),         # four turns, a CTA each
+    ([900] + [30] * 9, [100] + [1] * 9, 2, 1, 16),                        # four turns of 16 rows
+    ([2000, 2000], [300, 1], 1, 3, 128),                                  # clusters of eight
+])
+def test_a_request_of_many_turns(kda, mine, new, heads, group, page):
+    """Few requests, of which one brings far more rows than the others: its CTAs go over its own keys once a block of rows,
+    each turn's tiles where the last turn's partial outputs were."""
+    c = build_branches([150], [mine], page, heads, BF16, seed=79)
+    q, cu = queries(sum(new), heads * group, BF16, 79), cu_of(new)
+    o = call(kda, q, c, new)
+    assert kda.kda_get_device_status()[0] == 0
+    check(o, q, c, new)
+    busy = torch.randn((2048, 2048), device="cuda")
+    for i in range(30):
+        if i % 2:
+            torch.mm(busy, busy)
+        again = kda.kda_prefix_attention(q, c["pool"], c["table"], c["slot"], cu, c["kv_len"], c["cu_groups"],
+                                         c["prefix_len"], max_tokens=max(new))
+        assert torch.equal(again, o)
