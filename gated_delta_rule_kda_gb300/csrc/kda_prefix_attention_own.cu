@@ -49,6 +49,7 @@ struct Ring {
     uint64_t full[kStages], empty[kStages];
     int2 tile[kStages];       // first key; bit g: its keys 16 g .. have a page (and some row sees some)
     uint32_t abort;
+    uint32_t busy;  // warps in own_rows, which may take longer than a wait does
 };
 struct Shared {
     Ring ring;
@@ -57,7 +58,7 @@ struct Shared {
 };
 
 __device__ __forceinline__ bool wait(Ring &ring, uint64_t *bar, uint32_t parity, const Params &p, uint32_t what) {
-    return attn_wait_warp(bar, parity, &ring.abort, p.a, what);
+    return attn_wait_warp(bar, parity, &ring.abort, p.a, what, &ring.busy);
 }
 
 // The own keys of a chunk's rows: [from, last], tokens p0 .. last.
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_own_kernel(const __grid_co
             mbar_init(&sh.ring.full[i], 1);
             mbar_init(&sh.ring.empty[i], kWarps);
         }
-        sh.ring.abort = sh.tainted = 0;
+        sh.ring.abort = sh.ring.busy = sh.tainted = 0;
         fence_mbar_init();
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join comes up when the last CTA has
@@ -473,11 +474,13 @@ __device__ __forceinline__ int64_t place(const Params &p, const Item &it, int32_
     return (int64_t)(it.first + token) * p.a.num_q_heads + h * p.G + (row - token * p.G);
 }
 
-// Rows r0, r0 + step .. below r1 of an item, in kv head h, by own_row.
-__device__ __forceinline__ void own_rows(const Params &p, const Item &it, int32_t h, const Own &own, int32_t r0, int32_t r1,
+// Rows r0, r0 + step .. below r1 of an item, in kv head h, by own_row (a row of 640,000 keys takes 0.6 s: the other warps'
+// waits do not run out meanwhile).
+__device__ __forceinline__ void own_rows(const Params &p, Ring &ring, const Item &it, int32_t h, const Own &own, int32_t r0, int32_t r1,
                                          int32_t step) {
     const int lane = threadIdx.x & 31;
     const PrefixSpace space = prefix_space(p.a);
+    if (lane == 0) atomicAdd(&ring.busy, 1u);
     for (int32_t r = r0; r < r1; r += step) {
         float4 acc;
         const int64_t at = place(p, it, h, r);
@@ -485,6 +488,7 @@ __device__ __forceinline__ void own_rows(const Params &p, const Item &it, int32_
         store4(space.own_o + at * kD + 4 * lane, acc);
         if (lane == 0) space.own[at] = make_float4(x.x, x.y, it.from > 0, 0.f);
     }
+    if (lane == 0) atomicSub(&ring.busy, 1u);
 }
 
 // Barrier 1 of the four consumer warps; whether any thread says x.
@@ -582,7 +586,7 @@ __device__ __forceinline__ bool two_blocks(const Params &p, ManyShared &sh, unsi
     }
     if (consumers_or(attn_given_up(&sh.ring.abort))) return false;
     if (consumers_or(w.bad != 0)) {
-        own_rows(p, it, it.h, own, warp, it.rows, kWarps);
+        own_rows(p, sh.ring, it, it.h, own, warp, it.rows, kWarps);
         return true;
     }
     float top[2], sum[2];
@@ -675,7 +679,7 @@ __device__ __forceinline__ bool one_block(const Params &p, ManyShared &sh, unsig
     }
     if (consumers_or(attn_given_up(&sh.ring.abort))) return false;  // (the rows have no result)
     if (consumers_or(w.bad != 0)) {
-        own_rows(p, it, it.h, own, warp, it.rows, kWarps);
+        own_rows(p, sh.ring, it, it.h, own, warp, it.rows, kWarps);
         return true;
     }
     // The warps' shares joined: warp w gets channels 32 w .. of every row from the other three, one after
@@ -762,7 +766,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) prefix_own_many_kernel(const 
         }
         mbar_init(&sh.q_full, 1);
         mbar_init(&sh.q_empty, kWarps);
-        sh.ring.abort = 0;
+        sh.ring.abort = sh.ring.busy = 0;
         fence_mbar_init();
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join comes up when the last CTA has
@@ -815,7 +819,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) prefix_own_many_kernel(const 
                 if (consumers_or(!got)) break;
                 if (!mine) continue;
                 if (__any_sync(kAll, w.bad != 0)) {
-                    own_rows(p, it, h, own, r0, r1, 1);
+                    own_rows(p, sh.ring, it, h, own, r0, r1, 1);
                     continue;
                 }
 #pragma unroll

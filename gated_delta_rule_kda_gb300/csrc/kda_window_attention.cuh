@@ -159,20 +159,22 @@ __device__ __forceinline__ void attn_give_up(uint32_t *abort, const Args &a, uin
 }
 // A whole warp waits for a phase, for attn_wait_ns() at most or until another has given up.  Every lane gets the
 // same answer: what follows are full-mask exchanges and warp-wide instructions, which lanes that went
-// different ways could never meet in again.
+// different ways could never meet in again.  `busy` (may be null): a word of the CTA that is not 0 while one of its warps
+// computes something that may take longer than that, but ends; meanwhile the time does not count.
 template <typename Args>
 __device__ __forceinline__ bool attn_wait_warp(uint64_t *bar, uint32_t parity, uint32_t *abort,
-                                               const Args &a, uint32_t what) {
+                                               const Args &a, uint32_t what, const uint32_t *busy = nullptr) {
     constexpr uint32_t kAll = 0xffffffffu;
     bool done = tc::mbar_try_wait(bar, parity);
     if (__all_sync(kAll, done)) return true;
-    const uint64_t t0 = tc::global_timer_ns();
+    uint64_t t0 = tc::global_timer_ns();
     while (true) {
         for (int i = 0; i < 4; ++i) {
             done = done || tc::mbar_try_wait(bar, parity);
             if (__all_sync(kAll, done)) return true;
         }
         if (__any_sync(kAll, attn_given_up(abort))) return false;
+        if (busy != nullptr && *reinterpret_cast<const volatile uint32_t *>(busy) != 0) t0 = tc::global_timer_ns();
         if (__any_sync(kAll, tc::global_timer_ns() - t0 > attn_wait_ns(a))) {
             if ((threadIdx.x & 31) == 0) attn_give_up(abort, a, what);
             return false;

@@ -803,6 +803,11 @@ size_t kda_prefix_attention_workspace_size(kda_dtype dtype, int32_t batch, int32
  * tokens, the verify of a draft): requests that bring hundreds fill the tiles
  * alone, and kda_window_attention is then the faster call.
  * The same call gives the same bits again.
+ * An infinity or NaN among the values (bf16) of an own key that some tokens of
+ * a request's step see and others do not makes the call slow, not wrong: the
+ * rows next to it are computed one by one, each by a warp at 0.5 to 0.9 us an
+ * own key (two tokens of 16 heads behind 20,000 own keys: 90 ms).  A value that
+ * all tokens of a request see, or none, costs nothing.
  * Errors: KDA_ERR_INVALID_ARGUMENT (null/misaligned pointers, sizes below 1,
  * T < 0, Hq not a multiple of Hkv, dtype), KDA_ERR_WORKSPACE,
  * KDA_ERR_UNSUPPORTED (as kda_window_attention, and M page_size above

@@ -555,3 +555,27 @@ def test_a_request_of_many_turns(kda, mine, new, heads, group, page):
         again = kda.kda_prefix_attention(q, c["pool"], c["table"], c["slot"], cu, c["kv_len"], c["cu_groups"],
                                          c["prefix_len"], max_tokens=max(new))
         assert torch.equal(again, o)
+
+
+def test_rows_that_take_longer_than_a_wait(kda):
+    """A value that the last token alone sees is not finite, in a request of so many own keys that its rows, computed one by
+    one, take longer than the kernels wait for anything (2 s).  The CTA has further requests to go on with: its warps that
+    wait meanwhile do not give up.  (The first token's row: fp32 sums of 380,000 terms, one after the other, off by at most
+    2^-24 of the sum of the sizes each, above and below.)"""
+    B, heads, page, keys, late = 3000, 16, 128, 380000, 7
+    new = [2] * B
+    c = build_branches([64], [[5] * late + [keys] + [5] * (B - late - 1)], page, 1, BF16, seed=83)
+    q = queries(2 * B, heads, BF16, 83)
+    want = call(kda, q, c, new)
+    row, j = c["slot"][late].item(), 64 + keys - 1
+    c["pool"][c["table"][row, j // page].item(), 1, 0, j % page, 5] = float("inf")
+    o = call(kda, q, c, new)
+    assert kda.kda_get_device_status() == (0, 0)
+    first = 2 * late
+    assert torch.equal(o[:first], want[:first]) and torch.equal(o[first + 2:], want[first + 2:])
+    assert bool((o[first + 1, :, 5] == float("inf")).all())
+    at = torch.arange(j, device="cuda")
+    kv = c["pool"][c["table"][row].long()[at // page], :, 0, at % page].double()
+    p = torch.softmax(q[first].double() @ kv[:, 0].T * 128 ** -0.5, -1)
+    ref, a = p @ kv[:, 1], p @ kv[:, 1].abs()
+    assert ((o[first].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (2 * keys * 2.0 ** -24 + 2.0 ** -12) * a).all()
