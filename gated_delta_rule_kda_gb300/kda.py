@@ -934,7 +934,7 @@ def kda_beam_select(logits, scores, choices=None, *, ended=None, end_token=-1, p
     if not 1 <= N <= MAX_BEAMS:  # (no outputs of that size are made for the call to refuse)
         raise KdaError("kda_beam_select", 1 if N < 1 else 2)
     sb, sk, sv = logits.stride()
-    if (sv != 1 and V > 1) or (B > 1 and sb != K * sk):
+    if (sv != 1 and V > 1) or (B > 1 and K > 1 and sb != K * sk):
         raise ValueError("the rows of logits must be dense and evenly spaced")
     stride = sk if K > 1 else sb if B > 1 else V
     shape = torch.Size((B, N))

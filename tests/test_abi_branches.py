@@ -274,3 +274,23 @@ def test_what_a_call_allocates_belongs_to_its_stream(kda, name, monkeypatch):
 
 def test_normal_library_refuses_the_injection(kda):
     assert kda.library().kda_debug_inject_prefix_timeout() == 2
+
+
+@pytest.mark.parametrize("logits,stride", [
+    (torch.zeros((6, 40))[:, :33].unsqueeze(1), 40),            # one beam a prompt, out of a padded output
+    (torch.zeros((6, 4, 33))[:, :1], 4 * 33),                   # the first of several beams
+    (torch.zeros((6, 4, 40))[:, 2:3, :33], 4 * 40),
+    (torch.zeros((4, 6, 33)).transpose(0, 1)[:, 1:2], 33),
+    (torch.zeros((6, 4, 40))[..., :33], 40),
+    (torch.zeros((1, 4, 40))[..., :33], 40),
+    (torch.zeros((1, 1, 40))[..., :33], None),                  # one row: any stride does
+    (torch.zeros((6, 40))[:, :1].unsqueeze(1), 40)])
+def test_binding_takes_rows_that_are_evenly_spaced(kda, logits, stride, monkeypatch):
+    """The stride of a dimension of size 1 says nothing about where rows lie."""
+    lib = _NoLaunch()
+    monkeypatch.setattr(kda, "_lib", lib)
+    monkeypatch.setattr(kda, "_launch", lambda stream, dev: None)
+    B, K, V = logits.shape
+    kda.kda_beam_select(logits, torch.zeros((B, K)), 2, workspace=torch.zeros(1 << 20, dtype=torch.uint8))
+    (entry, a), = lib.calls
+    assert entry == "kda_beam_select" and a[1:4] == (B, K, V) and a[6] >= V and stride in (None, a[6])

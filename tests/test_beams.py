@@ -328,3 +328,12 @@ def test_reorder_at_the_limits_of_the_table(kda, pages, rows):
     pool = torch.randint(-99, 99, (1, pages, 4), dtype=torch.int32, device="cuda")
     reorder(kda, rng.randint(0, 4, (2, 4)), slot, table, kv_len, pool, pages, 16)
     assert kda.kda_get_device_status()[0] == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_one_beam_of_rows_of_any_stride(kda, dtype):
+    """One beam a prompt out of a padded output, and one of several beams: dense rows, evenly spaced."""
+    logits, scores = make(5, 3, 4001, dtype, seed=23, pad=6)
+    check(kda, logits[:, 0].unsqueeze(1), scores[:, :1].contiguous(), 7)
+    check(kda, logits[:, 1:2], scores[:, 1:2].contiguous(), 7)
+    check(kda, logits.transpose(0, 1)[2].unsqueeze(1), scores[:, 2:].contiguous(), 7)
