@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, kCtasSm) beam_segments_kernel(const 
                 if (r == N - 1) s_bound = g;
             }
             __syncthreads();
-            bound = s_bound;
+            bound = fminf(s_bound, kMost);  // (+inf counts as the largest number, which may come before it)
         }
         // What can be chosen: logits at or above the bound in the first chunk, above it later (N logits reach the
         // bound already, and go before equal ones).

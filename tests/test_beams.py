@@ -337,3 +337,23 @@ def test_one_beam_of_rows_of_any_stride(kda, dtype):
     check(kda, logits[:, 0].unsqueeze(1), scores[:, :1].contiguous(), 7)
     check(kda, logits[:, 1:2], scores[:, 1:2].contiguous(), 7)
     check(kda, logits.transpose(0, 1)[2].unsqueeze(1), scores[:, 2:].contiguous(), 7)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("V", [130, 5000, 70000])
+def test_infinities_tie_with_the_largest_number(kda, V, dtype):
+    """A logit of +inf counts as the largest fp32 number: among those and fp32 logits that are it the lower token goes first,
+    whichever of the two it is and wherever in the row they lie."""
+    most = torch.finfo(dtype).max
+    logits, scores = make(8, 2, V, dtype, seed=V)
+    logits = logits.clone()
+    logits[0, :, 3], logits[0, :, 100] = most, INF
+    logits[1, :, 100], logits[1, :, 3] = most, INF
+    logits[2, :, V // 2], logits[2, :, V - 1] = most, INF            # in other chunks, other segments
+    logits[3, :, V // 2], logits[3, :, V - 1] = INF, most
+    logits[4, :, 1::2], logits[4, :, 0] = INF, most                  # more than can be ranked by counting
+    logits[5], logits[5, 0, : V // 3] = most, INF
+    logits[6, 0, ::7], logits[6, 1, V // 4:] = most, INF
+    logits[7, :, 90:], logits[7, :, 64:90] = INF, most
+    for N in (1, 2, 5, 40):
+        check(kda, logits, scores, N)
