@@ -357,3 +357,46 @@ def test_infinities_tie_with_the_largest_number(kda, V, dtype):
     logits[7, :, 90:], logits[7, :, 64:90] = INF, most
     for N in (1, 2, 5, 40):
         check(kda, logits, scores, N)
+
+
+def crowded(left, seed=19):
+    """Two prompts of four beams in two pages each, the last one part-filled; two further rows name every page but `left`
+    that no row has, so that the beams that leave free none."""
+    rng = np.random.RandomState(seed)
+    R, M, page, pages = 11, 12, 16, 16 + left
+    names, slot = rng.permutation(pages), rng.permutation(R)[:8].reshape(2, 4).astype(np.int32)
+    table, kv_len = np.full((R, M), -1, np.int32), np.zeros(R, np.int32)
+    for i, r in enumerate(slot.reshape(-1)):
+        table[r, :2], kv_len[r] = names[2 * i: 2 * i + 2], 17 + i
+    keep = [r for r in range(R) if r not in slot]
+    table[keep[0], :8], table[keep[2], :8] = names[:8], names[8:16]
+    kv_len[keep[0]] = kv_len[keep[2]] = 128
+    pool = torch.randint(-2 ** 31, 2 ** 31 - 1, (2, pages, 64), dtype=torch.int32, device="cuda" if torch.cuda.is_available() else "cpu")
+    return table, kv_len, slot, pool, pages, page
+
+
+# parents: all of the first beam; some of none (they need no page)
+CROWDED = [([[0, 0, 0, 0], [0, 0, 0, 0]], [1, 2, 3, 5, 6, 7]), ([[2, 2, 1, 1], [3, -1, 3, 3]], [1, 3, 6, 7]),
+           ([[-1, 4, 0, 0], [1, 1, 2, 0]], [3, 5])]
+
+
+@pytest.mark.parametrize("left", [0, 1, 2, 5])
+@pytest.mark.parametrize("parent,branches", CROWDED)
+def test_reorder_where_pages_run_out(kda, parent, branches, left):
+    """The branches get the pages that are left, in order; the others' rows are left empty, and said."""
+    table, kv_len, slot, pool, pages, page = crowded(left)
+    parent = np.array(parent)
+    want = beam_reorder64(parent, slot, table, kv_len, pages, page)
+    dst = want[2].tolist()
+    for n, i in enumerate(branches):  # (what the plain implementation says, spelled out)
+        row = want[4][dst[i]].tolist()
+        if n < left:
+            assert want[5][dst[i]] == kv_len[want[1][i]] and row[1] >= 0 and row[2:] == [-1] * 10
+        else:
+            assert want[5][dst[i]] == 0 and row == [-1] * 12
+    assert len(want[6]) == min(left, len(branches))
+    kda.kda_get_device_status()
+    reorder(kda, parent, slot, table, kv_len, pool, pages, page)
+    lost = branches[left:]
+    status, detail = kda.kda_get_device_status()
+    assert (status == 6 and detail in lost) if lost else status == 0
