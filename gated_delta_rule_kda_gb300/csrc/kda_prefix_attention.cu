@@ -229,11 +229,11 @@ size_t space_bytes(const PrefixAttentionArgs &a, const PrefixCut &cut) {
 
 }  // namespace
 
-PrefixCut prefix_cut_rows(const PrefixAttentionArgs &a) {
-    return PrefixCut{1, a.num_q_heads / a.num_kv_heads, kRows, kTile, kPrefixCtas, kRows, 1, 8.f};
+PrefixCut prefix_cut_rows(const PrefixAttentionArgs &a, int32_t sms) {
+    return PrefixCut{1, a.num_q_heads / a.num_kv_heads, kRows, kTile, 2 * sms, kRows, 1, 8.f};
 }
 
-// (bf16: of either kind of kernels, as the scale decides)
+// (bf16: of either kind of kernels, as the scale decides; whatever GPU the call runs on)
 size_t prefix_attention_workspace(kda_dtype dtype, int32_t batch, int32_t total_tokens, int32_t num_groups,
                                   int32_t num_q_heads, int32_t num_kv_heads) {
     PrefixAttentionArgs a{};
@@ -242,7 +242,7 @@ size_t prefix_attention_workspace(kda_dtype dtype, int32_t batch, int32_t total_
     a.num_groups = num_groups;
     a.cache.batch = batch;
     a.cache.total_tokens = total_tokens;
-    const size_t rows = space_bytes(a, prefix_cut_rows(a)), tc = space_bytes(a, prefix_cut_tc(a));
+    const size_t rows = space_bytes(a, prefix_cut_rows(a, kPrefixSms)), tc = space_bytes(a, prefix_cut_tc(a, kPrefixSms));
     return dtype == KDA_BF16 && tc > rows ? tc : rows;
 }
 
@@ -251,13 +251,14 @@ cudaError_t launch_prefix_attention(const PrefixAttentionArgs &a, cudaStream_t s
     // The tensor-core kernels keep their running maximum on unscaled scores, in the order that a positive scale
     // leaves alone; any other scale (and fp32) runs on the FMA units.
     constexpr double kLog2e = 1.4426950408889634;
+    const int32_t sms = device_sm_count() < kPrefixSms ? device_sm_count() : kPrefixSms;
     if (a.dtype == KDA_BF16 && a.scale > 0.f && a.scale <= FLT_MAX) {
-        const PrefixCut cut = prefix_cut_tc(a);
+        const PrefixCut cut = prefix_cut_tc(a, sms);
         cudaError_t e = launch_prefix_tc(a, cut, stream);
         if (e == cudaSuccess) e = launch_prefix_own(a, cut, stream);
         return e == cudaSuccess ? launch_join<__nv_bfloat16>(a, cut, (float)((double)a.scale * kLog2e), stream) : e;
     }
-    const PrefixCut cut = prefix_cut_rows(a);
+    const PrefixCut cut = prefix_cut_rows(a, sms);
     if (a.dtype == KDA_BF16) {
         const cudaError_t e = launch_rows<__nv_bfloat16>(a, cut, stream);
         return e == cudaSuccess ? launch_join<__nv_bfloat16>(a, cut, (float)kLog2e, stream) : e;

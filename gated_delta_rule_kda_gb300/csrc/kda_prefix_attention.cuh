@@ -93,7 +93,8 @@ __device__ __forceinline__ PrefixRequest prefix_request(const PrefixAttentionArg
 // [T][Hq] the parts of prefixes (o [rows][128], (m, l) [rows]) and of own keys (o, (m, l, whether there is a
 // prefix) with l < 0 where there is no result), for each token and kv head the CTAs that have parts of its rows'
 // prefix, and the CTAs' slots (o, (m, l)).
-constexpr int32_t kPrefixCtas = 2 * 152;  // most of them
+constexpr int32_t kPrefixSms = 152;              // SMs that it is laid out for: the GPU's, but no more than these
+constexpr int32_t kPrefixCtas = 2 * kPrefixSms;  // most CTAs of the first launch
 struct PrefixSpace {
     uint32_t *done, *taken;  // taken: items of the second launch that a CTA has
     float *o, *own_o;
@@ -244,7 +245,8 @@ __device__ void prefix_make_plan(const PrefixAttentionArgs &a, const PrefixCut &
             // And where a CTA would have less than four units, fewer do, down to a third: the others are free for the own
             // keys at once, and there are fewer parts to join (those 10 beams: 26 us instead of 33; six prompts of one
             // request 23 instead of 29).
-            run.teams = teams = (int32_t)min((int64_t)teams, max(all / 4, min(all, (int64_t)(cut.ctas / 3))));
+            teams = (int32_t)min((int64_t)teams, max(all / 4, min(all, (int64_t)(cut.ctas / 3))));
+            run.teams = teams = max(teams, (int32_t)min(all, (int64_t)1));  // (a GPU of few SMs)
             run.all = all;
             run.width = cut.width;
             run.bad = falls;
@@ -331,8 +333,10 @@ struct PrefixWalk {
     }
 };
 
-PrefixCut prefix_cut_rows(const PrefixAttentionArgs &a);
-PrefixCut prefix_cut_tc(const PrefixAttentionArgs &a);
+// For a GPU of `sms` SMs (at most kPrefixSms): with fewer CTAs than these the first launch would leave some idle, with more its
+// last ones would begin when the others are done, and with them all of the second launch.
+PrefixCut prefix_cut_rows(const PrefixAttentionArgs &a, int32_t sms);
+PrefixCut prefix_cut_tc(const PrefixAttentionArgs &a, int32_t sms);
 cudaError_t launch_prefix_tc(const PrefixAttentionArgs &a, const PrefixCut &cut, cudaStream_t stream);
 cudaError_t launch_prefix_own(const PrefixAttentionArgs &a, const PrefixCut &cut, cudaStream_t stream);
 

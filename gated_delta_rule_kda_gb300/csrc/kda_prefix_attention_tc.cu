@@ -33,7 +33,6 @@ namespace {
 using namespace tc;
 using namespace attn_tc;
 
-constexpr int kCtas = 152;        // one an SM
 constexpr int kItems = 4;         // work items announced ahead
 constexpr int kItemReaders = 11;  // warps that read them: softmax, MMA, clearing
 constexpr int kTiles = 8;         // key tiles whose masks are kept
@@ -644,14 +643,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(const __grid_con
 // into L2, items that go through them at different times fetch them from HBM again each, at 64 KB a CTA for
 // the 1.1 us that a tile of 256 rows takes: 9.2 TB/s in all, 1.37 times what HBM gives.  Teams of two or more bring
 // that below it, but leave CTAs over, and work for nothing where an item is missing in a team.
-static int32_t team_width(const PrefixAttentionArgs &a, int32_t tokens) {
+static int32_t team_width(const PrefixAttentionArgs &a, int32_t tokens, int32_t ctas) {
     const int64_t T = a.cache.total_tokens, items = ((T + a.num_groups - 1) / a.num_groups + tokens - 1) / tokens;
     const int64_t keys = (int64_t)a.cache.table_width * a.cache.page_size * a.num_groups;
     if (items == 1 || keys * a.num_kv_heads * (4 * kD) < (96ll << 20)) return 1;
     int32_t best = 1;
     double most = 1 / 1.37;
     for (int32_t w = 2; w <= 8; ++w) {
-        const double share = (double)items / (double)((items + w - 1) / w * w) * (kCtas / w * w) / kCtas;
+        const double share = (double)items / (double)((items + w - 1) / w * w) * (ctas / w * w) / ctas;
         if (share >= most) {
             most = share;
             best = w;
@@ -660,9 +659,9 @@ static int32_t team_width(const PrefixAttentionArgs &a, int32_t tokens) {
     return best;
 }
 
-PrefixCut prefix_cut_tc(const PrefixAttentionArgs &a) {
+PrefixCut prefix_cut_tc(const PrefixAttentionArgs &a, int32_t sms) {
     const int32_t G = a.num_q_heads / a.num_kv_heads, tq = kTile / G;
-    return PrefixCut{0, G, 2 * tq, kTile, kCtas, 2 * kTile, a.num_groups > 0 ? team_width(a, 2 * tq) : 1, 1.6f};
+    return PrefixCut{0, G, 2 * tq, kTile, sms, 2 * kTile, a.num_groups > 0 ? team_width(a, 2 * tq, sms) : 1, 1.6f};
 }
 
 cudaError_t launch_prefix_tc(const PrefixAttentionArgs &a, const PrefixCut &cut, cudaStream_t stream) {

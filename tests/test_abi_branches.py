@@ -1,5 +1,7 @@
 """Refusals of the operators that decode branches (no GPU needed): bad arguments are turned down on the host
 before any launch (nothing is dereferenced in these calls)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -294,3 +296,36 @@ def test_binding_takes_rows_that_are_evenly_spaced(kda, logits, stride, monkeypa
     kda.kda_beam_select(logits, torch.zeros((B, K)), 2, workspace=torch.zeros(1 << 20, dtype=torch.uint8))
     (entry, a), = lib.calls
     assert entry == "kda_beam_select" and a[1:4] == (B, K, V) and a[6] >= V and stride in (None, a[6])
+
+
+class _Cut(ctypes.Structure):
+    """PrefixCut of csrc/kda_prefix_attention.cuh."""
+    _fields_ = [(x, ctypes.c_int32) for x in ("by_rows", "G", "tile", "keys", "ctas", "slot_rows", "width")] + [("tile_us", ctypes.c_float)]
+
+
+class _Cache(ctypes.Structure):
+    """CacheArgs of csrc/kda_common.cuh."""
+    _fields_ = ([(x, ctypes.c_int32) for x in ("batch", "total_tokens", "num_pages", "page_size", "table_rows", "table_width")]
+                + [(x, ctypes.c_void_p) for x in ("page_table", "slot", "cu_tokens", "kv_len")])
+
+
+class _Prefix(ctypes.Structure):
+    """PrefixAttentionArgs of csrc/kda_common.cuh."""
+    _fields_ = ([(x, ctypes.c_int32) for x in ("dtype", "max_tokens", "num_q_heads", "num_kv_heads", "num_groups")]
+                + [(x, ctypes.c_void_p) for x in ("q", "kv_pool", "cu_groups", "prefix_len")]
+                + [("scale", ctypes.c_float), ("o", ctypes.c_void_p), ("cache", _Cache), ("workspace", ctypes.c_void_p),
+                   ("status", ctypes.c_void_p)])
+
+
+@pytest.mark.parametrize("name,each", [("prefix_cut_tc", 1), ("prefix_cut_rows", 2)])
+@pytest.mark.parametrize("sms", [8, 16, 100, 148, 152])
+def test_prefix_launch_fits_the_gpu(kda, name, each, sms):
+    """Over the prefixes there are no more CTAs than a GPU of so many SMs holds at once (the launch over the own keys only
+    begins when all of them have), and a team of them is no larger than that."""
+    cut = getattr(kda.library(), f"_ZN3kda{len(name)}{name}ERKNS_19PrefixAttentionArgsEi")
+    cut.restype = _Cut
+    for groups, tokens, width in ((1, 4, 3), (1, 4000, 4096), (3, 100000, 1 << 20)):
+        a = _Prefix(num_q_heads=96, num_kv_heads=8, num_groups=groups,
+                    cache=_Cache(batch=tokens, total_tokens=tokens, num_pages=1 << 20, page_size=64, table_rows=tokens, table_width=width))
+        x = cut(ctypes.byref(a), sms)
+        assert x.G == 12 and x.ctas == each * sms and 1 <= x.width <= x.ctas
