@@ -295,8 +295,8 @@ __device__ void mma_thread(const Params &p, Shared &sh, unsigned char *sm, int r
         if (!(ok = wait_one(sh, B_QFULL, items & 1, p))) break;
         ++items;
         if (!it.two(p)) {
-            // Every other tile.  What it uses is freed for both (two arrivals); the others are only waited for: a wait
-            // tells two neighbouring phases of a barrier apart, so none may be passed over.
+            // Every other tile.  The others are waited for and given back at once: a wait tells two neighbouring phases of a
+            // barrier apart, so a place is not filled again before both engines have seen that it was.
             for (int32_t i = 0; i < n; ++i) {
                 const int k = ring.stage;
                 ring.next();
@@ -304,7 +304,10 @@ __device__ void mma_thread(const Params &p, Shared &sh, unsigned char *sm, int r
                 ring.next();
                 const bool tail = it.tail(i);
                 if ((i & 1) != r) {
-                    if (!(ok = full(k) && (tail ? clean(v) : full(v)))) break;
+                    if (!(ok = full(k))) break;
+                    mbar_arrive(sh.bar + B_KVEMPTY + k);
+                    if (!(ok = tail ? clean(v) : full(v))) break;
+                    mbar_arrive(sh.bar + B_KVEMPTY + v);
                     continue;
                 }
                 if (!(ok = full(k))) break;
@@ -312,12 +315,10 @@ __device__ void mma_thread(const Params &p, Shared &sh, unsigned char *sm, int r
                 mma_scores(tmem, q0_desc, k_desc + k * kTileStep, r, 0, kD / 16);
                 mma_commit(sh.bar + B_S + r);
                 mma_commit(sh.bar + B_KVEMPTY + k);
-                mma_commit(sh.bar + B_KVEMPTY + k);
                 if (i + 2 >= n) mma_commit(sh.bar + B_QEMPTY);
                 if (!(ok = tail ? clean(v) : full(v))) break;
                 fence_after_sync();
                 if (!(ok = values(v, i == r))) break;
-                mma_commit(sh.bar + B_KVEMPTY + v);
                 mma_commit(sh.bar + B_KVEMPTY + v);
                 if (i + 2 >= n) mma_commit(sh.bar + B_O + r);
             }

@@ -579,3 +579,28 @@ def test_rows_that_take_longer_than_a_wait(kda):
     p = torch.softmax(q[first].double() @ kv[:, 0].T * 128 ** -0.5, -1)
     ref, a = p @ kv[:, 1], p @ kv[:, 1].abs()
     assert ((o[first].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (2 * keys * 2.0 ** -24 + 2.0 ** -12) * a).all()
+
+
+def test_called_over_and_over(kda):
+    """Thirty thousand calls over prefixes of all lengths, single row tiles of few rows: whatever the CTA's warps run into,
+    none is left behind by the others (a wait that runs out takes 2 s, and is reported)."""
+    rng = np.random.RandomState(89)
+    prefix = [int(n) for n in rng.randint(500, 8192, 16)]
+    mine = [[int(n) for n in rng.randint(1, 300, 4)] for _ in prefix]
+    new = [1] * 64
+    c = build_branches(prefix, mine, 64, 8, BF16, seed=89)
+    q, cu = queries(64, 96, BF16, 89), cu_of(new)
+    want = call(kda, q, c, new)
+    o, workspace = torch.empty_like(q), torch.empty(kda.kda_prefix_attention_workspace_size(BF16, 64, 64, 16, 96, 8),
+                                                    dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(100):
+            kda.kda_prefix_attention(q, c["pool"], c["table"], c["slot"], cu, c["kv_len"], c["cu_groups"], c["prefix_len"],
+                                     max_tokens=1, o=o, workspace=workspace)
+    for i in range(300):
+        graph.replay()
+        if i % 20 == 19:  # (the first lost call ends the test)
+            assert kda.kda_get_device_status() == (0, 0)
+            assert torch.equal(o, want)
+            o.fill_(7.0)
