@@ -6,9 +6,9 @@
 // logits in falling order; the second joins a prompt's K x S lists: log-sum-exp in 64 bits, then the
 // list with the best head gives one continuation after the other.
 //
-// A CTA holds its segment in registers.  Its candidates are found with a bound: threads are taken in
-// groups, as many as N or more, and the smallest of the groups' maxima has at least N logits at or
-// above it (g groups of random logits: about g ln g).  What reaches the bound is ranked by counting.
+// A CTA goes over its segment in chunks.  Candidates are found with a bound from the first one: threads are taken
+// in groups, more than N, and the N-th best of the groups' maxima has at least N logits at or above it, and few
+// more.  What reaches the bound, in any chunk, is kept and ranked by counting.
 // Where too much does, the logits are gone through once more with the bound of all of them, and where that
 // leaves too much as well (few distinct values, a mask of the lowest value, a short segment) the CTA takes its
 // best logits one by one.
@@ -109,10 +109,11 @@ __device__ __noinline__ uint4 edge_vector(const T *src, int32_t e0, int32_t coun
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A CTA goes over its segment in chunks of kVecs 16-byte vectors a thread, the next one's loads in flight while one
-// is worked on, and no barrier but those of the bound after the first.  What is rare is kept out of the loop's
-// code, rolled, and reads from shared memory: unrolled beside it, the instructions did not come fast enough (68 us
-// where these take 31, 512 rows of 131,072 bf16 logits: 4.3 TB/s).
+// A CTA goes over its segment in chunks of kVecs 16-byte vectors a thread, each loaded when the last one is done with
+// (other CTAs of the SM have loads in flight meanwhile: with a second buffer there were four of them instead of six, and
+// 64 x 8 rows of 131,072 took 45 us instead of 38), and no barrier but those of the bound after the first.  What is rare
+// is kept out of the loop's code, rolled, and reads from shared memory: unrolled beside it, the instructions did not
+// come fast enough (68 us where these take 31, 512 rows of 131,072 bf16 logits: 4.3 TB/s).
 template <typename T, int kVecs>
 __global__ void __launch_bounds__(kThreads, kCtasSm) beam_segments_kernel(const BeamSelectArgs a, const Layout lay) {
     using V = Vec<T>;

@@ -439,9 +439,10 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_own_kernel(const __grid_co
 // ---------------------------------------------------------------------------
 // Many requests of a few rows a kv head each
 // ---------------------------------------------------------------------------
-// Here the CTAs (two an SM) stay and take work, kv heads of a request, as they get done, so that an item's beginning and end hide behind its neighbours' keys: a sixth warp takes the items,
-// looks their requests up and brings q, and the fetching warp goes on to the next item's keys while the
-// consumers end the last one's.  Which CTA computes an item makes no difference to it.  Own keys that fit in one tile
+// Here the CTAs (two an SM) stay and take work, kv heads of a request, as they get done, so that an item's beginning
+// and end hide behind its neighbours' keys: a sixth warp takes the items, looks their requests up and brings q, and
+// the fetching warp goes on to the next item's keys while the consumers end the last one's.  Which CTA computes an
+// item makes no difference to it.  Own keys that fit in one tile
 // go a warp a head (or row block), without a join.  256 requests of 1 to 2048 own keys (8 heads of 12 rows, 1.07 GB)
 // take 182 us alone, 6.1 TB/s: HBM, and a tail of some 25 us while the last items end.  2,520 requests of 14 own keys
 // in 4 heads: 69 us a call (a head at a time 123); there the time goes into items' beginnings and ends.
@@ -885,7 +886,8 @@ cudaError_t launch_prefix_own(const PrefixAttentionArgs &a, const PrefixCut &cut
     p.chunks = (int32_t)(need < share ? need : share);
     // Split a request's keys over a cluster as far as the CTAs fit on half of the SMs (two an SM; the other half may
     // have prefixes for long, and a cluster only starts whole) and keep two tiles each, as far as the table's width can
-    // tell.  Six prompts of one request: 30 us; 33 with clusters for all SMs; six prompts of 21 requests with
+    // tell (lengths are on the device: two requests of 16 own keys take 20.0 us in a table of 10 pages and 22.0 in one of
+    // 512 or 16,384; 6 x 21 requests of 200 the same 2 us more).  Six prompts of one request: 30 us; 33 with clusters for all SMs; six prompts of 21 requests with
     // up to 2,100 own keys the other way round, 41.7 against 40.8.
     const int64_t tiles = ((int64_t)a.cache.table_width * a.cache.page_size + kTile - 1) / kTile;
     const int64_t ctas = B * a.num_kv_heads * p.chunks;

@@ -879,7 +879,7 @@ def kda_prefix_attention(q, kv_pool, page_table, slot, cu_tokens, kv_len, cu_gro
     """Causal attention of q [T, Hq, 128] over the requests' rows of the cache, where the rows of group g's requests
     [cu_groups[g], cu_groups[g+1]) share their first prefix_len[g] tokens: those are read once for the group, through
     its first request's row.  cu_groups [Ng+1] and prefix_len [Ng] int32 on the device; the other arguments as
-    kda_window_attention's.  Returns o."""
+    kda_window_attention's, which is the faster call where little is shared (include/kda.h).  Returns o."""
     shape, dtype, dev = q.shape, q.dtype, q.get_device()
     T, Hq, d = shape
     P, Hkv, page = _pool_shape(kv_pool)

@@ -800,8 +800,14 @@ size_t kda_prefix_attention_workspace_size(kda_dtype dtype, int32_t batch, int32
  *               not shared by calls that overlap on the GPU
  *   (cache arguments as above)
  * Any number of tokens a request is right; the call is built for a few (single
- * tokens, the verify of a draft): requests that bring hundreds fill the tiles
- * alone, and kda_window_attention is then the faster call.
+ * tokens, the verify of a draft) that share much.  On rows that hold the same
+ * tokens kda_window_attention with window = INT32_MAX is the faster call, in bf16,
+ * where requests bring many tokens (64 of 8 requests behind 2,000: 77 us against
+ * 110) and where little is shared: this one takes some 20 us at least (three
+ * launches), that one 7 to 10 (one).  They meet, as a rule, where the shared
+ * tokens, counted once for each request of the step, come to some 100,000 (30,000
+ * for four beams, 2,000 for 32; measured 16,000 to 300,000).  fp32: this one from
+ * some 100 shared tokens on.
  * The same call gives the same bits again.
  * An infinity or NaN among the values (bf16) of an own key that some tokens of
  * a request's step see and others do not makes the call slow, not wrong: the
@@ -817,8 +823,8 @@ size_t kda_prefix_attention_workspace_size(kda_dtype dtype, int32_t batch, int32
  * kv_len[row] - n_b or whose group's first slot is out of range, is refused by
  * the kernel (its rows of o stay as they are; KDA_ERR_DEVICE_CHECK with
  * detail = b).  Where cu_groups falls from one entry to the next, no row of o
- * is written (detail: the group); after a KDA_ERR_DEVICE_TIMEOUT the rows that
- * were not computed stay as they are.
+ * is written (detail: the group, or a request that is refused for it).  After a
+ * KDA_ERR_DEVICE_TIMEOUT the rows that were not computed stay as they are.
  */
 kda_status kda_prefix_attention(kda_dtype dtype, int32_t batch, int32_t total_tokens,
                                 int32_t max_tokens, int32_t num_q_heads, int32_t num_kv_heads,
